@@ -156,9 +156,10 @@ def _quantise(x, fmt):
     amax = x.abs().amax(-1, keepdim=True)
     good = torch.isfinite(amax)
     amax = torch.where(good, amax, torch.ones_like(amax)).clamp_min(_AMAX_FLOOR)
-    y = torch.where(good, x * (top / amax), torch.zeros_like(x)).clamp(-top, top)
+    q = torch.full_like(amax, top)      # a tensor: dividing by or into a plain number may go through its reciprocal
+    y = torch.where(good, x * (q / amax), torch.zeros_like(x)).clamp(-top, top)
     codes = y.to(dt) if fmt == "e4m3" else torch.round(y).to(dt)
-    scale = torch.where(good, amax / top, torch.full_like(amax, float("nan")))
+    scale = torch.where(good, amax / q, torch.full_like(amax, float("nan")))
     return codes, scale.squeeze(-1)
 
 
