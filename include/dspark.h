@@ -81,7 +81,8 @@ typedef enum dspark_status {
 
 typedef enum dspark_dtype {
     DSPARK_BF16 = 0,
-    DSPARK_F32 = 1
+    DSPARK_F32 = 1,
+    DSPARK_F16 = 2   /* the cache and attention calls only */
 } dspark_dtype;
 
 /* which workspace: argument of dspark_workspace_bytes */
@@ -99,7 +100,10 @@ enum {
     DSPARK_FLAG_BAD_VERIFY_LEN = 4u,   /* a verify length outside [0, G] */
     DSPARK_FLAG_BAD_POS_TEMP = 8u,     /* a calibration temperature <= 0 or NaN */
     DSPARK_FLAG_TIMEOUT = 16u,         /* a bounded device-side wait gave up */
-    DSPARK_FLAG_BAD_TARGET_ROW = 32u   /* a packed target row outside the array */
+    DSPARK_FLAG_BAD_TARGET_ROW = 32u,  /* a packed target row outside the array */
+    DSPARK_FLAG_BAD_PAGE = 64u,        /* a page number outside [0, n_pages) */
+    DSPARK_FLAG_BAD_LENGTH = 128u,     /* row starts, a start or a length outside their ranges */
+    DSPARK_FLAG_NONFINITE = 256u       /* an inf or NaN among the values to be cached */
 };
 
 /* Library version, major * 10000 + minor * 100 + patch. */
@@ -384,6 +388,122 @@ DSPARK_API dspark_status dspark_verify_noalloc(
  * between overlapping calls).  Returns DSPARK_OK, DSPARK_ERR_INVALID_ARG for a
  * NULL flags pointer, or DSPARK_ERR_CUDA. */
 DSPARK_API dspark_status dspark_read_noalloc_flags(void *stream, uint32_t *flags);
+
+/* ---------------------------------------------------------------------------
+ * The target's side of a round: a quantised key/value cache and the attention
+ * of the scheduled block rows over it.  The pages place them around the path
+ * above: the scheduler's lengths size the target's batch of sum_b (L_b + 1)
+ * rows ("DSpark, la bozza che sa quando fermarsi", section "Verificare meglio,
+ * non di piu'"), and the parallel drafter's blocks attend to the same past.
+ *
+ * Packed rows: request b's rows are row0[b] .. row0[b+1] - 1 (row0 [B+1]
+ * int64, device, non-decreasing, row0[0] >= 0, row0[B] <= n_rows), the layout
+ * whose first B entries dspark_verify_packed takes as target_row0.  Rows from
+ * row0[B] on belong to no request: they are neither read nor written.
+ *
+ * Pages: the cache holds n_pages pages of page_size tokens.  block_table
+ * [B][max_pages] int32 (device) gives the pages of each request, position t
+ * being token t % page_size of page block_table[b][t / page_size].
+ *
+ * Format: for each (token, head), D = head_dim codes of 8 bits and one fp32
+ * scale, for keys and values apart; code c stands for c * scale.
+ *   amax = max(max_d |x_d|, 2^-100),  scale = amax / Q,
+ *   code_d = round(x_d * (Q / amax)), to nearest even, in fp32,
+ * with Q = 448 (DSPARK_KV_E4M3: codes are e4m3 numbers) or 127
+ * (DSPARK_KV_INT8: two's complement whole numbers).  A row that holds an inf
+ * or a NaN is stored as code 0 with scale NaN, so that only rows that attend
+ * to the token read a NaN; the e4m3 codes 0x7F and 0xFF (NaN) are never
+ * written and must not be in the cache.
+ *
+ * Flags: unlike the calls with a workspace, these OR their bits into the
+ * cache's flag word and never clear it; the caller zeroes it and reads it with
+ * dspark_read_device_flags(cache->flags, ...).
+ */
+typedef enum dspark_kv_format {
+    DSPARK_KV_E4M3 = 0,
+    DSPARK_KV_INT8 = 1
+} dspark_kv_format;
+
+typedef struct dspark_kv_cache {
+    void *k, *v;              /* [n_pages][n_kv_heads][page_size][head_dim] codes, 16-byte aligned */
+    float *k_scale, *v_scale; /* [n_pages][n_kv_heads][page_size], 16-byte aligned */
+    uint32_t *flags;          /* [1] device flag word */
+    int32_t n_pages, n_kv_heads, page_size, head_dim;
+    int32_t format;           /* dspark_kv_format */
+} dspark_kv_cache;
+
+/* which rows of a request's own block a row sees (dspark_block_attention) */
+typedef enum dspark_block_mask {
+    DSPARK_MASK_CAUSAL = 0,   /* itself and the rows before it */
+    DSPARK_MASK_FULL = 1      /* every row of its block */
+} dspark_block_mask;
+
+/*
+ * Quantise new keys and values into the cache as they are written.
+ *
+ * Row i of request b goes to position start[b] + i of the request.
+ * k, v [n_rows][n_kv_heads][head_dim] dtype (bf16, fp16 or fp32), rows
+ * k_stride and v_stride elements apart (so a slice of a fused projection can
+ * be passed), 16-byte aligned rows.  start [B] int32 >= 0.  A row whose
+ * position lies beyond max_pages pages, or whose page is outside the cache, is
+ * flagged and not written.  Two rows must not name the same place.
+ * Limits: head_dim a multiple of 16 up to 128, page_size a multiple of 16.
+ */
+DSPARK_API dspark_status dspark_kv_append(
+    const dspark_kv_cache *cache, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+    dspark_dtype dtype, const int64_t *row0, int n_rows, const int32_t *start,
+    const int32_t *block_table, int max_pages, int B, void *stream);
+
+/*
+ * Read cached tokens back as rows: row i of request b is position
+ * start[b] + i, code * scale in fp32 rounded once to dtype (bf16, fp16 or
+ * fp32).  k_out, v_out [n_rows][n_kv_heads][head_dim], either may be NULL.
+ * A row whose position or page is out of range is flagged and filled with NaN.
+ */
+DSPARK_API dspark_status dspark_kv_read(
+    const dspark_kv_cache *cache, const int64_t *row0, int n_rows, const int32_t *start,
+    const int32_t *block_table, int max_pages, int B, dspark_dtype dtype, void *k_out, void *v_out,
+    void *stream);
+
+/* Bytes of workspace of dspark_block_attention for n_rows packed rows of
+ * n_q_heads heads.  Returns 0 for invalid sizes. */
+DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Attention of every request's block over a shared prefix and its own tokens.
+ *
+ * Request b has n_b = row0[b+1] - row0[b] rows (L_b + 1 when verifying, 1 in
+ * plain decoding) and kv_len[b] >= n_b cached tokens of its own, the last n_b
+ * of which are the block itself (append first).  Row i sees
+ *   all prefix_len tokens of prefix_pages [n_prefix_pages] (prefix_len may be
+ *     0; it need not fill its last page), shared by every request,
+ *   its own tokens t < kv_len[b] - n_b, and
+ *   token t of its block (t = 0 .. n_b - 1): t <= i (DSPARK_MASK_CAUSAL), every
+ *     one (DSPARK_MASK_FULL), or, when row_mask [n_rows] is given, those with
+ *     bit t of its word set (a drafted tree; n_b <= 64; `mask` is not used).
+ * With s_j = scale * ks_j * (q . k_j) over the seen tokens j,
+ *   out = sum_j softmax(s)_j vs_j v_j,   lse = ln sum_j e^{s_j},
+ * where query head g reads kv head g / (n_q_heads / n_kv_heads).  A row that
+ * sees no token has out = 0 and lse = -inf.
+ *
+ * q [n_rows][n_q_heads][head_dim] bf16 or fp16 with rows q_stride elements
+ * apart, 16-byte aligned rows; out [n_rows][n_q_heads][head_dim] of the same
+ * type, contiguous; lse [n_rows][n_q_heads] fp32 (natural logarithm) or NULL.
+ * A request whose kv_len is below n_b or beyond max_pages pages (or, with
+ * row_mask, whose n_b passes 64) is flagged and its rows are NaN; a page
+ * outside the cache is flagged and gives NaN to the rows that see it.
+ * Statistics and sums are fp32; the two roundings in between are those of the
+ * operands of the tensor cores: q scaled by a power of two per row and the
+ * softmax terms times vs_j, both to fp16 (11 bits).
+ * Limits: head_dim a multiple of 16 up to 128, page_size a multiple of 16,
+ * scale finite and > 0, kv scales >= 0 (below 2^100).
+ */
+DSPARK_API dspark_status dspark_block_attention(
+    const dspark_kv_cache *cache, const void *q, int64_t q_stride, dspark_dtype dtype, int n_q_heads,
+    const int64_t *row0, int n_rows, int B, const int32_t *block_table, int max_pages, const int32_t *kv_len,
+    const int32_t *prefix_pages, int n_prefix_pages, int prefix_len, dspark_block_mask mask,
+    const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream);
 
 /*
  * Self-test of the bounded device-side waits (the library's failure

@@ -19,6 +19,9 @@ from . import build as _build
 DSPARK_OK = 0
 DSPARK_BF16 = 0
 DSPARK_F32 = 1
+DSPARK_F16 = 2
+KV_E4M3, KV_INT8 = 0, 1
+MASK_CAUSAL, MASK_FULL = 0, 1
 WS_DRAFT, WS_SCHEDULE, WS_VERIFY, WS_DRAFT_RNN = 0, 1, 2, 3
 
 FLAG_BAD_TOKEN = 1
@@ -27,14 +30,24 @@ FLAG_BAD_VERIFY_LEN = 4
 FLAG_BAD_POS_TEMP = 8
 FLAG_TIMEOUT = 16
 FLAG_BAD_TARGET_ROW = 32
+FLAG_BAD_PAGE = 64
+FLAG_BAD_LENGTH = 128
+FLAG_NONFINITE = 256
 
 EXPORTS = ("dspark_version", "dspark_last_error", "dspark_workspace_bytes", "dspark_draft_sample",
            "dspark_schedule_prefix", "dspark_schedule_policy", "dspark_verify", "dspark_read_device_flags",
            "dspark_verify_noalloc", "dspark_draft_sample_rnn", "dspark_verify_packed", "dspark_pack_target",
-           "dspark_selftest_bounded_wait", "dspark_read_noalloc_flags", "dspark_selftest_philox_rate")
+           "dspark_selftest_bounded_wait", "dspark_read_noalloc_flags", "dspark_selftest_philox_rate",
+           "dspark_kv_append", "dspark_kv_read", "dspark_attention_workspace_bytes", "dspark_block_attention")
 
 _lib = None
 _lock = threading.Lock()
+
+
+class _CacheStruct(ctypes.Structure):
+    """struct dspark_kv_cache"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "flags")]
+                + [(n, ctypes.c_int32) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "format")])
 
 
 class DSparkError(RuntimeError):
@@ -94,6 +107,16 @@ def load(build_if_missing: bool = True):
         L.dspark_read_device_flags.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
         L.dspark_selftest_philox_rate.restype = ctypes.c_int
         L.dspark_selftest_philox_rate.argtypes = [vp, sz, i32, ctypes.POINTER(ctypes.c_double), vp]
+        i64, cache_p = ctypes.c_int64, ctypes.POINTER(_CacheStruct)
+        L.dspark_kv_append.restype = ctypes.c_int
+        L.dspark_kv_append.argtypes = [cache_p, vp, vp, i64, i64, i32, vp, i32, vp, vp, i32, i32, vp]
+        L.dspark_kv_read.restype = ctypes.c_int
+        L.dspark_kv_read.argtypes = [cache_p, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]
+        L.dspark_attention_workspace_bytes.restype = sz
+        L.dspark_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.dspark_block_attention.restype = ctypes.c_int
+        L.dspark_block_attention.argtypes = [cache_p, vp, i64, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32, i32,
+                                             i32, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.dspark_read_noalloc_flags.restype = ctypes.c_int
         L.dspark_read_noalloc_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         _lib = L
@@ -163,7 +186,12 @@ class WorkspaceCache:
         self._bufs = {}
 
     def get(self, which, B, G, V, r, device):
-        n = workspace_bytes(which, B, G, V, r)
+        return self._sized(which, workspace_bytes(which, B, G, V, r), device)
+
+    def attention(self, B, n_rows, n_q_heads, n_kv_heads, head_dim, device):
+        return self._sized("attention", attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim), device)
+
+    def _sized(self, which, n, device):
         if n == 0:
             raise ValueError("invalid sizes for a workspace")
         key = (which, device)
@@ -380,6 +408,147 @@ def pack_target(target, verify_len, *, out=None, stream=None):
     _check(lib.dspark_pack_target(_ptr(target), _ptr(verify_len), B, G1 - 1, V, _dtype_code(target),
                                   _ptr(out["target"]), _ptr(out["row0"]), _ptr(out.get("n_rows")),
                                   _stream(stream)))
+    return out
+
+
+# ------------------------------------------------- quantised cache, attention
+_KV_FORMATS = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+_ROW_DTYPES = {torch.bfloat16: DSPARK_BF16, torch.float32: DSPARK_F32, torch.float16: DSPARK_F16}
+_MASKS = {"causal": MASK_CAUSAL, "full": MASK_FULL}
+
+
+class KVCache:
+    """A paged, quantised key/value cache (struct dspark_kv_cache).
+
+    ``k`` and ``v`` [n_pages, n_kv_heads, page_size, head_dim] hold float8_e4m3fn
+    or int8 codes, ``k_scale`` and ``v_scale`` [n_pages, n_kv_heads, page_size]
+    fp32 one scale per token and head.  ``flags`` is the device flag word that
+    the calls on this cache OR their bits into: read it with
+    :func:`read_device_flags`, clear it with ``cache.flags.zero_()``."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dtype not in _KV_FORMATS:
+            raise TypeError("cache codes must be float8_e4m3fn or int8, got %s" % k.dtype)
+        if k.dim() != 4:
+            raise ValueError("cache codes are [n_pages, n_kv_heads, page_size, head_dim]")
+        _need(k, "k")
+        _need(v, "v", dtype=k.dtype, shape=k.shape, device=k.device)
+        _need(k_scale, "k_scale", dtype=torch.float32, shape=k.shape[:3], device=k.device)
+        _need(v_scale, "v_scale", dtype=torch.float32, shape=k.shape[:3], device=k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.flags = torch.zeros(64, dtype=torch.int32, device=k.device)
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                   self.flags.data_ptr(), *k.shape, _KV_FORMATS[k.dtype])
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, page_size, head_dim, *, dtype=torch.float8_e4m3fn, device="cuda"):
+        """A cache of zero codes and zero scales."""
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2)]
+        return cls(*codes, *[torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)])
+
+
+def _row_stride(t, name, heads, D, device):
+    """Checks packed rows [n, heads, D], whose rows may lie any 16-byte multiple
+    apart; returns their distance in elements."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    n, h, d = t.shape
+    if h != heads or d != D:
+        raise ValueError("%s must have shape (rows, %d, %d), got %s" % (name, heads, D, tuple(t.shape)))
+    row, head, elem = t.stride()
+    if elem != 1 or (h > 1 and head != D):
+        raise ValueError("the heads of a row of %s must be contiguous" % name)
+    return row if n > 1 else h * D
+
+
+def _paged(block_table, start, name, row0, device):
+    B, max_pages = block_table.shape
+    _need(block_table, "block_table", dtype=torch.int32, device=device)
+    _need(start, name, dtype=torch.int32, shape=(B,), device=device)
+    _need(row0, "row0", dtype=torch.int64, shape=(B + 1,), device=device)
+    return B, max_pages
+
+
+def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
+    """Quantise packed rows ``k``, ``v`` [n_rows, n_kv_heads, head_dim] into
+    ``cache``: row i of request b (rows row0[b] .. row0[b+1] - 1, ``row0``
+    [B+1] int64) at position start[b] + i of the request's pages
+    (``block_table`` [B, max_pages] int32).  See dspark_kv_append."""
+    lib = load()
+    dev = cache.device
+    B, max_pages = _paged(block_table, start, "start", row0, dev)
+    if k.dtype not in _ROW_DTYPES or v.dtype != k.dtype or v.shape != k.shape:
+        raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
+    ks = _row_stride(k, "k", cache.n_kv_heads, cache.head_dim, dev)
+    vs = _row_stride(v, "v", cache.n_kv_heads, cache.head_dim, dev)
+    _check(lib.dspark_kv_append(cache.struct, k.data_ptr(), v.data_ptr(), ks, vs, _ROW_DTYPES[k.dtype],
+                                row0.data_ptr(), k.shape[0], start.data_ptr(), block_table.data_ptr(), max_pages, B,
+                                _stream(stream)))
+
+
+def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, out=None, stream=None):
+    """Cached tokens as packed rows: row i of request b is position
+    start[b] + i.  Returns dict(k, v) of [n_rows, n_kv_heads, head_dim]; an
+    ``out`` with only one of them reads that one.  See dspark_kv_read."""
+    lib = load()
+    dev = cache.device
+    B, max_pages = _paged(block_table, start, "start", row0, dev)
+    shape = (n_rows, cache.n_kv_heads, cache.head_dim)
+    if out is None:
+        out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev))
+    if dtype not in _ROW_DTYPES:
+        raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
+    for name in out:
+        _need(out[name], name, dtype=dtype, shape=shape, device=dev)
+    _check(lib.dspark_kv_read(cache.struct, row0.data_ptr(), n_rows, start.data_ptr(), block_table.data_ptr(),
+                              max_pages, B, _ROW_DTYPES[dtype], _ptr(out.get("k")), _ptr(out.get("v")),
+                              _stream(stream)))
+    return out
+
+
+def attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) -> int:
+    return int(load().dspark_attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim))
+
+
+def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, prefix_len=0, mask="causal",
+                    row_mask=None, scale=None, out=None, workspace=None, stream=None):
+    """Attention of every request's block rows ``q`` [n_rows, n_q_heads,
+    head_dim] (row i of request b is row row0[b] + i) over the first
+    ``prefix_len`` tokens of ``prefix_pages`` (int32), which all requests share,
+    and over the request's own kv_len[b] cached tokens, the last ones of which
+    are the block itself.  ``mask`` ("causal" or "full") or ``row_mask``
+    ([n_rows] int64, bit t: the row sees token t of its block) rules inside the
+    block; ``scale`` is head_dim ** -0.5 by default.  See dspark_block_attention.
+
+    Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
+    lib = load()
+    dev = cache.device
+    B, max_pages = _paged(block_table, kv_len, "kv_len", row0, dev)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q must be bfloat16 or float16, got %s" % q.dtype)
+    n, Hq, D = q.shape
+    qs = _row_stride(q, "q", Hq, cache.head_dim, dev)
+    if prefix_pages is not None:
+        _need(prefix_pages, "prefix_pages", dtype=torch.int32, device=dev)
+    if row_mask is not None:
+        _need(row_mask, "row_mask", dtype=torch.int64, shape=(n,), device=dev)
+    if out is None:
+        out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
+                   lse=torch.empty((n, Hq), dtype=torch.float32, device=dev))
+    else:
+        _need(out["out"], "out", dtype=q.dtype, shape=(n, Hq, D), device=dev)
+        if out.get("lse") is not None:
+            _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
+    if workspace is None:
+        workspace = _default_ws.attention(B, n, Hq, cache.n_kv_heads, D, dev)
+    _check(lib.dspark_block_attention(
+        cache.struct, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0.data_ptr(), n, B, block_table.data_ptr(),
+        max_pages, kv_len.data_ptr(), _ptr(prefix_pages), 0 if prefix_pages is None else prefix_pages.numel(),
+        int(prefix_len), _MASKS[mask], _ptr(row_mask), D ** -0.5 if scale is None else float(scale),
+        out["out"].data_ptr(), _ptr(out.get("lse")), _ptr(workspace), workspace.numel(), _stream(stream)))
     return out
 
 

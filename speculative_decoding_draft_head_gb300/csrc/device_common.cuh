@@ -38,6 +38,9 @@ constexpr uint32_t kFlagBadVerifyLen = 4u;
 constexpr uint32_t kFlagBadPosTemp = 8u;
 constexpr uint32_t kFlagTimeout = 16u;
 constexpr uint32_t kFlagBadTargetRow = 32u;
+constexpr uint32_t kFlagBadPage = 64u;
+constexpr uint32_t kFlagBadLength = 128u;
+constexpr uint32_t kFlagNonfinite = 256u;
 
 // Row j of request b's target logits: the dense layout [B][G+1][V], or the
 // packed one (request b's rows 0, 1, .. from row row0[b] of n_rows rows).

@@ -220,6 +220,41 @@ constexpr int kScheduleMaxSmem = 200 * 1024;  // dynamic shared memory of the sc
 size_t schedule_smem_bytes(int B, int G, int L_min, int L_max);
 cudaError_t launch_schedule(const ScheduleArgs &a, cudaStream_t s);
 
+// ------------------------------------------------------- cache, attention --
+constexpr int kMaxHeadDim = 128;
+
+// rows of requests, their pages and the positions they start at (or their
+// lengths): what the cache and attention kernels find tokens with
+struct PagedRows {
+    const int64_t *row0;         // [B + 1]
+    const int32_t *start;        // [B] first position (append, read) or own length (attention)
+    const int32_t *block_table;  // [B][max_pages]
+    int max_pages, B, n_rows;
+};
+cudaError_t launch_kv_append(const dspark_kv_cache &c, const PagedRows &p, const void *k, const void *v,
+                             int64_t k_stride, int64_t v_stride, dspark_dtype dt, cudaStream_t s);
+cudaError_t launch_kv_read(const dspark_kv_cache &c, const PagedRows &p, dspark_dtype dt, void *k_out, void *v_out,
+                           cudaStream_t s);
+
+struct AttentionArgs {
+    dspark_kv_cache cache;
+    PagedRows rows;
+    const void *q;
+    int64_t q_stride;
+    dspark_dtype dt;
+    int n_q_heads;
+    const int32_t *prefix_pages;
+    int prefix_len;
+    int mask;                    // dspark_block_mask
+    const uint64_t *row_mask;
+    float scale;
+    void *out;
+    float *lse;
+    unsigned char *ws;
+};
+size_t attention_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s);
+
 // Launch `kernel` as a programmatic dependent of the stream's previous kernel:
 // its blocks may be scheduled while that kernel drains, and every kernel
 // launched this way starts with griddepcontrol.wait (griddep_wait), which
