@@ -491,7 +491,8 @@ DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_he
  * type, contiguous; lse [n_rows][n_q_heads] fp32 (natural logarithm) or NULL.
  * A request whose kv_len is below n_b or beyond max_pages pages (or, with
  * row_mask, whose n_b passes 64) is flagged and its rows are NaN; a page
- * outside the cache is flagged and gives NaN to the rows that see it.
+ * outside the cache is flagged; its tokens, like those stored with a NaN scale,
+ * give a NaN out and lse to the rows that see them and to no other.
  * Statistics and sums are fp32; the two roundings in between are those of the
  * operands of the tensor cores: q scaled by a power of two per row and the
  * softmax terms times vs_j, both to fp16 (11 bits).
