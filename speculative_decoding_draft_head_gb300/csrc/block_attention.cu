@@ -53,9 +53,9 @@ enum { kDirect = 0, kFirst = 1, kContinued = 2 };
 template <int DP>
 struct Layout {
     static constexpr int kOps = DP == 128 ? 3 : 4;    // fp16 operand ring (K and V tiles)
-    static constexpr int kRaw = DP == 128 ? 6 : 12;   // ring of 64-token halves as loaded
+    static constexpr int kRaw = DP == 128 ? 3 : 6;    // ring of tiles as loaded
     static constexpr uint32_t kTileBytes = 128 * DP * 2;
-    static constexpr uint32_t kRawBytes = 64 * DP + 512;
+    static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kOp = kQ + 2 * kTileBytes;
     static constexpr uint32_t kRawAt = kOp + kOps * kTileBytes;
@@ -153,15 +153,6 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     const bool ok = mbar_wait(bar, parity, abort, kSpinLimit);
     return __all_sync(0xffffffffu, ok);
-}
-
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // Steps of a piece in the order its operands are loaded, converted and used:
@@ -289,6 +280,65 @@ struct Walk {
     }
 };
 
+// ------------------------------------------------------------------------- q --
+// Up to 128 rows of a row tile, from its row t0 on, to fp16 in the swizzled
+// layout, each scaled by the power of two that takes its largest element into
+// [2^7, 2^8); qscale[row of the tile] is what its scores still lack (the power,
+// the caller's scale and log2 e).  Warp `part` of `parts` takes every parts-th
+// group of rows.
+template <typename T, int DP>
+__device__ __forceinline__ void load_q(const AttentionArgs &a, const Piece &p, int t0, int part, int parts, int group,
+                                       uint32_t dst, float *qscale, int lane) {
+    constexpr int kLanes = DP / 8, kPer = 32 / kLanes;  // lanes of a row (8 elements each), rows a warp takes at once
+    constexpr int kBatch = 4;
+    const int D = a.cache.head_dim, sub = lane % kLanes, d = sub * 8;
+    const int here = min(p.rows - t0, plan::kHalfRows);
+    const float inv_group = 1.f / (float)group;
+    const int blk0 = (p.m0 + t0) / group, g0 = p.m0 + t0 - blk0 * group;
+    const T *q0 = static_cast<const T *>(a.q) + ((int64_t)p.row_base + blk0) * a.q_stride + (int64_t)p.head * group * D + d;
+#pragma unroll 1
+    for (int r00 = part * kPer; r00 < here; r00 += parts * kPer * kBatch) {
+        const int r0 = r00 + lane / kLanes;
+        uint4 in[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * parts * kPer;
+            in[i] = make_uint4(0, 0, 0, 0);
+            if (r < here && d < D) {
+                // (g0 + r) / group: below 2^21, where this product is exact enough
+                const int g = g0 + r, row = (int)(((float)g + 0.5f) * inv_group);
+                in[i] = __ldg(reinterpret_cast<const uint4 *>(q0 + row * a.q_stride + (int64_t)(g - row * group) * D));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * parts * kPer;
+            const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+            float2 x[4];
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = pair_to_float<T>(w[e]);
+                top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
+            }
+#pragma unroll
+            for (int k = kLanes / 2; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+            if (r < here) {
+                const int e2 = top == 0 ? 7 : max((int)(top >> 23) - 127, -110);
+                const float mul = top >= 0x7f800000u ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + 7 - e2) << 23);
+                if (sub == 0)
+                    qscale[t0 + r] = fmaxf(__uint_as_float((uint32_t)(127 - 7 + min(e2, 127)) << 23) * (a.scale * kLog2e), 1e-37f);
+                if (d < D)
+                    st_shared_v4(dst + (uint32_t)(d >> 6) * (128u * 128u) + (uint32_t)r * 128u +
+                                     ((((uint32_t)d >> 3 & 7u) ^ ((uint32_t)r & 7u)) << 4),
+                                 make_uint4(half_pair(x[0].x * mul, x[0].y * mul), half_pair(x[1].x * mul, x[1].y * mul),
+                                            half_pair(x[2].x * mul, x[2].y * mul), half_pair(x[3].x * mul, x[3].y * mul)));
+            }
+            __syncwarp();
+        }
+    }
+}
+
 // ----------------------------------------------------------------- the kernel --
 template <typename T, int kFormat, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -330,11 +380,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t o_free = bar1 + 8u * 12u, drain = bar1 + 8u * 13u;
 
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), 4);
+        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 33), mbar_init(raw_empty(i), 4);
         for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), 4), mbar_init(op_empty(i), 1);
         for (int i = 0; i < kPieces; ++i) mbar_init(piece_full(i), 1), mbar_init(piece_empty(i), 15);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), 2), mbar_init(q_empty(i), 1);
+            mbar_init(q_full(i), 4), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
             mbar_init(o_full(i), 1), mbar_init(stat_full(i), 4);
         }
@@ -408,32 +458,43 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t tmem = (uint32_t)misc[2];
 
     if (warp >= 8) {
-        regs_dec<64>();
         if (warp == 12) {
             // ------------------------------------------------------ producer --
             Walk walk{a, lane, group, prefix_m, prefix_tiles, prefix_head, prefix_total};
             walk.begin(lo, hi, found_request, found_units);
             Piece cur, nxt;
             bool have = walk.next(cur), ok = true;
-            uint32_t raw = 0, count = 0;   // halves issued, pieces published
-            // pages of 32 chunks of 16 tokens (4 tiles) from tile t of a piece on, one a lane;
-            // -1: past the end, -2: a page outside the cache
+            uint32_t raw = 0, count = 0;   // tiles issued, pieces published
+            // Pages of 32 chunks of 16 tokens (4 tiles) from tile t of a piece on, one a lane; the
+            // chunk's number in the cache (in units of 16 head rows) is made from it when the page is
+            // first needed, 128 tokens x 4 later than its load.  A chunk lies inside one page.
             const int chunks_per_page = c.page_size / 16;
-            auto load_pages = [&](const Piece &p, int t) -> int {
+            const uint32_t page_chunks = (uint32_t)c.n_kv_heads * (uint32_t)chunks_per_page;
+            constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;
+            auto load_pages = [&](const Piece &p, int t, int &off) -> int {
                 const int chunk = (p.first + t) * 8 + lane;
-                if (t >= p.tiles || (int64_t)chunk * 16 >= p.len) return -1;
+                if (t >= p.tiles || (int64_t)chunk * 16 >= p.len) {
+                    off = -1;
+                    return 0;
+                }
                 const int slot = chunk / chunks_per_page;
-                const int page =
-                    p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
-                return page;
+                off = p.head * chunks_per_page + (chunk - slot * chunks_per_page);
+                return p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
             };
-            int pages_next = have ? load_pages(cur, 0) : -1;
+            auto number = [&](int page, int off) -> uint32_t {
+                return off < 0 ? kNone : (page < 0 || page >= c.n_pages) ? kBad : (uint32_t)page * page_chunks + (uint32_t)off;
+            };
+            const unsigned char *k_lane = static_cast<const unsigned char *>(c.k) + lane * 16;
+            const unsigned char *v_lane = static_cast<const unsigned char *>(c.v) + lane * 16;
+            // scales: lane's 16 bytes are tokens 4 (lane & 3) .. of chunk lane / 4
+            const float *ks_lane = c.k_scale + (lane & 3) * 4, *vs_lane = c.v_scale + (lane & 3) * 4;
+            int off_next = -1;
+            int page_next = have ? load_pages(cur, 0, off_next) : 0;
             while (ok) {
-                int pages[2];
-                pages[0] = pages_next;
-                pages[1] = -1;
+                int page = page_next, off = off_next;            // the next window to be needed
+                uint32_t chunk_id[2] = {kNone, kNone};            // this lane's chunk in even and odd windows
                 const bool more = have && walk.next(nxt);
-                pages_next = more ? load_pages(nxt, 0) : -1;
+                page_next = more ? load_pages(nxt, 0, off_next) : 0;
                 const int ps = (int)(count % kPieces);
                 if (!warp_wait(piece_empty(ps), ((count / kPieces) & 1) ^ 1, abort)) { ok = false; break; }
                 if (!have) cur.tiles = 0;
@@ -445,94 +506,107 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (!have) break;
                 const bool pair = cur.rows > plan::kHalfRows;
                 bool flagged = false;
-                for (int s = 0; s < 2 * cur.tiles && ok; ++s) {
+                const int steps = 2 * cur.tiles;
+                for (int s = 0; s < steps; ++s, ++raw) {
                     bool is_v;
                     int j;
                     step_of(s, cur.tiles, pair, is_v, j);
-                    // all values of the previous four tiles are on their way: their register is free
-                    if (is_v && (j & 3) == 0) {
-                        const int pg = load_pages(cur, (j & ~3) + 4);
-                        if ((j >> 2) & 1) pages[0] = pg; else pages[1] = pg;
+                    const bool odd = (j >> 2) & 1;
+                    if (!is_v && (j & 3) == 0) {
+                        // a new window; the one before it is still needed for values
+                        const uint32_t id = number(page, off);
+                        if (odd) chunk_id[1] = id; else chunk_id[0] = id;
+                        page = load_pages(cur, j + 4, off);
                     }
-                    for (int half = 0; half < 2; ++half, ++raw) {
-                        const int slot = (int)(raw % kRaw);
-                        // lanes 0-3: the half's four chunks of codes; 4-7, 8-11 (with the keys): both scales
-                        const int piece16 = half * 4 + (lane & 3);
-                        const int tok = (cur.first + j) * plan::kTile + piece16 * 16;
-                        const int from = ((j & 3) << 3) + piece16;
-                        const int p0 = __shfl_sync(0xffffffffu, pages[0], from), p1 = __shfl_sync(0xffffffffu, pages[1], from);
-                        const int page = ((j >> 2) & 1) ? p1 : p0;
-                        const bool inside = tok < cur.len, good = inside && page >= 0 && page < c.n_pages;
-                        const unsigned bad = __ballot_sync(0xffffffffu, inside && !good) & 0xfu;
-                        const unsigned here = __ballot_sync(0xffffffffu, good) & 0xfu;
-                        if (!warp_wait(raw_empty(slot), ((raw / kRaw) & 1) ^ 1, abort)) { ok = false; break; }
-                        const uint32_t at = base + L::kRawAt + (uint32_t)slot * L::kRawBytes;
-                        if (lane == 0) {
-                            raw_bad[slot] = (int)bad;
-                            mbar_arrive_expect_tx(raw_full(slot),
-                                                  (uint32_t)__popc(here) * (uint32_t)(16 * D + (is_v ? 0 : 128)));
+                    const uint32_t mine = odd ? chunk_id[1] : chunk_id[0];
+                    const int from = (j & 3) << 3;
+                    const int slot = (int)(raw % kRaw);
+                    if (!warp_wait(raw_empty(slot), ((raw / kRaw) & 1) ^ 1, abort)) { ok = false; break; }
+                    const uint32_t at = base + L::kRawAt + (uint32_t)slot * L::kRawBytes + (uint32_t)lane * 16u;
+                    const unsigned char *codes = is_v ? v_lane : k_lane;
+                    const unsigned bad = (__ballot_sync(0xffffffffu, mine == kBad) >> from) & 0xffu;
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        const uint32_t id = __shfl_sync(0xffffffffu, mine, from + ch);
+                        if (id >= kBad) continue;
+                        const unsigned char *src = codes + (uint64_t)id * (uint32_t)(16 * D);
+                        const uint32_t dst = at + (uint32_t)(ch * 16 * D);
+                        if (D == 128) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) cp_async_16(dst + 512u * i, src + 512 * i, 16);
+                        } else {
+                            for (int i = lane; i < D; i += 32) cp_async_16(dst + 16u * (uint32_t)(i - lane), src + 16 * (i - lane), 16);
                         }
-                        __syncwarp();
-                        if (good && lane < (is_v ? 4 : 12)) {
-                            const int64_t place = ((int64_t)page * c.n_kv_heads + cur.head) * c.page_size + tok % c.page_size;
-                            const uint32_t i = (uint32_t)(lane & 3);
-                            if (lane < 4)
-                                bulk_load(at + i * 16u * (uint32_t)D,
-                                          static_cast<const unsigned char *>(is_v ? c.v : c.k) + place * D, 16u * (uint32_t)D,
-                                          raw_full(slot));
-                            else
-                                bulk_load(at + 64u * DP + (lane < 8 ? 0u : 256u) + i * 64u,
-                                          (lane < 8 ? c.k_scale : c.v_scale) + place, 64u, raw_full(slot));
-                        }
-                        flagged |= bad != 0;
                     }
+                    if (!is_v) {
+                        const uint32_t id = __shfl_sync(0xffffffffu, mine, from + (lane >> 2));
+                        if (id < kBad) {
+                            cp_async_16(at + 128u * DP, ks_lane + (uint64_t)id * 16u, 16);
+                            cp_async_16(at + 128u * DP + 512u, vs_lane + (uint64_t)id * 16u, 16);
+                        }
+                    }
+                    cp_async_arrive(raw_full(slot));
+                    if (lane == 0) {
+                        raw_bad[slot] = (int)bad;
+                        mbar_arrive(raw_full(slot));
+                    }
+                    flagged |= bad != 0;
                 }
                 if (flagged && lane == 0) atomicOr(c.flags, kFlagBadPage);
                 cur = nxt;
                 have = more;
             }
-            if (!ok) {
-                if (lane == 0) *abort = 1;
-                // copies in flight must land before the block's memory goes
-                for (uint32_t i = raw > (uint32_t)kRaw ? raw - kRaw : 0; i < raw; ++i)
-                    mbar_wait(raw_full((int)(i % kRaw)), (i / kRaw) & 1, never, kDrainLimit);
-            }
+            if (!ok && lane == 0) *abort = 1;
+            cp_async_wait_all();   // nothing may be in flight when the block's memory goes
         } else if (warp == 13) {
             // ------------------------------------------- tensor-core products --
-            if (lane == 0) {
+            {
+                const bool leader = elect_one();
                 const uint32_t hi_desc = (uint32_t)(sw128_kmajor_desc(0) >> 32);
                 const uint32_t id_qk = idesc_f16_f32(128, 128, false), id_pv = idesc_f16_f32(128, D, true);
                 constexpr uint32_t kAtom = 128 * 128;  // bytes of a 64-column atom of a 128-row tile
                 uint32_t op = 0, qc = 0, count = 0, pc[2] = {0, 0};
                 bool ok = true;
+                const int k_steps = D / 16;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     if (!ok) return false;
-                    ok = mbar_wait(bar, parity, abort, kSpinLimit);
+                    ok = warp_wait(bar, parity, abort);
                     tc_fence_after();
                     return ok;
+                };
+                // the whole warp walks the loop, so that addresses stay warp-uniform; one lane issues
+                auto commit = [&](uint32_t bar) {
+                    if (leader) umma_commit(bar);
                 };
                 auto qk = [&](int w, uint32_t qbuf, uint32_t slot) {
                     const uint32_t qa = (base + L::kQ + qbuf * L::kTileBytes) >> 4 | 1u << 16;
                     const uint32_t ka = (base + L::kOp + slot * L::kTileBytes) >> 4 | 1u << 16;
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32u) >> 4;
-                        umma_bf16_w(tmem + kColS + 128u * w, qa + off, ka + off, hi_desc, id_qk, k > 0);
+                    const uint32_t d = tmem + kColS + 128u * (uint32_t)w;
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k) {
+                            const uint32_t off = ((uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32u) >> 4;
+                            if (k < k_steps) umma_bf16_w(d, qa + off, ka + off, hi_desc, id_qk, k > 0);
+                        }
+                        umma_commit(s_full(w));
                     }
-                    umma_commit(s_full(w));
                 };
                 auto pv = [&](int w, uint32_t slot, bool accumulate) {
                     const uint32_t va = (base + L::kOp + slot * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
+                    const uint32_t d = tmem + kColO + 128u * (uint32_t)w, pa = tmem + kColS + 128u * (uint32_t)w;
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_bf16_ts(tmem + kColO + 128u * w, tmem + kColS + 128u * w + 8u * k, va + (uint32_t)k * (2048u >> 4),
-                                     hi_desc, id_pv, accumulate || k > 0);
+                        for (int k = 0; k < 8; ++k)
+                            umma_bf16_ts(d, pa + 8u * (uint32_t)k, va + (uint32_t)k * (2048u >> 4), hi_desc, id_pv,
+                                         k > 0 ? 1u : (uint32_t)accumulate);
+                    }
                 };
                 while (true) {
                     const int ps = (int)(count % kPieces);
                     if (!wait(piece_full(ps), (count / kPieces) & 1)) break;
                     const int n = pieces[ps].tiles;
                     const bool pair = pieces[ps].rows > plan::kHalfRows;
-                    mbar_arrive(piece_empty(ps));
+                    if (lane == 0) mbar_arrive(piece_empty(ps));
                     if (n == 0) break;
                     // this piece's q tiles: one, or one per group
                     uint32_t qb[2] = {qc & 1, qc & 1}, qp[2] = {(qc >> 1) & 1, (qc >> 1) & 1};
@@ -545,9 +619,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         if (!op_ready(op)) break;
                         for (int w = 0; w < 2; ++w) {
                             qk(w, qb[w], op % kOps);
-                            if (n == 1) umma_commit(q_empty((int)qb[w]));
+                            if (n == 1) commit(q_empty((int)qb[w]));
                         }
-                        umma_commit(op_empty((int)(op % kOps)));
+                        commit(op_empty((int)(op % kOps)));
                         if (count > 0 && !wait(o_free, (count - 1) & 1)) break;
                         for (int j = 0; j < n && ok; ++j) {
                             const uint32_t vi = op + 2 * j + 1, ki = op + 2 * j + 2;
@@ -556,14 +630,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                 if (!wait(p_ready(w), pc[w] & 1)) break;
                                 ++pc[w];
                                 pv(w, vi % kOps, j > 0);
-                                if (w == 1) umma_commit(op_empty((int)(vi % kOps)));
+                                if (w == 1) commit(op_empty((int)(vi % kOps)));
                                 if (j + 1 < n) {
                                     if (w == 0 && !op_ready(ki)) break;
                                     qk(w, qb[w], ki % kOps);
-                                    if (j + 2 == n) umma_commit(q_empty((int)qb[w]));
-                                    if (w == 1) umma_commit(op_empty((int)(ki % kOps)));
+                                    if (j + 2 == n) commit(q_empty((int)qb[w]));
+                                    if (w == 1) commit(op_empty((int)(ki % kOps)));
                                 } else {
-                                    umma_commit(o_full(w));
+                                    commit(o_full(w));
                                 }
                             }
                         }
@@ -574,8 +648,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         for (int j = 0; j < 2 && j < n; ++j) {
                             if (!op_ready(k_at(j))) break;
                             qk(j, qb[0], k_at(j) % kOps);
-                            umma_commit(op_empty((int)(k_at(j) % kOps)));
-                            if (j == n - 1) umma_commit(q_empty((int)qb[0]));
+                            commit(op_empty((int)(k_at(j) % kOps)));
+                            if (j == n - 1) commit(q_empty((int)qb[0]));
                         }
                         if (!ok) break;
                         if (count > 0 && !wait(o_free, (count - 1) & 1)) break;
@@ -584,14 +658,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             if (!op_ready(v_at(j)) || !wait(p_ready(w), pc[w] & 1)) break;
                             ++pc[w];
                             pv(w, v_at(j) % kOps, j >= 2);
-                            umma_commit(op_empty((int)(v_at(j) % kOps)));
+                            commit(op_empty((int)(v_at(j) % kOps)));
                             if (j + 2 < n) {
                                 if (!op_ready(k_at(j + 2))) break;
                                 qk(w, qb[0], k_at(j + 2) % kOps);
-                                umma_commit(op_empty((int)(k_at(j + 2) % kOps)));
-                                if (j + 3 == n) umma_commit(q_empty((int)qb[0]));
+                                commit(op_empty((int)(k_at(j + 2) % kOps)));
+                                if (j + 3 == n) commit(q_empty((int)qb[0]));
                             } else {
-                                umma_commit(o_full(w));
+                                commit(o_full(w));
                             }
                         }
                     }
@@ -600,71 +674,30 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     ++count;
                 }
                 if (!ok) {
-                    *abort = 1;
-                    umma_commit(drain);
+                    if (lane == 0) *abort = 1;
+                    commit(drain);
                     mbar_wait(drain, 0, never, kDrainLimit);
                 }
             }
         } else if (warp >= 14) {
             // ------------------------------------------------------------ q --
-            constexpr int kLanes = DP / 8, kPer = 32 / kLanes;  // lanes of a row (8 elements each), rows a warp takes at once
-            constexpr int kBatch = 4;
-            const int sub = lane % kLanes, d = sub * 8;
+            // (pieces of at most 128 rows, ahead of their use)
             uint32_t qc = 0, count = 0;
             bool ok = true;
             while (ok) {
                 const int ps = (int)(count % kPieces);
                 if (!warp_wait(piece_full(ps), (count / kPieces) & 1, abort)) { ok = false; break; }
-                const int n = pieces[ps].tiles, rows = pieces[ps].rows, m0 = pieces[ps].m0, head = pieces[ps].head;
-                const int64_t row_base = pieces[ps].row_base;
-                float *qscale = reinterpret_cast<float *>(gen + L::kQScale) + ps * 256;
-                for (int t0 = 0; n > 0 && t0 < rows && ok; t0 += plan::kHalfRows, ++qc) {
-                    const int buf = (int)(qc & 1), here = min(rows - t0, plan::kHalfRows);
+                const int n = pieces[ps].tiles, rows = pieces[ps].rows;
+                if (n > 0 && rows > plan::kHalfRows) qc += 2;
+                else if (n > 0) {
+                    const int buf = (int)(qc & 1);
                     if (!warp_wait(q_empty(buf), ((qc >> 1) & 1) ^ 1, abort)) { ok = false; break; }
-                    const uint32_t dst = base + L::kQ + (uint32_t)buf * L::kTileBytes;
-                    for (int r0 = (warp - 14) * kPer + lane / kLanes; r0 - lane / kLanes < here; r0 += 2 * kPer * kBatch) {
-                        uint4 in[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int r = r0 + i * 2 * kPer;
-                            in[i] = make_uint4(0, 0, 0, 0);
-                            if (r < here && d < D) {
-                                const int m = m0 + t0 + r, row = m / group;
-                                in[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                    static_cast<const T *>(a.q) + (row_base + row) * a.q_stride +
-                                    ((int64_t)head * group + (m - row * group)) * D + d));
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int r = r0 + i * 2 * kPer;
-                            const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                            float2 x[4];
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                x[e] = pair_to_float<T>(w[e]);
-                                top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
-                            }
-#pragma unroll
-                            for (int k = kLanes / 2; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
-                            if (r >= here) continue;
-                            // the power of two that takes the row's largest element into [2^7, 2^8)
-                            const int e2 = top == 0 ? 7 : max((int)(top >> 23) - 127, -110);
-                            const float mul = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
-                                                                 : __uint_as_float((uint32_t)(127 + 7 - e2) << 23);
-                            if (sub == 0)
-                                qscale[t0 + r] = fmaxf(__uint_as_float((uint32_t)(127 - 7 + min(e2, 127)) << 23) * (a.scale * kLog2e), 1e-37f);
-                            if (d < D)
-                                st_shared_v4(dst + (uint32_t)(d >> 6) * (128u * 128u) + (uint32_t)r * 128u +
-                                                 ((((uint32_t)d >> 3 & 7u) ^ ((uint32_t)r & 7u)) << 4),
-                                             make_uint4(half_pair(x[0].x * mul, x[0].y * mul), half_pair(x[1].x * mul, x[1].y * mul),
-                                                        half_pair(x[2].x * mul, x[2].y * mul), half_pair(x[3].x * mul, x[3].y * mul)));
-                        }
-                    }
+                    load_q<T, DP>(a, pieces[ps], 0, warp - 14, 2, group, base + L::kQ + (uint32_t)buf * L::kTileBytes,
+                                  reinterpret_cast<float *>(gen + L::kQScale) + ps * 256, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full(buf));
+                    if (lane < 2) mbar_arrive(q_full(buf));
+                    ++qc;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(piece_empty(ps));
@@ -676,7 +709,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             // ---------------------------------------------------- converters --
             const int t = tid - 256;
             const int cpr = D / 16;                      // 16-code chunks of a token
-            uint32_t raw = 0, op = 0, count = 0, tile0 = 0;
+            uint32_t op = 0, count = 0, tile0 = 0;
             bool ok = true;
             while (ok) {
                 const int ps = (int)(count % kPieces);
@@ -689,65 +722,74 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     step_of(s, n, pair, is_v, j);
                     const uint32_t dst = base + L::kOp + (op % kOps) * L::kTileBytes;
                     if (!warp_wait(op_empty((int)(op % kOps)), ((op / kOps) & 1) ^ 1, abort)) { ok = false; break; }
-                    for (int half = 0; half < 2; ++half, ++raw) {
-                        const int slot = (int)(raw % kRaw);
-                        if (!warp_wait(raw_full(slot), (raw / kRaw) & 1, abort)) { ok = false; break; }
-                        const uint32_t src = base + L::kRawAt + (uint32_t)slot * L::kRawBytes;
-                        const int bad = raw_bad[slot];
-                        const int valid = min(64, len - ((first + j) * plan::kTile + half * 64));  // tokens of this half (or <= 0)
-                        const bool whole = valid == 64 && bad == 0;
-                        auto convert = [&](int row, int ch) {
-                            uint4 in = ld_shared_v4(src + (uint32_t)(row * cpr + ch) * 16u);
-                            if (!whole && (row >= valid || (bad >> (row >> 4) & 1))) in = make_uint4(0, 0, 0, 0);
-                            __half2 h[8];
-                            decode4<kFormat>(in.x, h[0], h[1]);
-                            decode4<kFormat>(in.y, h[2], h[3]);
-                            decode4<kFormat>(in.z, h[4], h[5]);
-                            decode4<kFormat>(in.w, h[6], h[7]);
-                            const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
-                            const uint4 lo4 = make_uint4(u[0], u[1], u[2], u[3]), hi4 = make_uint4(u[4], u[5], u[6], u[7]);
-                            const uint32_t r = (uint32_t)(half * 64 + row), c8 = (uint32_t)(ch & 3) * 2u;
-                            const uint32_t line = dst + (uint32_t)(ch >> 2) * (128u * 128u) + r * 128u;
-                            // lanes of the upper 64 columns write their second half first: no two of a
-                            // row's lanes then meet in a bank
-                            const uint32_t o = (uint32_t)(ch >> 2) & 1u;
-                            st_shared_v4(line + (((c8 + o) ^ (r & 7u)) << 4), o ? hi4 : lo4);
-                            st_shared_v4(line + (((c8 + 1u - o) ^ (r & 7u)) << 4), o ? lo4 : hi4);
-                        };
-                        if (D == DP) {
-                            constexpr int kCpr = DP / 16;
-#pragma unroll
-                            for (int i = 0; i < 64 * kCpr / 128; ++i) convert((t + 128 * i) / kCpr, (t + 128 * i) % kCpr);
-                        } else {
-                            for (int i = t; i < 64 * cpr; i += 128) convert(i / cpr, i % cpr);
-                        }
-                        if (!is_v && t < 64) {
-                            // the tile's scales, for the softmax groups
-                            const int ss = (int)((tile0 + j) % kScaleSlots);
-                            float *sc = reinterpret_cast<float *>(gen + L::kScale) + ss * 256 + half * 64;
-                            const float *rs = reinterpret_cast<const float *>(gen + L::kRawAt + (uint32_t)slot * L::kRawBytes + 64 * DP);
-                            float ks = 0.f, vs = 0.f;
-                            if (t < valid) {
-                                // a token whose value scale (or page) is no number carries its NaN in the
-                                // key's scale alone: where it is masked, P is 0 times the value's
-                                ks = rs[t];
-                                vs = rs[64 + t];
-                                if ((bad >> (t >> 4) & 1) || !(vs <= 3.4028235e38f)) ks = __int_as_float(0x7fffffff), vs = 0.f;
-                            }
-                            sc[t] = ks;
-                            sc[128 + t] = vs;
-                            float top = fmaxf(vs, 0.f);   // a NaN gives 0
-#pragma unroll
-                            for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                            if (lane == 0) vmax[ss][half * 2 + (t >> 5)] = top;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(raw_empty(slot));
-                            if (half == 1) mbar_arrive(op_full((int)(op % kOps)));
-                        }
+                    const int slot = (int)(op % kRaw);
+                    if (!warp_wait(raw_full(slot), (op / kRaw) & 1, abort)) { ok = false; break; }
+                    const uint32_t src = base + L::kRawAt + (uint32_t)slot * L::kRawBytes;
+                    const int bad = raw_bad[slot];
+                    const int valid = len - (first + j) * plan::kTile;   // tokens of this tile that exist (128 or more: all)
+                    const bool whole = valid >= plan::kTile && bad == 0;
+                    auto decode_store = [&](uint4 in, int row, int ch) {
+                        __half2 h[8];
+                        decode4<kFormat>(in.x, h[0], h[1]);
+                        decode4<kFormat>(in.y, h[2], h[3]);
+                        decode4<kFormat>(in.z, h[4], h[5]);
+                        decode4<kFormat>(in.w, h[6], h[7]);
+                        const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
+                        const uint4 lo4 = make_uint4(u[0], u[1], u[2], u[3]), hi4 = make_uint4(u[4], u[5], u[6], u[7]);
+                        const uint32_t r = (uint32_t)row, c8 = (uint32_t)(ch & 3) * 2u;
+                        const uint32_t line = dst + (uint32_t)(ch >> 2) * (128u * 128u) + r * 128u;
+                        // lanes of the upper 64 columns write their second half first: no two of a
+                        // row's lanes then meet in a bank
+                        const uint32_t o = (uint32_t)(ch >> 2) & 1u;
+                        st_shared_v4(line + (((c8 + o) ^ (r & 7u)) << 4), o ? hi4 : lo4);
+                        st_shared_v4(line + (((c8 + 1u - o) ^ (r & 7u)) << 4), o ? lo4 : hi4);
+                    };
+                    auto keep = [&](uint4 in, int row) {   // nothing of a token that is not there
+                        return row < valid && !(bad >> (row >> 4) & 1) ? in : make_uint4(0, 0, 0, 0);
+                    };
+                    float ks = 0.f, vs = 0.f;
+                    if (!is_v && t < valid) {
+                        // a token whose value scale (or page) is no number carries its NaN in the key's
+                        // scale alone: where it is masked, P is 0 times the value's
+                        const float *rs = reinterpret_cast<const float *>(gen + L::kRawAt + (uint32_t)slot * L::kRawBytes + 128 * DP);
+                        ks = rs[t];
+                        vs = rs[128 + t];
+                        if ((bad >> (t >> 4) & 1) || !(vs <= 3.4028235e38f)) ks = __int_as_float(0x7fffffff), vs = 0.f;
                     }
+                    if (D == DP) {
+                        // all loads first: the slot goes back before the decoding
+                        constexpr int kCpr = DP / 16, kEach = kCpr;
+                        uint4 in[kEach];
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) in[i] = ld_shared_v4(src + (uint32_t)(t + 128 * i) * 16u);
+                        if (!whole) {
+#pragma unroll
+                            for (int i = 0; i < kEach; ++i) in[i] = keep(in[i], (t + 128 * i) / kCpr);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty(slot));
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) decode_store(in[i], (t + 128 * i) / kCpr, (t + 128 * i) % kCpr);
+                    } else {
+                        for (int i = t; i < 128 * cpr; i += 128) {
+                            const int row = i / cpr;
+                            decode_store(keep(ld_shared_v4(src + (uint32_t)i * 16u), row), row, i - row * cpr);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty(slot));
+                    }
+                    if (!is_v) {
+                        // the tile's scales, for the softmax groups
+                        const int ss = (int)((tile0 + j) % kScaleSlots);
+                        float *sc = reinterpret_cast<float *>(gen + L::kScale) + ss * 256;
+                        sc[t] = ks;
+                        sc[128 + t] = vs;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.f)));
+                        if (lane == 0) vmax[ss][t >> 5] = __uint_as_float(top);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(op_full((int)(op % kOps)));
                 }
                 tile0 += (uint32_t)n;
                 __syncwarp();
@@ -759,12 +801,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         }
     } else {
         // -------------------------------------------------------------- softmax --
-        regs_inc<192>();
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * w, my_o = lanes + kColO + 128u * w;
         float2 *stats = reinterpret_cast<float2 *>(gen + L::kStats);
-        uint32_t sc_count = 0, oc = 0, xc = 0, count = 0, tile0 = 0;
+        uint32_t sc_count = 0, oc = 0, xc = 0, count = 0, tile0 = 0, qc = 0;
         bool ok = true;
         while (ok) {
             const int ps = (int)(count % kPieces);
@@ -775,6 +816,17 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 break;
             }
             const bool pair = p.rows > plan::kHalfRows;
+            if (pair) {
+                const uint32_t q = qc + (uint32_t)w;
+                const int buf = (int)(q & 1);
+                if (!warp_wait(q_empty(buf), ((q >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+                load_q<T, DP>(a, p, w * 128, warp & 3, 4, group, base + L::kQ + (uint32_t)buf * L::kTileBytes,
+                              reinterpret_cast<float *>(gen + L::kQScale) + ps * 256, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(buf));
+            }
+            qc += pair ? 2 : 1;
             const int step = pair ? 1 : 2, t_first = pair ? 0 : w;
             const int rows = pair ? min(max(p.rows - w * 128, 0), 128) : p.rows;
             const int mt = pair ? w * 128 + row : row;       // row of the row tile
@@ -799,43 +851,55 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     if (j == t_first) cm = live ? (reinterpret_cast<const float *>(gen + L::kQScale))[ps * 256 + mt] : 0.f;
                     const int ss = (int)((tile0 + j) % kScaleSlots);
                     const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + ss * 256, *vs = ks + 128;
-                    __syncwarp();
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(my_s + 32u * q, x[q]);
                     const float4 vm = *reinterpret_cast<const float4 *>(vmax[ss]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_wait32(x[q]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    const int t0 = (p.first + j) * plan::kTile;
+                    const bool masked = t0 > p.ctx - plan::kTile;   // some row does not see some token of this tile
+                    __syncwarp();
+                    // x = ks * (q . k~) of 32 columns, those the row does not see -inf
+                    auto scores = [&](uint32_t (&x)[32], int q) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + e);
                             float y0, y1, y2, y3;
-                            unpack2(mul2(pack2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), pack2(k4.x, k4.y)), y0, y1);
-                            unpack2(mul2(pack2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3])), pack2(k4.z, k4.w)), y2, y3);
-                            x[q][e] = __float_as_uint(y0), x[q][e + 1] = __float_as_uint(y1);
-                            x[q][e + 2] = __float_as_uint(y2), x[q][e + 3] = __float_as_uint(y3);
+                            unpack2(mul2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pack2(k4.x, k4.y)), y0, y1);
+                            unpack2(mul2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), pack2(k4.z, k4.w)), y2, y3);
+                            x[e] = __float_as_uint(y0), x[e + 1] = __float_as_uint(y1);
+                            x[e + 2] = __float_as_uint(y2), x[e + 3] = __float_as_uint(y3);
                         }
-                    }
-                    const int t0 = (p.first + j) * plan::kTile;
-                    if (t0 > p.ctx - plan::kTile) {   // some row does not see some token of this tile
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        if (masked) {
                             const int from = t0 + 32 * q, full = min(max(sees - from, 0), 32);
                             uint32_t bits = full == 32 ? 0xffffffffu : (1u << full) - 1u;
                             const int sh = from - p.ctx;   // block token of the first column
                             if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(bits >> e & 1u)) x[q][e] = 0xff800000u;
+                                if (!(bits >> e & 1u)) x[e] = 0xff800000u;
                         }
+                    };
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto maxima = [&](uint32_t (&x)[32], int q) {
+                        scores(x, q);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tops[k] = max3(tops[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
+                    };
+                    // the scores are read twice from tensor memory, 32 columns at a time and one load
+                    // ahead: holding a row's 128 scores instead spills
+                    uint32_t xa[32], xb[32];
+                    tmem_ld32(my_s, xa);
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        tmem_ld_wait32(xa);
+                        tmem_ld32(my_s + 32u * (q + 1), xb);
+                        maxima(xa, q);
+                        tmem_ld_wait32(xb);
+                        tmem_ld32(my_s + 32u * ((q + 2) & 3), xa);
+                        maxima(xb, q + 1);
                     }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
+                    tmem_ld_wait32(xa);
+                    const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
                     // P <= 2^(bound - r): the row's largest score with the tile's largest value scale
                     const float vt = fmaxf(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kScaleFloor);
                     const float bound = top * cm + (float)((int)(__float_as_uint(vt) >> 23) - 126);
@@ -847,30 +911,28 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         l *= f;
                         if (j != t_first) {
                             // the group's previous product has ended (the scores came after it)
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < DP / 32; ++q) {
-                                uint32_t o[32];
-                                tmem_ld32(my_o + 32u * q, o);
-                                tmem_ld_wait32(o);
+                                tmem_ld32(my_o + 32u * q, xb);
+                                tmem_ld_wait32(xb);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(my_o + 32u * q, o);
+                                for (int e = 0; e < 32; ++e) xb[e] = __float_as_uint(__uint_as_float(xb[e]) * f);
+                                tmem_st32(my_o + 32u * q, xb);
                             }
                         }
                     }
                     const float ref = r == -INFINITY ? 0.f : r;
                     const uint64_t c2 = pack2(cm, cm), r2 = pack2(-ref, -ref);
                     uint64_t sum[2] = {0, 0};
+                    auto terms = [&](uint32_t (&x)[32], int q) {
+                        scores(x, q);
+                        uint32_t pr[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pr[32];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const int q = 2 * h + (e >> 5), f = e & 31;
-                            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 64 * h + e);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * q + e);
                             float y0, y1, y2, y3;
-                            unpack2(fma2(pack2(__uint_as_float(x[q][f]), __uint_as_float(x[q][f + 1])), c2, r2), y0, y1);
-                            unpack2(fma2(pack2(__uint_as_float(x[q][f + 2]), __uint_as_float(x[q][f + 3])), c2, r2), y2, y3);
+                            unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, r2), y0, y1);
+                            unpack2(fma2(pack2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c2, r2), y2, y3);
                             const uint64_t e0 = pack2(fast_exp2(y0), fast_exp2(y1)), e1 = pack2(fast_exp2(y2), fast_exp2(y3));
                             sum[0] = add2(sum[0], e0);
                             sum[1] = add2(sum[1], e1);
@@ -879,7 +941,17 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             pr[e >> 1] = half_pair(y0, y1);
                             pr[(e >> 1) + 1] = half_pair(y2, y3);
                         }
-                        tmem_st32(my_s + 32u * h, pr);
+                        // P's 16 columns lie below the scores still to be read
+                        tmem_st16(my_s + 16u * q, pr);
+                    };
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        tmem_ld32(my_s + 32u * (q + 1), xb);
+                        terms(xa, q);
+                        tmem_ld_wait32(xb);
+                        if (q == 0) tmem_ld32(my_s + 64u, xa);
+                        terms(xb, q + 1);
+                        if (q == 0) tmem_ld_wait32(xa);
                     }
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
