@@ -493,9 +493,10 @@ DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_he
  * row_mask, whose n_b passes 64) is flagged and its rows are NaN; a page
  * outside the cache is flagged; its tokens, like those stored with a NaN scale,
  * give a NaN out and lse to the rows that see them and to no other.
- * Statistics and sums are fp32; the two roundings in between are those of the
- * operands of the tensor cores: q scaled by a power of two per row and the
- * softmax terms times vs_j, both to fp16 (11 bits).
+ * Statistics and sums are fp32.  The operands of the tensor cores are fp16:
+ * codes exactly, q scaled by a power of two (exact to 2^-25 of its row's
+ * largest element), the softmax terms, and the values with their scale; the
+ * last two are rounded (2^-11 each).
  * Limits: head_dim a multiple of 16 up to 128, page_size a multiple of 16,
  * scale finite and > 0, kv scales >= 0 (below 2^100).
  */

@@ -2,29 +2,34 @@
 // request's own tokens, both in the quantised cache.
 //
 // Mathematics.  Row m (a block row of a query head) against tokens j, with 8-bit
-// codes k~, v~ and scales ks, vs: x_j = ks_j (q . k~_j), s_j = c x_j in log2
-// units, and with any reference r
-//   O = sum_j [2^(s_j - r) vs_j] v~_j,   l = sum_j 2^(s_j - r),   out = O / l,
+// codes k~, v~ and scales ks, vs: scores s_j = c ks_j (q . k~_j) in log2 units,
+// and with any reference r
+//   O = sum_j 2^(s_j - r) v_j,   l = sum_j 2^(s_j - r),   out = O / l,
 //   lse = ln 2 (r + log2 l).
-// The bracket is the fp16 operand P of the second product, so r follows
-// max_j s_j + log2 vs_j (an integer, moved only when P could pass 2^15 of
-// fp16's 2^16, then starting again at 2^7; O is scaled by an exact power of
-// two).  Codes are exact in fp16 and so is q after a power-of-two scaling
-// (exact to 2^-25 of the row's largest element), hence both products run
-// on fp16 tensor cores with fp32 sums, and the only rounding of the inner
-// terms is P's, 2^-11.  Neither scale is folded into codes: that would round
-// every key and value.
+// Both products run on the fp16 tensor cores with fp32 sums:
+//   q . k~   codes are exact in fp16, and so is q after a power-of-two scaling (to
+//            2^-25 of its row's largest element); ks_j stays in fp32 and multiplies
+//            the sums, since rounding keys would err by 2^-11 of every score.
+//   P . V    V = v~_j vs_j 2^(6 - e) rounded to fp16 (2^e the power of two above the
+//            tile's largest vs, so a value scale costs the softmax nothing and
+//            no range), P = 2^(s_j - r + e) rounded to fp16.  r follows
+//            max_j s_j + e; it is an integer and moves only when P could pass
+//            2^15 of fp16's 2^16, then starting again at 2^7, and O is scaled by
+//            an exact power of two.
+// So the inner terms take two roundings of 2^-11, everything else is fp32.
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
 // 128 tokens a tile.  Roles (16 warps):
 //   0-7   two softmax groups of 128 threads, a thread per row (TMEM lane)
 //   8-11  converters: raw codes -> fp16 operands in the swizzled layout
-//   12    producer: plans tiles, loads codes and scales (cp.async)
+//   12    producer: plans tiles, loads codes and scales (bulk copies)
 //   13    issues the tensor-core products;  14, 15  load and scale q
 // A pair tile's keys and values serve both groups; single tiles alternate
 // between the groups' own items.  Operands are loaded, converted and used in
 // one order, K0 K1 V0 K2 V1 ..: keys one tile ahead, so that a group's scores
 // are ready while the other group's softmax runs.  Every wait is bounded.
+#include <type_traits>
+
 #include "attention_plan.h"
 #include "paged_rows.cuh"
 #include "tc_primitives.cuh"
@@ -44,7 +49,10 @@ constexpr long long kDrainLimit = 200000000LL;  // ~0.1 s: products in flight af
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: scores (and P) of the groups, then their outputs
 
 constexpr float kScaleFloor = 0x1p-100f;   // value scales below it lose precision, not range
-constexpr float kPeak = 7.f;               // log2 of P's largest bound when the reference moves
+constexpr float kPeak = 7.f;               // log2 of P's largest bound when the reference moves ...
+constexpr float kMost = 32768.f;           // ... which it does when 32 terms of P sum to more than this
+constexpr int kVUp = 6;                    // log2 of what V is multiplied by: its codes reach 448 * 2^6 in fp16
+constexpr float kVDown = 0x1p-6f;
 constexpr float kQUp = 16.f;               // what q is multiplied by before it becomes fp16 ...
 constexpr int kQLow = -4, kQHigh = 11;     // ... when its row's largest element lies in [2^-4, 2^11)
 
@@ -55,7 +63,7 @@ enum { kTileFirst = 4, kTileLast = 8, kTileEnd = 16 };
 // Shared memory: operands first (1024-byte aligned for the swizzle)
 template <int DP>
 struct Layout {
-    static constexpr int kOps = DP == 128 ? 3 : 4;    // fp16 operand ring (K and V tiles)
+    static constexpr int kOps = 3;                    // fp16 operand ring (K and V tiles)
     static constexpr int kRaw = DP == 128 ? 3 : 6;    // ring of tiles as loaded
     static constexpr uint32_t kTileBytes = 128 * DP * 2;
     static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales
@@ -81,7 +89,7 @@ struct Piece {
     int pad;
 };
 struct Tile {
-    int flags, token, piece, pad;   // first token; where its piece is
+    int flags, token, piece, number;   // first token; where its piece is; its place among the CTA's tiles
 };
 
 // Device workspace: where partial results go
@@ -123,11 +131,6 @@ __device__ __forceinline__ uint64_t pack2(float x, float y) {
 __device__ __forceinline__ void unpack2(uint64_t v, float &x, float &y) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -152,6 +155,12 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
     return r;
+}
+
+// e such that every value scale of a tile, given by four partial maxima, is below 2^e.
+__device__ __forceinline__ int scale_exponent(const float (&m)[4]) {
+    const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), kScaleFloor);
+    return min((int)(__float_as_uint(top) >> 23) - 126, 120);
 }
 
 // Bounded wait of a whole warp on one barrier.
@@ -424,9 +433,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     using L = Layout<DP>;
     constexpr int kOps = L::kOps, kRaw = L::kRaw;
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 2 * kRing + 16];
+    __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 6 * kRing + 16];
     __shared__ Piece pieces[2][kPieces];
-    __shared__ __align__(16) Tile ring[kRing];
+    __shared__ __align__(16) Tile ring[3][kRing];   // tiles of the softmax groups; all of them, for the others
     __shared__ __align__(16) float vmax[kScaleSlots][4];
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
@@ -448,9 +457,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     auto raw_empty = [&](uint32_t i) { return bar0 + 8u * (kRaw + i); };
     auto op_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + i); };
     auto op_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + kOps + i); };
-    auto tile_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + i); };
-    auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + kRing + i); };
-    const uint32_t bar1 = bar0 + 8u * (uint32_t)(2 * kRaw + 2 * kOps + 2 * kRing);
+    auto tile_full = [&](int k, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)k * kRing + i); };
+    auto tile_empty = [&](int k, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)(k + 3) * kRing + i); };
+    const uint32_t bar1 = bar0 + 8u * (uint32_t)(2 * kRaw + 2 * kOps + 6 * kRing);
     auto q_full = [&](int i) { return bar1 + 8u * (uint32_t)i; };
     auto q_empty = [&](int i) { return bar1 + 8u * (uint32_t)(2 + i); };
     auto s_full = [&](int i) { return bar1 + 8u * (uint32_t)(4 + i); };
@@ -460,9 +469,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t drain = bar1 + 8u * 12u;
 
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 33), mbar_init(raw_empty(i), 4);
+        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), 4);
         for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), 4), mbar_init(op_empty(i), 1);
-        for (int i = 0; i < kRing; ++i) mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 15);
+        for (int k = 0; k < 3; ++k)
+            for (int i = 0; i < kRing; ++i) mbar_init(tile_full(k, i), 1), mbar_init(tile_empty(k, i), k == 2 ? 7 : 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 4), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
@@ -585,51 +595,50 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             uint32_t raw = 0;                    // operand tiles loaded
             uint32_t ids = kNoChunk, ids_v = kNoChunk;
             bool flagged = false, turn = false;
-            const unsigned char *k_lane = static_cast<const unsigned char *>(c.k) + lane * 16;
-            const unsigned char *v_lane = static_cast<const unsigned char *>(c.v) + lane * 16;
-            // scales: a lane's 16 bytes are tokens 4 (lane & 3) .. of chunk lane / 4
-            const float *ks_lane = c.k_scale + (lane & 3) * 4, *vs_lane = c.v_scale + (lane & 3) * 4;
+            // A tile is loaded in runs of tokens that share a page: lanes 0 .. 7 copy a run of codes
+            // each; with the keys, lanes 8 .. 15 and 16 .. 23 the runs' scales.  (Copies by the warp's
+            // own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
+            const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
             auto load = [&](uint32_t mine, bool is_v) {
                 const uint32_t slot = raw % kRaw;
-                if (!warp_wait(raw_empty(slot), ((raw / kRaw) & 1) ^ 1, abort)) return false;
-                const uint32_t at = base + L::kRawAt + slot * L::kRawBytes + (uint32_t)lane * 16u;
-                const unsigned char *codes = is_v ? v_lane : k_lane;
+                const int i = lane & 7;
+                const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
+                const bool good = i < runs && id < kBadChunk;
                 const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
-#pragma unroll 2
-                for (int ch = 0; ch < 8; ++ch) {
-                    const uint32_t id = __shfl_sync(0xffffffffu, mine, ch);
-                    if (id >= kBadChunk) continue;
-                    const unsigned char *src = codes + (uint64_t)id * (uint32_t)(16 * D);
-                    const uint32_t dst = at + (uint32_t)(ch * 16 * D);
-                    if (D == 128) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) cp_async_16(dst + 512u * i, src + 512 * i, 16);
-                    } else {
-                        for (int i = lane; i < D; i += 32) cp_async_16(dst + 16u * (uint32_t)(i - lane), src + 16 * (i - lane), 16);
-                    }
-                }
-                if (!is_v) {
-                    const uint32_t id = __shfl_sync(0xffffffffu, mine, lane >> 2);
-                    if (id < kBadChunk) {
-                        cp_async_16(at + 128u * DP, ks_lane + (uint64_t)id * 16u, 16);
-                        cp_async_16(at + 128u * DP + 512u, vs_lane + (uint64_t)id * 16u, 16);
-                    }
-                }
-                cp_async_arrive(raw_full(slot));
+                const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
+                if (!warp_wait(raw_empty(slot), ((raw / kRaw) & 1) ^ 1, abort)) return false;
+                const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
                 if (lane == 0) {
                     raw_bad[slot] = (int)bad;
-                    mbar_arrive(raw_full(slot));
+                    mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D : D + 8)));
+                }
+                __syncwarp();
+                if (good && lane < (is_v ? 8 : 24)) {
+                    uint32_t to, bytes;
+                    const unsigned char *src;
+                    if (lane < 8) {
+                        src = static_cast<const unsigned char *>(is_v ? c.v : c.k) + (uint64_t)id * (uint32_t)(16 * D);
+                        to = at + (uint32_t)(i * run * D);
+                        bytes = (uint32_t)(run * D);
+                    } else {
+                        src = reinterpret_cast<const unsigned char *>((lane < 16 ? c.k_scale : c.v_scale) + (uint64_t)id * 16u);
+                        to = at + 128u * DP + (lane < 16 ? 0u : 512u) + (uint32_t)(i * run * 4);
+                        bytes = (uint32_t)(run * 4);
+                    }
+                    bulk_load(to, src, bytes, raw_full(slot));
                 }
                 flagged |= bad != 0;
                 ++raw;
                 return true;
             };
+            uint32_t taken[2] = {0, 0};          // tiles given to the groups
             for (uint32_t g = 0; ok; ++g) {
                 Tile t;
                 t.flags = kTileEnd;
-                t.token = t.piece = t.pad = 0;
+                t.token = t.piece = 0;
+                t.number = (int)g;
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_empty(e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
+                if (!warp_wait(tile_empty(2, e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
                 if (pairing && s0.tiles == 0) {
                     pairing = false;
                     start(s0, 1);
@@ -645,17 +654,34 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     t.flags |= 2;
                     turn = false;
                 }
+                const int mask = (t.flags & kTileEnd) ? 3 : t.flags & 3;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!(mask >> w & 1)) continue;
+                    const uint32_t i = taken[w] % kRing;
+                    if (ok) ok = warp_wait(tile_empty(w, i), ((taken[w] / kRing) & 1) ^ 1, abort);
+                    if (ok && lane == 0) {
+                        ring[w][i] = t;
+                        mbar_arrive(tile_full(w, i));
+                    }
+                    ++taken[w];
+                }
+                if (!ok) break;
                 if (lane == 0) {
-                    ring[e] = t;
-                    mbar_arrive(tile_full(e));
+                    ring[2][e] = t;
+                    mbar_arrive(tile_full(2, e));
                 }
                 if (!(t.flags & kTileEnd) && !load(ids, false)) { ok = false; break; }
                 if (g > 0 && !load(ids_v, true)) { ok = false; break; }
                 if (t.flags & kTileEnd) break;
             }
             if (flagged && lane == 0) atomicOr(c.flags, kFlagBadPage);
-            if (!ok && lane == 0) *abort = 1;
-            cp_async_wait_all();   // nothing may be in flight when the block's memory goes
+            if (!ok) {
+                if (lane == 0) *abort = 1;
+                // copies in flight must land before the block's memory goes
+                for (uint32_t i = raw > (uint32_t)kRaw ? raw - kRaw : 0; i < raw; ++i)
+                    mbar_wait(raw_full(i % kRaw), (i / kRaw) & 1, never, kDrainLimit);
+            }
         } else if (warp == 13) {
             // ------------------------------------------- tensor-core products --
             // the whole warp walks the loop, so that addresses stay warp-uniform; one lane issues
@@ -713,8 +739,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
             };
             int now = kTileEnd;
-            if (wait(tile_full(0), 0)) {
-                now = ring[0].flags;
+            if (wait(tile_full(2, 0), 0)) {
+                now = ring[2][0].flags;
                 if (!(now & kTileEnd)) {
                     for (int w = 0; w < 2 && ok; ++w)
                         if (now >> w & 1) qk(w, 0, now);
@@ -724,8 +750,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             }
             for (uint32_t g = 0; ok && !(now & kTileEnd); ++g) {
                 const uint32_t e = (g + 1) % kRing;
-                if (!wait(tile_full(e), ((g + 1) / kRing) & 1)) break;
-                const int nxt = ring[e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3;
+                if (!wait(tile_full(2, e), ((g + 1) / kRing) & 1)) break;
+                const int nxt = ring[2][e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3;
                 const uint32_t ki = op, vi = op + (next_mask ? 1 : 0);
                 op = vi + 1;
                 // groups that only the next tile uses have their scores first
@@ -740,7 +766,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (!ok) break;
                 commit(op_empty(vi % kOps));
                 if (next_mask) commit(op_empty(ki % kOps));
-                if (lane == 0) mbar_arrive(tile_empty(g % kRing));
+                if (lane == 0) mbar_arrive(tile_empty(2, g % kRing));
                 now = nxt;
             }
             if (!ok) {
@@ -755,15 +781,15 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             bool ok = true;
             for (uint32_t g = 0; ok; ++g) {
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const int flags = ring[e].flags;
+                if (!warp_wait(tile_full(2, e), (g / kRing) & 1, abort)) { ok = false; break; }
+                const int flags = ring[2][e].flags;
                 if (flags & kTileEnd) break;
                 if (flags & kTileFirst) {
                     const int mask = flags & 3, w = mask == 2 ? 1 : 0;
                     const uint32_t n = w ? qc[1] : qc[0];
                     if (mask != 3) {
                         if (!warp_wait(q_empty(w), (n & 1) ^ 1, abort)) { ok = false; break; }
-                        load_q<T, DP>(a, (&pieces[0][0])[ring[e].piece], 0, warp - 14, 2, group,
+                        load_q<T, DP>(a, (&pieces[0][0])[ring[2][e].piece], 0, warp - 14, 2, group,
                                       base + L::kQ + (uint32_t)w * L::kTileBytes,
                                       reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(n & 1) * 128, lane);
                         fence_proxy_async_smem();
@@ -774,7 +800,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     qc[1] += mask >> 1;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tile_empty(e));
+                if (lane == 0) mbar_arrive(tile_empty(2, e));
             }
             if (!ok && lane == 0) *abort = 1;
         } else {
@@ -782,26 +808,42 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const int t = tid - 256;
             const int cpr = D / 16;                      // 16-code chunks of a token
             const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
-            uint32_t op = 0;
+            uint32_t op = 0, key_op = 0;                 // operands; the last key tile's
             bool ok = true;
             // One operand tile.  All loads come first, so that the slot goes back before the
             // decoding.  The lanes of a quarter warp take four chunks each of the lower and the
             // upper 64 columns of an even and an odd row: neither their loads nor their
             // stores (the swizzle takes even chunks of an odd row to odd places) meet in a bank.
-            auto convert = [&](bool is_v, int valid, uint32_t g) {
+            auto convert = [&](bool is_v, int valid, uint32_t g, uint32_t key_v) {
                 if (!warp_wait(op_empty(op % kOps), ((op / kOps) & 1) ^ 1, abort)) return false;
                 const uint32_t slot = op % kRaw;
                 if (!warp_wait(raw_full(slot), (op / kRaw) & 1, abort)) return false;
+                // a value tile needs the scales that all the warps left with its keys
+                if (is_v && !warp_wait(op_full(key_v % kOps), (key_v / kOps) & 1, abort)) return false;
                 const uint32_t src = base + L::kRawAt + slot * L::kRawBytes;
                 const uint32_t dst = base + L::kOp + (op % kOps) * L::kTileBytes;
                 const int bad = raw_bad[slot];
                 const bool whole = valid >= plan::kTile && bad == 0;
-                auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch) {
+                // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
+                // leaves the tile's largest below 2^15
+                const float *vs_row = reinterpret_cast<const float *>(gen + L::kScale) + (g % kScaleSlots) * 256 + 128;
+                float v_unit = 1.f;
+                if (is_v) v_unit = __uint_as_float((uint32_t)(127 + kVUp - scale_exponent(vmax[g % kScaleSlots])) << 23);
+                auto row_factor = [&](uint32_t row, __half2 &hi, __half2 &lo) {
+                    const float f = vs_row[row] * v_unit;
+                    hi = __float2half2_rn(f);
+                    lo = __float2half2_rn(f - __low2float(hi));
+                };
+                auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch, __half2 hi, __half2 lo) {
                     __half2 h[8];
                     decode4<kFormat>(in.x, h[0], h[1]);
                     decode4<kFormat>(in.y, h[2], h[3]);
                     decode4<kFormat>(in.z, h[4], h[5]);
                     decode4<kFormat>(in.w, h[6], h[7]);
+                    if (is_v) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = __hfma2(h[i], hi, __hmul2(h[i], lo));
+                    }
                     const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
                     const uint32_t at = dst + (ch >> 2) * (128u * 128u) + row * 128u, c8 = (ch & 3u) * 2u;
                     st_shared_v4(at + ((c8 ^ (row & 7u)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
@@ -813,7 +855,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 float ks = 0.f, vs = 0.f;
                 if (!is_v && t < valid) {
                     // a token whose value scale (or page) is no number carries its NaN in the key's
-                    // scale alone: where it is masked, P is 0 times the value's
+                    // scale alone: where it is masked, its zero values must not become 0 times NaN
                     const float *rs = reinterpret_cast<const float *>(gen + L::kRawAt + slot * L::kRawBytes + 128 * DP);
                     ks = rs[t] * up;
                     vs = rs[128 + t];
@@ -841,12 +883,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty(slot));
+                    __half2 hi = {}, lo = {};
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) decode_store(in[i], (uint32_t)row[i], (uint32_t)ch[i]);
+                    for (int i = 0; i < kEach; ++i) {
+                        if (is_v && (DP == 64 || (i & 1) == 0)) row_factor((uint32_t)row[i], hi, lo);
+                        decode_store(in[i], (uint32_t)row[i], (uint32_t)ch[i], hi, lo);
+                    }
                 } else {
                     for (int i = t; i < 128 * cpr; i += 128) {
                         const int row = i / cpr;
-                        decode_store(keep(ld_shared_v4(src + (uint32_t)i * 16u), row), (uint32_t)row, (uint32_t)(i - row * cpr));
+                        __half2 hi = {}, lo = {};
+                        if (is_v) row_factor((uint32_t)row, hi, lo);
+                        decode_store(keep(ld_shared_v4(src + (uint32_t)i * 16u), row), (uint32_t)row, (uint32_t)(i - row * cpr), hi, lo);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty(slot));
@@ -869,16 +917,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             int valid = 0;
             for (uint32_t g = 0; ok; ++g) {
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const Tile tile = ring[e];
+                if (!warp_wait(tile_full(2, e), (g / kRing) & 1, abort)) { ok = false; break; }
+                const Tile tile = ring[2][e];
                 const int valid_v = valid;
+                const uint32_t key_v = key_op;
                 if (!(tile.flags & kTileEnd)) {
                     valid = (&pieces[0][0])[tile.piece].len - tile.token;
-                    if (!convert(false, valid, g)) { ok = false; break; }
+                    key_op = op;
+                    if (!convert(false, valid, g, 0)) { ok = false; break; }
                 }
-                if (g > 0 && !convert(true, valid_v, g)) { ok = false; break; }
+                if (g > 0 && !convert(true, valid_v, g - 1, key_v)) { ok = false; break; }
                 if (tile.flags & kTileEnd) break;
-                if (lane == 0) mbar_arrive(tile_empty(e));
+                if (lane == 0) mbar_arrive(tile_empty(2, e));
             }
             if (!ok && lane == 0) *abort = 1;
         }
@@ -887,23 +937,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * (uint32_t)w, my_o = lanes + kColO + 128u * (uint32_t)w;
-        uint32_t tiles_done = 0, pieces_done = 0;
+        uint32_t pieces_done = 0;
         bool ok = true;
         // of the piece
         bool live = false, warp_live = false, rescale_q = false;
         int sees = 0, ctx = 0, blk = 0, m = 0, mt = 0;
         uint64_t word = 0;
         float r = -INFINITY, l = 0.f, lack = 1.f;
-        for (uint32_t g = 0; ok; ++g) {
-            const uint32_t e = g % kRing;
-            if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
-            const Tile tile = ring[e];
+        for (uint32_t n = 0; ok; ++n) {
+            const uint32_t e = n % kRing;
+            if (!warp_wait(tile_full(w, e), (n / kRing) & 1, abort)) { ok = false; break; }
+            const Tile tile = ring[w][e];
             if (tile.flags & kTileEnd) break;
-            if (!(tile.flags >> w & 1)) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tile_empty(e));
-                continue;
-            }
             const Piece &p = (&pieces[0][0])[tile.piece];
             const bool first = tile.flags & kTileFirst, pair = (tile.flags & 3) == 3;
             if (first) {
@@ -935,38 +980,36 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     if (lane == 0) mbar_arrive(q_full(w));
                 }
             }
-            if (!warp_wait(s_full(w), tiles_done & 1, abort)) { ok = false; break; }
-            ++tiles_done;
+            if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
             tc_fence_after();
             if (first) {
                 lack = live ? (reinterpret_cast<const float *>(gen + L::kQScale))[w * 256 + (int)(pieces_done & 1) * 128 + row] : 1.f;
                 rescale_q = __any_sync(0xffffffffu, lack != 1.f);
             }
             if (warp_live) {
-                const uint32_t ss = g % kScaleSlots;
-                const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + ss * 256, *vs = ks + 128;
-                const float4 vm = *reinterpret_cast<const float4 *>(vmax[ss]);
-                const float vt = fmaxf(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), kScaleFloor);
-                const int lv = (int)(__float_as_uint(vt) >> 23) - 126;   // every value scale is below 2^lv
-                // 32 terms whose sum is at most this leave P below 2^15
-                const float most = __uint_as_float((uint32_t)(127 + 15 - lv) << 23);
+                const uint32_t ss = (uint32_t)tile.number % kScaleSlots;
+                const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + ss * 256;
+                const int lv = scale_exponent(vmax[ss]);
+                const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
                 const bool masked = tile.token > ctx - plan::kTile;   // some row does not see some token of this tile
-                float ref = r == -INFINITY ? 0.f : r;
+                float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
                 __syncwarp();
                 // the row's scores 32 columns at a time: holding more of them spills, and with this
                 // much shared memory a spilled register comes back from L2
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t x[32], pr[16], bits = 0xffffffffu;
+                    bool some_hidden = false;
                     tmem_ld32(my_s + 32u * (uint32_t)q, x);
                     if (masked) {
                         const int from_t = tile.token + 32 * q, full = min(max(sees - from_t, 0), 32);
                         bits = full == 32 ? 0xffffffffu : (1u << full) - 1u;
                         const int sh = from_t - ctx;   // block token of the first column
                         if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
+                        some_hidden = __any_sync(0xffffffffu, bits != 0xffffffffu);
                     }
                     tmem_ld_wait32(x);
-                    if (!__any_sync(0xffffffffu, live && bits != 0)) {
+                    if (masked && !__any_sync(0xffffffffu, live && bits != 0)) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pr[i] = 0;
                         tmem_st16(my_s + 16u * (uint32_t)q, pr);
@@ -976,49 +1019,49 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * lack);
                     }
-                    const bool some_hidden = masked && __any_sync(0xffffffffu, bits != 0xffffffffu);
                     // scores in log2 units less `ref2`; those the row does not see -inf
-                    auto four = [&](int i, uint64_t ref2, float (&y)[4]) {
+                    auto four = [&](int i, uint64_t ref2, float (&y)[4], auto hidden) {
                         const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + i);
                         unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pack2(k4.x, k4.y), ref2), y[0], y[1]);
                         unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), pack2(k4.z, k4.w), ref2), y[2], y[3]);
-                        if (some_hidden) {
+                        if constexpr (decltype(hidden)::value) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
                         }
                     };
-                    float s;
-#pragma unroll 1
-                    for (int again = 0;; ++again) {
+                    // the 32 terms, and their sum
+                    auto terms = [&](auto hidden) {
                         const uint64_t ref2 = pack2(-ref, -ref);
-                        uint64_t sum[2] = {0, 0};
+                        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             float y[4];
-                            four(i, ref2, y);
-                            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * q + i);
-                            const uint64_t e0 = pack2(fast_exp2(y[0]), fast_exp2(y[1])), e1 = pack2(fast_exp2(y[2]), fast_exp2(y[3]));
-                            sum[0] = add2(sum[0], e0);
-                            sum[1] = add2(sum[1], e1);
-                            float p0, p1, p2, p3;
-                            unpack2(mul2(e0, pack2(v4.x, v4.y)), p0, p1);
-                            unpack2(mul2(e1, pack2(v4.z, v4.w)), p2, p3);
-                            pr[i >> 1] = half_pair(p0, p1);
-                            pr[(i >> 1) + 1] = half_pair(p2, p3);
+                            four(i, ref2, y, hidden);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
+                            sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
+                            sum[(i >> 1 & 2) + 1] = add2(sum[(i >> 1 & 2) + 1], pack2(y[2], y[3]));
+                            pr[i >> 1] = half_pair(y[0], y[1]);
+                            pr[(i >> 1) + 1] = half_pair(y[2], y[3]);
                         }
                         float s0, s1;
-                        unpack2(add2(sum[0], sum[1]), s0, s1);
-                        s = s0 + s1;
+                        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                        return s0 + s1;
+                    };
+                    float s;
+#pragma unroll 1
+                    for (int again = 0;; ++again) {
+                        s = some_hidden ? terms(std::true_type{}) : terms(std::false_type{});
                         // the reference has to move when a term could pass 2^15 (the sum of 32 says so), or
                         // when there is none yet
-                        const bool moves = live && (s > most || (r == -INFINITY && bits != 0));
+                        const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
                         if (again || !__any_sync(0xffffffffu, moves)) break;
                         float top = -INFINITY;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             float y[4];
-                            four(i, 0, y);
+                            four(i, 0, y, std::true_type{});
                             top = max3(max3(top, y[0], y[1]), y[2], y[3]);
                         }
                         float f = 1.f;
@@ -1028,7 +1071,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             r = r_new;
                             l *= f;
                         }
-                        ref = r == -INFINITY ? 0.f : r;
+                        ref = r == -INFINITY ? 0.f : r - (float)lv;
                         // what is summed so far: the output of earlier tiles (their product has ended, these
                         // scores came after it) and this tile's P
                         if (!first) {
@@ -1057,7 +1100,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             tmem_st16(my_s + 16u * (uint32_t)i, o);
                         }
                     }
-                    l += s;
+                    l = fmaf(s, unit, l);
                     // P's 16 columns lie below the scores still to be read
                     tmem_st16(my_s + 16u * (uint32_t)q, pr);
                 }
@@ -1080,7 +1123,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         out_kind != kContinued ? (p.request < 0 ? place : all + place)
                         : pair ? 2 * all + (int64_t)blockIdx.x * plan::kTileRows + mt
                                : 2 * all + (int64_t)kCtas * plan::kTileRows + ((int64_t)blockIdx.x * 2 + w) * plan::kHalfRows + mt;
-                    const float inv = out_kind == kDirect ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                    const float inv = out_kind == kDirect ? (l == 0.f ? 0.f : kVDown / l) : kVDown;
 #pragma unroll 1
                     for (int q = 0; q * 32 < D; ++q) {
                         uint32_t o[32];
@@ -1102,7 +1145,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
                                 if (32 * q + i >= D) break;
-                                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                *reinterpret_cast<float4 *>(dst + i) =
+                                    make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
                             }
                         }
                         __syncwarp();
@@ -1117,7 +1162,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (lane == 0) mbar_arrive(o_free(w));
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(tile_empty(e));
+            if (lane == 0) mbar_arrive(tile_empty(w, e));
         }
         if (!ok && lane == 0) *abort = 1;
     }

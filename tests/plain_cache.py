@@ -3,8 +3,8 @@ the CPU, with the error bounds the GPU results are held to.
 
 A rounding to a type is off by at most finfo(type).eps / 2 relative.  The
 attention's bound counts the roundings of its definition: the output's own, the
-fp16 rounding of each softmax term times its value scale, and fp32 sums and
-exponentials in between (see ``attention``)."""
+fp16 roundings of each softmax term and of each value with its scale, and fp32
+sums and exponentials in between (see ``attention``)."""
 import math
 
 import torch
@@ -86,9 +86,10 @@ def attention(q, pool, row0, lens, mask="causal", words=None, scale=None):
     With p_j the softmax, A = max_j scale sum_d |q_d k_jd| and n seen tokens:
       scores: fp32 sums of D products and a few fp32 factors, each rounding (or
         truncation inside a tensor-core sum) at most 2^-23 of A: ds = 2 (D + 8) 2^-24 A
-      terms: relative ds + 2^-20 (fp32 exponential) + 2^-11 (fp16 rounding); terms
-        that fp16 holds as subnormals are off by 2^-25 against a largest one of at
-        least 2^7 in units of the largest value scale: 2^-32 n max|v| in all
+      terms: relative ds + 2^-20 (fp32 exponential) + 2^-11 (fp16 rounding of the
+        term) + 2^-11 (fp16 rounding of the value with its scale); terms that fp16
+        holds as subnormals are off by 2^-25 against a largest one of at least 2^6
+        where the values are largest: 2^-30 n max|v| in all
       q of fp16 or bf16 is exact in fp16 after a power-of-two scaling, but for
         elements 2^-14 below the row's largest: 2^-24 max|q| sum_d |k_jd|
       sums: fp32 over n terms in many partial sums: 2^-18
@@ -131,8 +132,8 @@ def attention(q, pool, row0, lens, mask="causal", words=None, scale=None):
             out[r:r + n, g] = o
             lse[r:r + n, g] = torch.logsumexp(s, -1)
             tol_out[r:r + n, g] = (half * o.abs().nan_to_num(0) * (1 + 2.0 ** -8)
-                                   + (2 * ds + 2.0 ** -11 + 2.0 ** -18)[:, None] * spread
-                                   + (sees.sum(1) * 2.0 ** -32 * vmax)[:, None]
+                                   + (2 * ds + 2.0 ** -10 + 2.0 ** -18)[:, None] * spread
+                                   + (sees.sum(1) * 2.0 ** -30 * vmax)[:, None]
                                    + torch.finfo(q.dtype).smallest_normal * torch.finfo(q.dtype).eps / 2)
             tol_lse[r:r + n, g] = ds + 2.0 ** -18 + 2.0 ** -22 * lse[r:r + n, g].abs().nan_to_num(0, posinf=0)
     return out, lse, tol_out, tol_lse
