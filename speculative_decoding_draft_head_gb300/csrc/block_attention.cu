@@ -43,7 +43,7 @@ constexpr int kThreads = 512;
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // tiles planned ahead
 constexpr int kScaleSlots = 4;    // tiles whose scales are held
-constexpr long long kSpinLimit = 4000000000LL;  // ~2 s of clock cycles
+constexpr uint32_t kSpinLimit = 2000000000u;    // ~1 s of clock cycles (below the 32-bit clock's lap)
 constexpr long long kDrainLimit = 200000000LL;  // ~0.1 s: products in flight after a timeout
 
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: scores (and P) of the groups, then their outputs
@@ -163,20 +163,27 @@ __device__ __forceinline__ int scale_exponent(const float (&m)[4]) {
     return min((int)(__float_as_uint(top) >> 23) - 126, 120);
 }
 
-// Bounded wait of a whole warp on one barrier.
+// Bounded wait of a whole warp on one barrier: false when it took longer than
+// about a second or another warp gave up.  (Kept small: it stands in the code
+// some thirty times, and the roles' loops have to stay in the instruction cache
+// together.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    const bool ok = mbar_wait(bar, parity, abort, kSpinLimit);
+    const uint32_t t0 = (uint32_t)clock();
+    bool ok;
+#pragma unroll 1
+    while (!(ok = mbar_try_wait_sleep(bar, parity, 20000u)))
+        if (*abort || (uint32_t)clock() - t0 > kSpinLimit) break;
     return __all_sync(0xffffffffu, ok);
 }
 
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
+// Place in a ring of n slots, with the parity of the lap.
+template <int n>
+struct Place {
+    uint32_t slot, lap;
+    __device__ __forceinline__ void step() {
+        if (++slot == n) slot = 0, lap ^= 1;
+    }
+};
 
 // ------------------------------------------------------------------ the plan --
 // The line as a CTA sees it.
@@ -185,110 +192,134 @@ struct Line {
     int64_t prefix[2], pairs, total;   // units of the prefix's items by class, of all pairs, of all
 };
 
-// Walks one worker's pieces of a class (one warp, all lanes alike).
+// Walks one worker's pieces of a class.  Lives in shared memory and is stepped
+// out of line by the producer warp, all lanes alike: it runs once a piece, and
+// its registers and code would burden the loop over tiles.
 struct Walk {
-    int cls, lane;
-    int64_t u, hi;
-    // the item at the cursor
-    int b, head, k, m, tiles;
-    int64_t start;
-    // 32 requests' sizes, a lane each, from request wb on
-    int wb, w_n, w_len;
-    int64_t w_first;
+    int64_t u, hi, start;             // cursor, end, first unit of the item at the cursor
+    int cls, b, head, k, m, tiles;    // that item: request (-1: the prefix), head, row tile of the class, rows, tiles
+    int wb;                           // 32 requests' sizes from request wb on:
+    int w_n[32], w_len[32], w_first[32];
 
-    __device__ __forceinline__ void window(const AttentionArgs &a, int group, int from) {
-        wb = from;
-        w_n = 0;
+    __device__ __forceinline__ void window(const AttentionArgs &a, int group, int from, int lane) {
+        __syncwarp();
+        int n = 0, len = 0, first = 0;
         if (from + lane < a.rows.B) {
             const Request q = load_request(a, from + lane);
-            w_n = q.len_ok && plan::class_tiles(cls, q.n * group) > 0 ? q.n : 0;
-            w_len = q.len;
-            w_first = q.first;
+            n = q.len_ok && plan::class_tiles(cls, q.n * group) > 0 ? q.n : 0;
+            len = q.len;
+            first = (int)q.first;
         }
+        w_n[lane] = n;
+        w_len[lane] = len;
+        w_first[lane] = first;
+        wb = from;
+        __syncwarp();
     }
     // the next request with items of the class, from b on; false when there is none
-    __device__ __forceinline__ bool seek(const AttentionArgs &a, int group) {
-        while (b < a.rows.B) {
-            if (b >= wb + 32) window(a, group, b);
-            const unsigned with = __ballot_sync(0xffffffffu, w_n > 0) & (0xffffffffu << (b - wb));
+    __device__ __forceinline__ bool seek(const AttentionArgs &a, int group, int lane) {
+        int at = b;
+        while (at < a.rows.B) {
+            if (at >= wb + 32) window(a, group, at, lane);
+            const unsigned with = __ballot_sync(0xffffffffu, w_n[lane] > 0) & (0xffffffffu << (at - wb));
             if (with) {
-                b = wb + __ffs(with) - 1;
-                m = __shfl_sync(0xffffffffu, w_n, b - wb) * group;
-                tiles = plan::token_tiles(__shfl_sync(0xffffffffu, w_len, b - wb));
+                at = wb + __ffs(with) - 1;
+                __syncwarp();
+                b = at;
+                m = w_n[at - wb] * group;
+                tiles = plan::token_tiles(w_len[at - wb]);
+                __syncwarp();
                 return true;
             }
-            b = wb + 32;
+            at = wb + 32;
         }
-        return false;
-    }
-    // from unit `lo` to `to` of the line; own items begin in request b0 at unit own0 of the class's
-    __device__ __forceinline__ void begin(const AttentionArgs &a, const Line &z, int which, int64_t lo, int64_t to, int b0,
-                                          int64_t own0) {
-        cls = which;
-        u = lo;
-        hi = to;
-        wb = -32;
-        w_n = w_len = 0;
-        w_first = 0;
-        b = -1;
-        if (u >= hi) return;
-        int64_t at = cls == plan::kPair ? 0 : z.pairs;
-        if (u - at < z.prefix[cls]) {
-            m = z.prefix_m;
-            tiles = z.prefix_tiles;
-        } else {
-            b = b0;
-            window(a, z.group, b0);
-            if (!seek(a, z.group)) {
-                u = hi;
-                return;
-            }
-            at += z.prefix[cls] + own0;
-        }
-        const int64_t per = plan::head_units(cls, m, tiles), item = plan::item_total(cls, tiles);
-        head = (int)((u - at) / per);
-        k = (int)((u - at - head * per) / item);
-        start = at + head * per + k * item;
-    }
-    __device__ __forceinline__ bool next(const AttentionArgs &a, const Line &z, Piece &p) {
-        while (u < hi) {
-            const int t0 = plan::first_tile(cls, u, start, tiles), t1 = plan::first_tile(cls, hi, start, tiles);
-            const int rt = plan::class_row_tile(cls, m, k);
-            p.tiles = t1 - t0;
-            p.first = t0;
-            p.rows = plan::tile_rows(m, rt);
-            p.m0 = rt * plan::kTileRows;
-            p.head = head;
-            p.request = b;
-            if (b < 0) {
-                p.row_base = 0;
-                p.len = p.ctx = a.prefix_len;
-                p.n = 0;
-            } else {
-                p.row_base = (int)__shfl_sync(0xffffffffu, w_first, b - wb);
-                p.len = __shfl_sync(0xffffffffu, w_len, b - wb);
-                p.n = __shfl_sync(0xffffffffu, w_n, b - wb);
-                p.ctx = p.len - p.n;
-            }
-            p.out = t0 > 0 ? kContinued : (b >= 0 && z.prefix_tiles == 0 && t1 == tiles) ? kDirect : kFirst;
-            p.pad = 0;
-            // the cursor moves to the next item
-            start += plan::item_total(cls, tiles);
-            u = start;
-            if (++k == plan::class_tiles(cls, m)) {
-                k = 0;
-                if (++head == a.cache.n_kv_heads) {
-                    head = 0;
-                    ++b;
-                    if (!seek(a, z.group)) u = hi;
-                }
-            }
-            if (p.tiles > 0) return true;
-        }
-        p.tiles = 0;
+        __syncwarp();
+        b = at;
+        __syncwarp();
         return false;
     }
 };
+// (All lanes store the same values to a walk's fields.)
+
+// from unit `lo` to `to` of the line; own items begin in request b0 at unit own0 of the class's
+__device__ __noinline__ void walk_begin(const AttentionArgs &a, const Line &z, Walk &k, int cls, int64_t lo, int64_t to,
+                                        int b0, int64_t own0, int lane) {
+    __syncwarp();
+    k.cls = cls;
+    k.u = lo;
+    k.hi = to;
+    k.wb = -32;
+    k.b = -1;
+    __syncwarp();
+    if (lo >= to) return;
+    int64_t at = cls == plan::kPair ? 0 : z.pairs;
+    if (lo - at < z.prefix[cls]) {
+        k.m = z.prefix_m;
+        k.tiles = z.prefix_tiles;
+    } else {
+        k.b = b0;
+        k.window(a, z.group, b0, lane);
+        if (!k.seek(a, z.group, lane)) {
+            k.u = to;
+            __syncwarp();
+            return;
+        }
+        at += z.prefix[cls] + own0;
+    }
+    __syncwarp();
+    const int64_t per = plan::head_units(cls, k.m, k.tiles), item = plan::item_total(cls, k.tiles);
+    const int64_t head = (lo - at) / per, t = (lo - at - head * per) / item;
+    k.head = (int)head;
+    k.k = (int)t;
+    k.start = at + head * per + t * item;
+    __syncwarp();
+}
+// the next piece, to `slot`; its tiles, 0 when there is none
+__device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Walk &k, Piece &slot, int lane) {
+    __syncwarp();
+    while (k.u < k.hi) {
+        const int cls = k.cls, b = k.b, m = k.m, tiles = k.tiles, head = k.head, kk = k.k;
+        const int64_t start = k.start;
+        const int t0 = plan::first_tile(cls, k.u, start, tiles), t1 = plan::first_tile(cls, k.hi, start, tiles);
+        const int rt = plan::class_row_tile(cls, m, kk);
+        Piece p;
+        p.tiles = t1 - t0;
+        p.first = t0;
+        p.rows = plan::tile_rows(m, rt);
+        p.m0 = rt * plan::kTileRows;
+        p.head = head;
+        p.request = b;
+        p.row_base = b < 0 ? 0 : k.w_first[b - k.wb];
+        p.len = b < 0 ? a.prefix_len : k.w_len[b - k.wb];
+        p.n = b < 0 ? 0 : k.w_n[b - k.wb];
+        p.ctx = p.len - p.n;
+        p.out = t0 > 0 ? kContinued : (b >= 0 && z.prefix_tiles == 0 && t1 == tiles) ? kDirect : kFirst;
+        p.pad = 0;
+        __syncwarp();
+        // the cursor moves to the next item
+        k.start = k.u = start + plan::item_total(cls, tiles);
+        if (kk + 1 < plan::class_tiles(cls, m)) {
+            k.k = kk + 1;
+        } else {
+            k.k = 0;
+            if (head + 1 < a.cache.n_kv_heads) {
+                k.head = head + 1;
+            } else {
+                k.head = 0;
+                k.b = b + 1;
+                __syncwarp();
+                if (!k.seek(a, z.group, lane)) k.u = k.hi;
+            }
+        }
+        if (p.tiles > 0) {
+            if (lane == 0) slot = p;
+            __syncwarp();
+            return p.tiles;
+        }
+        __syncwarp();
+    }
+    return 0;
+}
 
 // A worker's tiles in order, with the cache places of their tokens.  Places are
 // kept by chunk of 16 tokens (a chunk lies inside one page), as the chunk's
@@ -300,23 +331,11 @@ constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 // one's tiles are taken, hence more than kRing slots).
 constexpr int kPieces = 2 * kRing;
 struct Stream {
-    Walk walk;
-    Piece *slots;             // [kPieces] in shared memory
-    int j, tiles, next_tiles, token, page, off;
-    uint32_t window, count;   // chunk numbers of the current four tiles; pieces begun
+    int j, tiles, next_tiles, token, page, off;   // tile of the piece, its tiles, the next piece's; page and place of a chunk
+    uint32_t window, count;                        // chunk numbers of the current four tiles; pieces begun
 
-    // plans a piece into its slot; its tiles, 0 if there is none
-    __device__ __forceinline__ int plan_piece(const AttentionArgs &a, const Line &z, uint32_t n) {
-        Piece p;
-        walk.next(a, z, p);
-        __syncwarp();
-        if (walk.lane == 0) slots[n % kPieces] = p;
-        __syncwarp();
-        return p.tiles;
-    }
-    __device__ __forceinline__ void load_pages(const AttentionArgs &a, uint32_t n, int t) {
-        const Piece &p = slots[n % kPieces];
-        const int per_page = a.cache.page_size / 16, chunk = (p.first + t) * 8 + walk.lane;
+    __device__ __forceinline__ void load_pages(const AttentionArgs &a, const Piece &p, int t, int lane) {
+        const int per_page = a.cache.page_size / 16, chunk = (p.first + t) * 8 + lane;
         off = -1;
         page = 0;
         if ((int64_t)chunk * 16 < p.len) {
@@ -325,30 +344,24 @@ struct Stream {
             page = p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
         }
     }
-    __device__ __forceinline__ void begin(const AttentionArgs &a, const Line &z, int cls, int64_t lo, int64_t hi, int b0,
-                                          int64_t own0) {
-        walk.begin(a, z, cls, lo, hi, b0, own0);
-        tiles = plan_piece(a, z, count);
-        next_tiles = 0;
-        j = 0;
-        if (tiles) load_pages(a, count, 0);
-    }
     // the next tile (tiles > 0): its chunk numbers in lanes 0 .. 7 (and again in 8 .. 15 and so on)
-    __device__ __forceinline__ uint32_t take(const AttentionArgs &a, const Line &z, Tile &t) {
-        if (j == 0) token = slots[count % kPieces].first * plan::kTile;
+    __device__ __forceinline__ uint32_t take(const AttentionArgs &a, const Line &z, Walk &walk, Piece *slots, Tile &t, int lane) {
         if ((j & 3) == 0) {
             window = off < 0 ? kNoChunk
                              : (page < 0 || page >= a.cache.n_pages)
                                    ? kBadChunk
                                    : (uint32_t)page * (uint32_t)(a.cache.n_kv_heads * (a.cache.page_size / 16)) + (uint32_t)off;
-            if (j + 4 < tiles) {
-                load_pages(a, count, j + 4);
-            } else {
-                next_tiles = plan_piece(a, z, count + 1);
-                if (next_tiles) load_pages(a, count + 1, 0);
+            const Piece *p = slots + count % kPieces;
+            if (j == 0) token = p->first * plan::kTile;
+            int from = j + 4;
+            if (from >= tiles) {
+                p = slots + (count + 1) % kPieces;
+                next_tiles = walk_next(a, z, walk, slots[(count + 1) % kPieces], lane);
+                from = 0;
             }
+            if (from || next_tiles) load_pages(a, *p, from, lane);
         }
-        const uint32_t ids = __shfl_sync(0xffffffffu, window, ((j & 3) << 3) + (walk.lane & 7));
+        const uint32_t ids = __shfl_sync(0xffffffffu, window, ((j & 3) << 3) + (lane & 7));
         t.token = token;
         t.piece = (int)(count % kPieces);
         t.flags = (j == 0 ? kTileFirst : 0) | (j + 1 == tiles ? kTileLast : 0);
@@ -440,6 +453,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
     __shared__ Line line;
+    __shared__ Walk walks[2];
     __shared__ int64_t found_units[3], from_s[3], to_s[3];   // of the workers: pairs, and each group's singles
     __shared__ int found_request[3];
     __shared__ int misc[3];       // abort, a word that stays 0, TMEM address
@@ -580,19 +594,31 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     if (warp >= 8) {
         if (warp == 12) {
             // ------------------------------------------------------ producer --
-            Stream s0, s1;
-            s0.count = s1.count = 0;
-            s0.walk.lane = s1.walk.lane = lane;
-            s0.slots = pieces[0];
-            s1.slots = pieces[1];
-            auto start = [&](Stream &s, int i) {
-                s.begin(a, line, i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i], found_units[i]);
+            // `cur` is the stream whose tile comes next, stream `id` of the two: pairs, then the
+            // first group's singles, are stream 0's, the second group's singles stream 1's
+            Stream cur, oth;
+            cur.count = oth.count = 0;
+            int id = 0;
+            auto start = [&](Stream &s, int k, int i) {
+                walk_begin(a, line, walks[k], i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
+                           found_units[i], lane);
+                s.tiles = walk_next(a, line, walks[k], pieces[k][s.count % kPieces], lane);
+                s.next_tiles = s.j = 0;
+                if (s.tiles) s.load_pages(a, pieces[k][s.count % kPieces], 0, lane);
             };
-            start(s0, 0);
-            start(s1, 2);
-            bool ok = true, pairing = s0.tiles > 0;
-            if (!pairing) start(s0, 1);
-            uint32_t raw = 0;                    // operand tiles loaded
+            bool ok = true, pairing = true;
+            oth.tiles = 0;
+#pragma unroll 1
+            for (int i = 2; i >= 0; i -= 2) {     // the second group's singles, then the pairs
+                start(cur, id = i >> 1, i);
+                if (i == 2) {
+                    const Stream x = cur;
+                    cur = oth;
+                    oth = x;
+                }
+            }
+            Place<kRaw> raw = {0, 0};            // operand tiles loaded
+            uint32_t loaded = 0;
             uint32_t ids = kNoChunk, ids_v = kNoChunk;
             bool flagged = false, turn = false;
             // A tile is loaded in runs of tokens that share a page: lanes 0 .. 7 copy a run of codes
@@ -600,13 +626,13 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             // own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
             const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
             auto load = [&](uint32_t mine, bool is_v) {
-                const uint32_t slot = raw % kRaw;
                 const int i = lane & 7;
                 const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
                 const bool good = i < runs && id < kBadChunk;
                 const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
                 const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
-                if (!warp_wait(raw_empty(slot), ((raw / kRaw) & 1) ^ 1, abort)) return false;
+                const uint32_t slot = raw.slot;
+                if (!warp_wait(raw_empty(slot), raw.lap ^ 1, abort)) return false;
                 const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
                 if (lane == 0) {
                     raw_bad[slot] = (int)bad;
@@ -628,10 +654,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     bulk_load(to, src, bytes, raw_full(slot));
                 }
                 flagged |= bad != 0;
-                ++raw;
+                raw.step();
+                ++loaded;
                 return true;
             };
-            uint32_t taken[2] = {0, 0};          // tiles given to the groups
+            uint32_t taken = 0;                  // tiles given to the groups, modulo 2^16 (a multiple of the ring's laps)
             for (uint32_t g = 0; ok; ++g) {
                 Tile t;
                 t.flags = kTileEnd;
@@ -639,47 +666,49 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 t.number = (int)g;
                 const uint32_t e = g % kRing;
                 if (!warp_wait(tile_empty(2, e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
-                if (pairing && s0.tiles == 0) {
+                if (pairing && cur.tiles == 0) {
                     pairing = false;
-                    start(s0, 1);
+                    start(cur, 0, 1);
                 }
+                if (!pairing && oth.tiles && (cur.tiles == 0 || turn)) {   // the other group's turn
+                    const Stream x = cur;
+                    cur = oth;
+                    oth = x;
+                    id ^= 1;
+                }
+                turn = true;
                 ids_v = ids;
-                if (s0.tiles && (pairing || !turn || !s1.tiles)) {
-                    ids = s0.take(a, line, t);
-                    t.flags |= pairing ? 3 : 1;
-                    turn = true;
-                } else if (s1.tiles) {
-                    ids = s1.take(a, line, t);
-                    t.piece += kPieces;
-                    t.flags |= 2;
-                    turn = false;
+                if (cur.tiles) {
+                    ids = cur.take(a, line, walks[id], pieces[id], t, lane);
+                    t.flags |= pairing ? 3 : 1 << id;
+                    t.piece += id * kPieces;
                 }
                 const int mask = (t.flags & kTileEnd) ? 3 : t.flags & 3;
-#pragma unroll
+#pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     if (!(mask >> w & 1)) continue;
-                    const uint32_t i = taken[w] % kRing;
-                    if (ok) ok = warp_wait(tile_empty(w, i), ((taken[w] / kRing) & 1) ^ 1, abort);
+                    const uint32_t n = w ? taken >> 16 : taken & 0xffffu, i = n % kRing;
+                    if (ok) ok = warp_wait(tile_empty(w, i), ((n / kRing) & 1) ^ 1, abort);
                     if (ok && lane == 0) {
                         ring[w][i] = t;
                         mbar_arrive(tile_full(w, i));
                     }
-                    ++taken[w];
+                    taken = w ? taken + 0x10000u : (taken & 0xffff0000u) | ((taken + 1) & 0xffffu);
                 }
                 if (!ok) break;
                 if (lane == 0) {
                     ring[2][e] = t;
                     mbar_arrive(tile_full(2, e));
                 }
-                if (!(t.flags & kTileEnd) && !load(ids, false)) { ok = false; break; }
-                if (g > 0 && !load(ids_v, true)) { ok = false; break; }
+#pragma unroll 1
+                for (int v = (t.flags & kTileEnd) ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v) ok = load(v ? ids_v : ids, v);
                 if (t.flags & kTileEnd) break;
             }
             if (flagged && lane == 0) atomicOr(c.flags, kFlagBadPage);
             if (!ok) {
                 if (lane == 0) *abort = 1;
                 // copies in flight must land before the block's memory goes
-                for (uint32_t i = raw > (uint32_t)kRaw ? raw - kRaw : 0; i < raw; ++i)
+                for (uint32_t i = loaded > (uint32_t)kRaw ? loaded - kRaw : 0; i < loaded; ++i)
                     mbar_wait(raw_full(i % kRaw), (i / kRaw) & 1, never, kDrainLimit);
             }
         } else if (warp == 13) {
@@ -690,7 +719,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const uint32_t id_qk = idesc_f16_f32(128, 128, false), id_pv = idesc_f16_f32(128, D, true);
             constexpr uint32_t kAtom = 128 * 128;  // bytes of a 64-column atom of a 128-row tile
             const int k_steps = D / 16;
-            uint32_t op = 0, pc[2] = {0, 0}, qc[2] = {0, 0}, fc[2] = {0, 0};  // operands; P's, q's, results of the groups
+            Place<kOps> op = {0, 0};
+            uint32_t laps = 0;      // bits: parity of the next q, P and result of the groups; 6, 7: a group has had a result
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (ok) ok = warp_wait(bar, parity, abort);
@@ -700,73 +730,69 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             auto commit = [&](uint32_t bar) {
                 if (leader) umma_commit(bar);
             };
-            auto op_ready = [&](uint32_t i) { return wait(op_full(i % kOps), (i / kOps) & 1); };
             // scores of group w for a tile: waits for the item's q with its first tile, gives it back with its last
-            auto qk = [&](int w, uint32_t i, int flags) {
+            auto qk = [&](int w, Place<kOps> k, int flags) {
                 if (flags & kTileFirst) {
-                    if (!wait(q_full(w), qc[w] & 1)) return;
-                    ++qc[w];
+                    if (!wait(q_full(w), laps >> w & 1)) return;
+                    laps ^= 1u << w;
                 }
-                if (!op_ready(i)) return;
+                if (!wait(op_full(k.slot), k.lap)) return;
                 const uint32_t qa = (base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16;
-                const uint32_t ka = (base + L::kOp + (i % kOps) * L::kTileBytes) >> 4 | 1u << 16;
+                const uint32_t ka = (base + L::kOp + k.slot * L::kTileBytes) >> 4 | 1u << 16;
                 const uint32_t d = tmem + kColS + 128u * (uint32_t)w;
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t off = ((uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32u) >> 4;
-                        if (k < k_steps) umma_bf16_w(d, qa + off, ka + off, hi_desc, id_qk, k > 0);
+                    for (int i = 0; i < DP / 16; ++i) {
+                        const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
+                        if (i < k_steps) umma_bf16_w(d, qa + off, ka + off, hi_desc, id_qk, i > 0);
                     }
                     umma_commit(s_full(w));
                     if (flags & kTileLast) umma_commit(q_empty(w));
                 }
             };
-            auto pv = [&](int w, uint32_t i, int flags) {
+            auto pv = [&](int w, Place<kOps> v, int flags) {
                 if (flags & kTileFirst) {
-                    if (fc[w] > 0 && !wait(o_free(w), (fc[w] - 1) & 1)) return;
-                    ++fc[w];
+                    if ((laps >> (6 + w) & 1) && !wait(o_free(w), (laps >> (4 + w) & 1) ^ 1)) return;
+                    laps = (laps ^ 1u << (4 + w)) | 1u << (6 + w);
                 }
-                if (!wait(p_ready(w), pc[w] & 1)) return;
-                ++pc[w];
-                const uint32_t va = (base + L::kOp + (i % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
+                if (!wait(p_ready(w), laps >> (2 + w) & 1)) return;
+                laps ^= 1u << (2 + w);
+                const uint32_t va = (base + L::kOp + v.slot * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
                 const uint32_t d = tmem + kColO + 128u * (uint32_t)w, pa = tmem + kColS + 128u * (uint32_t)w;
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_bf16_ts(d, pa + 8u * (uint32_t)k, va + (uint32_t)k * (2048u >> 4), hi_desc, id_pv,
-                                     k > 0 ? 1u : (flags & kTileFirst) ? 0u : 1u);
+                    for (int i = 0; i < 8; ++i)
+                        umma_bf16_ts(d, pa + 8u * (uint32_t)i, va + (uint32_t)i * (2048u >> 4), hi_desc, id_pv,
+                                     i > 0 ? 1u : (flags & kTileFirst) ? 0u : 1u);
                     if (flags & kTileLast) umma_commit(o_full(w));
                 }
             };
-            int now = kTileEnd;
-            if (wait(tile_full(2, 0), 0)) {
-                now = ring[2][0].flags;
-                if (!(now & kTileEnd)) {
-                    for (int w = 0; w < 2 && ok; ++w)
-                        if (now >> w & 1) qk(w, 0, now);
-                    commit(op_empty(0));
-                    op = 1;
-                }
-            }
+            // Step g: the scores of tile g as soon as a group is free for them (those of the groups that
+            // tile g - 1 does not use before tile g - 1's P is waited for), and tile g - 1's output.
+            int now = 0;
+#pragma unroll 1
             for (uint32_t g = 0; ok && !(now & kTileEnd); ++g) {
-                const uint32_t e = (g + 1) % kRing;
-                if (!wait(tile_full(2, e), ((g + 1) / kRing) & 1)) break;
-                const int nxt = ring[2][e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3;
-                const uint32_t ki = op, vi = op + (next_mask ? 1 : 0);
-                op = vi + 1;
-                // groups that only the next tile uses have their scores first
-                for (int w = 0; w < 2 && ok; ++w)
-                    if ((next_mask & ~now) >> w & 1) qk(w, ki, nxt);
-                if (!ok || !op_ready(vi)) break;
-                for (int w = 0; w < 2 && ok; ++w) {
-                    if (!(now >> w & 1)) continue;
-                    pv(w, vi, now);
-                    if (ok && (next_mask >> w & 1)) qk(w, ki, nxt);
+                const uint32_t e = g % kRing;
+                if (!wait(tile_full(2, e), (g / kRing) & 1)) break;
+                const int nxt = ring[2][e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
+                const Place<kOps> ki = op;
+                if (next_mask) op.step();
+                const Place<kOps> vi = op;
+                if (mask) op.step();
+                // passes: 0 and 1 the early scores of the groups, 2 and 3 their outputs and later scores
+#pragma unroll 1
+                for (int i = 0; i < 4 && ok; ++i) {
+                    const int w = i & 1, has = mask >> w & 1, late = i >> 1;
+                    if (i == 2 && mask && !wait(op_full(vi.slot), vi.lap)) break;
+                    if (late && has) pv(w, vi, now);
+                    if (ok && (next_mask >> w & 1) && has == late) qk(w, ki, nxt);
                 }
                 if (!ok) break;
-                commit(op_empty(vi % kOps));
-                if (next_mask) commit(op_empty(ki % kOps));
-                if (lane == 0) mbar_arrive(tile_empty(2, g % kRing));
+                if (mask) {
+                    commit(op_empty(vi.slot));
+                    if (lane == 0) mbar_arrive(tile_empty(2, (g - 1) % kRing));
+                }
+                if (next_mask) commit(op_empty(ki.slot));
                 now = nxt;
             }
             if (!ok) {
@@ -808,20 +834,21 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const int t = tid - 256;
             const int cpr = D / 16;                      // 16-code chunks of a token
             const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
-            uint32_t op = 0, key_op = 0;                 // operands; the last key tile's
+            Place<kOps> op = {0, 0}, key = {0, 0};       // operands; the last key tile's
+            Place<kRaw> raw = {0, 0};
             bool ok = true;
             // One operand tile.  All loads come first, so that the slot goes back before the
             // decoding.  The lanes of a quarter warp take four chunks each of the lower and the
             // upper 64 columns of an even and an odd row: neither their loads nor their
             // stores (the swizzle takes even chunks of an odd row to odd places) meet in a bank.
-            auto convert = [&](bool is_v, int valid, uint32_t g, uint32_t key_v) {
-                if (!warp_wait(op_empty(op % kOps), ((op / kOps) & 1) ^ 1, abort)) return false;
-                const uint32_t slot = op % kRaw;
-                if (!warp_wait(raw_full(slot), (op / kRaw) & 1, abort)) return false;
+            auto convert = [&](bool is_v, int valid, uint32_t g, Place<kOps> key_v) {
+                if (!warp_wait(op_empty(op.slot), op.lap ^ 1, abort)) return false;
+                const uint32_t slot = raw.slot;
+                if (!warp_wait(raw_full(slot), raw.lap, abort)) return false;
                 // a value tile needs the scales that all the warps left with its keys
-                if (is_v && !warp_wait(op_full(key_v % kOps), (key_v / kOps) & 1, abort)) return false;
+                if (is_v && !warp_wait(op_full(key_v.slot), key_v.lap, abort)) return false;
                 const uint32_t src = base + L::kRawAt + slot * L::kRawBytes;
-                const uint32_t dst = base + L::kOp + (op % kOps) * L::kTileBytes;
+                const uint32_t dst = base + L::kOp + op.slot * L::kTileBytes;
                 const int bad = raw_bad[slot];
                 const bool whole = valid >= plan::kTile && bad == 0;
                 // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
@@ -862,32 +889,37 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     if ((bad >> (t >> 4) & 1) || !(vs <= 3.4028235e38f)) ks = __int_as_float(0x7fffffff), vs = 0.f;
                 }
                 if (D == DP) {
-                    constexpr int kEach = DP / 16;
-                    uint4 in[kEach];
-                    int row[kEach], ch[kEach];
+                    constexpr int kEach = DP / 32;
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        uint4 in[kEach];
+                        int row[kEach], ch[kEach];
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) {
-                        if constexpr (DP == 128) {
-                            const int odd = t >> 2 & 1;
-                            row[i] = 2 * ((t >> 3) + 16 * (i >> 1)) + odd;
-                            ch[i] = (t & 3) + 4 * (odd ^ (i & 1));
-                        } else {
-                            row[i] = (t >> 2) + 32 * i;
-                            ch[i] = t & 3;
+                        for (int i = 0; i < kEach; ++i) {
+                            if constexpr (DP == 128) {
+                                const int odd = t >> 2 & 1;
+                                row[i] = 2 * ((t >> 3) + 16 * (2 * part + (i >> 1))) + odd;
+                                ch[i] = (t & 3) + 4 * (odd ^ (i & 1));
+                            } else {
+                                row[i] = (t >> 2) + 32 * (2 * part + i);
+                                ch[i] = t & 3;
+                            }
+                            in[i] = ld_shared_v4(src + (uint32_t)(row[i] * (DP / 16) + ch[i]) * 16u);
                         }
-                        in[i] = ld_shared_v4(src + (uint32_t)(row[i] * (DP / 16) + ch[i]) * 16u);
-                    }
-                    if (!whole) {
+                        if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < kEach; ++i) in[i] = keep(in[i], row[i]);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(raw_empty(slot));
-                    __half2 hi = {}, lo = {};
+                            for (int i = 0; i < kEach; ++i) in[i] = keep(in[i], row[i]);
+                        }
+                        if (part == 1) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(raw_empty(slot));
+                        }
+                        __half2 hi = {}, lo = {};
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) {
-                        if (is_v && (DP == 64 || (i & 1) == 0)) row_factor((uint32_t)row[i], hi, lo);
-                        decode_store(in[i], (uint32_t)row[i], (uint32_t)ch[i], hi, lo);
+                        for (int i = 0; i < kEach; ++i) {
+                            if (is_v && (DP == 64 || (i & 1) == 0)) row_factor((uint32_t)row[i], hi, lo);
+                            decode_store(in[i], (uint32_t)row[i], (uint32_t)ch[i], hi, lo);
+                        }
                     }
                 } else {
                     for (int i = t; i < 128 * cpr; i += 128) {
@@ -910,8 +942,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(op_full(op % kOps));
-                ++op;
+                if (lane == 0) mbar_arrive(op_full(op.slot));
+                op.step();
+                raw.step();
                 return true;
             };
             int valid = 0;
@@ -920,13 +953,16 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (!warp_wait(tile_full(2, e), (g / kRing) & 1, abort)) { ok = false; break; }
                 const Tile tile = ring[2][e];
                 const int valid_v = valid;
-                const uint32_t key_v = key_op;
-                if (!(tile.flags & kTileEnd)) {
+                const bool end = tile.flags & kTileEnd;
+                const Place<kOps> key_v = key;
+                if (!end) {
                     valid = (&pieces[0][0])[tile.piece].len - tile.token;
-                    key_op = op;
-                    if (!convert(false, valid, g, 0)) { ok = false; break; }
+                    key = op;
                 }
-                if (g > 0 && !convert(true, valid_v, g - 1, key_v)) { ok = false; break; }
+#pragma unroll 1
+                for (int v = end ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v)
+                    ok = convert(v, v ? valid_v : valid, v ? g - 1 : g, key_v);
+                if (!ok) break;
                 if (tile.flags & kTileEnd) break;
                 if (lane == 0) mbar_arrive(tile_empty(2, e));
             }
