@@ -42,7 +42,7 @@ using namespace tc;
 constexpr int kThreads = 512;
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // tiles planned ahead
-constexpr int kScaleSlots = 4;    // tiles whose scales are held
+constexpr int kScaleSlots = 4;    // tiles of a group whose key scales are held
 constexpr uint32_t kSpinLimit = 2000000000u;    // ~1 s of clock cycles (below the 32-bit clock's lap)
 constexpr long long kDrainLimit = 200000000LL;  // ~0.1 s: products in flight after a timeout
 
@@ -66,12 +66,12 @@ struct Layout {
     static constexpr int kOps = 3;                    // fp16 operand ring (K and V tiles)
     static constexpr int kRaw = DP == 128 ? 3 : 6;    // ring of tiles as loaded
     static constexpr uint32_t kTileBytes = 128 * DP * 2;
-    static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales
+    static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales, with the values theirs
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kOp = kQ + 2 * kTileBytes;
     static constexpr uint32_t kRawAt = kOp + kOps * kTileBytes;
-    static constexpr uint32_t kScale = kRawAt + kRaw * kRawBytes;        // [slots][ks 128, vs 128]
-    static constexpr uint32_t kQScale = kScale + kScaleSlots * 1024;     // [groups][2 pieces][128]
+    static constexpr uint32_t kScale = kRawAt + kRaw * kRawBytes;        // [groups][slots][128] key scales
+    static constexpr uint32_t kQScale = kScale + 2 * kScaleSlots * 512;  // [groups][2 pieces][128]
     static constexpr uint32_t kBytes = kQScale + 2048 + 1024;            // + alignment slack
 };
 
@@ -89,7 +89,7 @@ struct Piece {
     int pad;
 };
 struct Tile {
-    int flags, token, piece, number;   // first token; where its piece is; its place among the CTA's tiles
+    int flags, token, piece, pad;   // first token; where its piece is
 };
 
 // Device workspace: where partial results go
@@ -157,10 +157,19 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     return r;
 }
 
-// e such that every value scale of a tile, given by four partial maxima, is below 2^e.
-__device__ __forceinline__ int scale_exponent(const float (&m)[4]) {
-    const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), kScaleFloor);
-    return min((int)(__float_as_uint(top) >> 23) - 126, 120);
+// e such that every value scale of a tile is below 2^e: `vs` are the tile's 128
+// scales in shared memory (16-byte aligned), of which the first `valid` exist
+// except for the 16-token chunks in `bad`.  The whole warp, all lanes alike.
+__device__ __forceinline__ int scale_exponent(const float *vs, int valid, int bad, int lane) {
+    const float4 v = *reinterpret_cast<const float4 *>(vs + 4 * lane);
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    float top = kScaleFloor;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * lane + i < valid && x[i] <= 3.4028235e38f) top = fmaxf(top, x[i]);
+    if (bad >> (lane >> 2) & 1) top = kScaleFloor;
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    return min((int)(bits >> 23) - 126, 120);
 }
 
 // Bounded wait of a whole warp on one barrier: false when it took longer than
@@ -447,9 +456,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     constexpr int kOps = L::kOps, kRaw = L::kRaw;
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 6 * kRing + 16];
+    __shared__ int group_pieces[2][kRing];          // pieces of the softmax groups: slot, flags
     __shared__ Piece pieces[2][kPieces];
-    __shared__ __align__(16) Tile ring[3][kRing];   // tiles of the softmax groups; all of them, for the others
-    __shared__ __align__(16) float vmax[kScaleSlots][4];
+    __shared__ __align__(16) Tile ring[kRing];      // tiles, for the other roles
+    __shared__ int exponents[2][kScaleSlots];       // of the value scales of the groups' tiles
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
     __shared__ Line line;
@@ -471,8 +481,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     auto raw_empty = [&](uint32_t i) { return bar0 + 8u * (kRaw + i); };
     auto op_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + i); };
     auto op_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + kOps + i); };
-    auto tile_full = [&](int k, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)k * kRing + i); };
-    auto tile_empty = [&](int k, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)(k + 3) * kRing + i); };
+    auto piece_full = [&](int w, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)w * kRing + i); };
+    auto piece_empty = [&](int w, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)(w + 2) * kRing + i); };
+    auto tile_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 4 * kRing + i); };
+    auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 5 * kRing + i); };
     const uint32_t bar1 = bar0 + 8u * (uint32_t)(2 * kRaw + 2 * kOps + 6 * kRing);
     auto q_full = [&](int i) { return bar1 + 8u * (uint32_t)i; };
     auto q_empty = [&](int i) { return bar1 + 8u * (uint32_t)(2 + i); };
@@ -485,8 +497,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     if (tid == 0) {
         for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), 4);
         for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), 4), mbar_init(op_empty(i), 1);
-        for (int k = 0; k < 3; ++k)
-            for (int i = 0; i < kRing; ++i) mbar_init(tile_full(k, i), 1), mbar_init(tile_empty(k, i), k == 2 ? 7 : 4);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 7);
+            for (int w = 0; w < 2; ++w) mbar_init(piece_full(w, i), 1), mbar_init(piece_empty(w, i), 4);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 4), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
@@ -622,7 +636,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             uint32_t ids = kNoChunk, ids_v = kNoChunk;
             bool flagged = false, turn = false;
             // A tile is loaded in runs of tokens that share a page: lanes 0 .. 7 copy a run of codes
-            // each; with the keys, lanes 8 .. 15 and 16 .. 23 the runs' scales.  (Copies by the warp's
+            // each, lanes 8 .. 15 (with the keys) and 16 .. 23 the runs' scales.  (Copies by the warp's
             // own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
             const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
             auto load = [&](uint32_t mine, bool is_v) {
@@ -636,10 +650,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
                 if (lane == 0) {
                     raw_bad[slot] = (int)bad;
-                    mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D : D + 8)));
+                    mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D + 4 : D + 8)));
                 }
                 __syncwarp();
-                if (good && lane < (is_v ? 8 : 24)) {
+                if (good && lane < 24 && !(is_v && (lane & 8))) {
                     uint32_t to, bytes;
                     const unsigned char *src;
                     if (lane < 8) {
@@ -658,14 +672,13 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 ++loaded;
                 return true;
             };
-            uint32_t taken = 0;                  // tiles given to the groups, modulo 2^16 (a multiple of the ring's laps)
+            uint32_t taken = 0;                  // pieces given to the groups, modulo 2^16 (a multiple of the ring's laps)
             for (uint32_t g = 0; ok; ++g) {
                 Tile t;
                 t.flags = kTileEnd;
-                t.token = t.piece = 0;
-                t.number = (int)g;
+                t.token = t.piece = t.pad = 0;
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_empty(2, e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
+                if (!warp_wait(tile_empty(e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
                 if (pairing && cur.tiles == 0) {
                     pairing = false;
                     start(cur, 0, 1);
@@ -683,22 +696,23 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     t.flags |= pairing ? 3 : 1 << id;
                     t.piece += id * kPieces;
                 }
-                const int mask = (t.flags & kTileEnd) ? 3 : t.flags & 3;
+                // a new piece (or the end) is told to the groups it is for
+                const int mask = (t.flags & kTileEnd) ? 3 : (t.flags & kTileFirst) ? t.flags & 3 : 0;
 #pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     if (!(mask >> w & 1)) continue;
                     const uint32_t n = w ? taken >> 16 : taken & 0xffffu, i = n % kRing;
-                    if (ok) ok = warp_wait(tile_empty(w, i), ((n / kRing) & 1) ^ 1, abort);
+                    if (ok) ok = warp_wait(piece_empty(w, i), ((n / kRing) & 1) ^ 1, abort);
                     if (ok && lane == 0) {
-                        ring[w][i] = t;
-                        mbar_arrive(tile_full(w, i));
+                        group_pieces[w][i] = t.piece | t.flags << 16;
+                        mbar_arrive(piece_full(w, i));
                     }
                     taken = w ? taken + 0x10000u : (taken & 0xffff0000u) | ((taken + 1) & 0xffffu);
                 }
                 if (!ok) break;
                 if (lane == 0) {
-                    ring[2][e] = t;
-                    mbar_arrive(tile_full(2, e));
+                    ring[e] = t;
+                    mbar_arrive(tile_full(e));
                 }
 #pragma unroll 1
                 for (int v = (t.flags & kTileEnd) ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v) ok = load(v ? ids_v : ids, v);
@@ -773,8 +787,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll 1
             for (uint32_t g = 0; ok && !(now & kTileEnd); ++g) {
                 const uint32_t e = g % kRing;
-                if (!wait(tile_full(2, e), (g / kRing) & 1)) break;
-                const int nxt = ring[2][e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
+                if (!wait(tile_full(e), (g / kRing) & 1)) break;
+                const int nxt = ring[e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
                 const Place<kOps> ki = op;
                 if (next_mask) op.step();
                 const Place<kOps> vi = op;
@@ -790,7 +804,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (!ok) break;
                 if (mask) {
                     commit(op_empty(vi.slot));
-                    if (lane == 0) mbar_arrive(tile_empty(2, (g - 1) % kRing));
+                    if (lane == 0) mbar_arrive(tile_empty((g - 1) % kRing));
                 }
                 if (next_mask) commit(op_empty(ki.slot));
                 now = nxt;
@@ -807,15 +821,15 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             bool ok = true;
             for (uint32_t g = 0; ok; ++g) {
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(2, e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const int flags = ring[2][e].flags;
+                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
+                const int flags = ring[e].flags;
                 if (flags & kTileEnd) break;
                 if (flags & kTileFirst) {
                     const int mask = flags & 3, w = mask == 2 ? 1 : 0;
                     const uint32_t n = w ? qc[1] : qc[0];
                     if (mask != 3) {
                         if (!warp_wait(q_empty(w), (n & 1) ^ 1, abort)) { ok = false; break; }
-                        load_q<T, DP>(a, (&pieces[0][0])[ring[2][e].piece], 0, warp - 14, 2, group,
+                        load_q<T, DP>(a, (&pieces[0][0])[ring[e].piece], 0, warp - 14, 2, group,
                                       base + L::kQ + (uint32_t)w * L::kTileBytes,
                                       reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(n & 1) * 128, lane);
                         fence_proxy_async_smem();
@@ -826,7 +840,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     qc[1] += mask >> 1;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tile_empty(2, e));
+                if (lane == 0) mbar_arrive(tile_empty(e));
             }
             if (!ok && lane == 0) *abort = 1;
         } else {
@@ -834,30 +848,29 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const int t = tid - 256;
             const int cpr = D / 16;                      // 16-code chunks of a token
             const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
-            Place<kOps> op = {0, 0}, key = {0, 0};       // operands; the last key tile's
+            Place<kOps> op = {0, 0};
             Place<kRaw> raw = {0, 0};
+            uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
             bool ok = true;
-            // One operand tile.  All loads come first, so that the slot goes back before the
-            // decoding.  The lanes of a quarter warp take four chunks each of the lower and the
-            // upper 64 columns of an even and an odd row: neither their loads nor their
+            // One operand tile.  The lanes of a quarter warp take four chunks each of the lower and
+            // the upper 64 columns of an even and an odd row: neither their loads nor their
             // stores (the swizzle takes even chunks of an odd row to odd places) meet in a bank.
-            auto convert = [&](bool is_v, int valid, uint32_t g, Place<kOps> key_v) {
+            auto convert = [&](bool is_v, int valid, int mask) {
                 if (!warp_wait(op_empty(op.slot), op.lap ^ 1, abort)) return false;
                 const uint32_t slot = raw.slot;
                 if (!warp_wait(raw_full(slot), raw.lap, abort)) return false;
-                // a value tile needs the scales that all the warps left with its keys
-                if (is_v && !warp_wait(op_full(key_v.slot), key_v.lap, abort)) return false;
                 const uint32_t src = base + L::kRawAt + slot * L::kRawBytes;
                 const uint32_t dst = base + L::kOp + op.slot * L::kTileBytes;
                 const int bad = raw_bad[slot];
                 const bool whole = valid >= plan::kTile && bad == 0;
+                const float *raw_scale = reinterpret_cast<const float *>(gen + L::kRawAt + slot * L::kRawBytes + 128 * DP);
+                const int exponent = scale_exponent(raw_scale + 128, valid, bad, lane);
                 // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
                 // leaves the tile's largest below 2^15
-                const float *vs_row = reinterpret_cast<const float *>(gen + L::kScale) + (g % kScaleSlots) * 256 + 128;
-                float v_unit = 1.f;
-                if (is_v) v_unit = __uint_as_float((uint32_t)(127 + kVUp - scale_exponent(vmax[g % kScaleSlots])) << 23);
-                auto row_factor = [&](uint32_t row, __half2 &hi, __half2 &lo) {
-                    const float f = vs_row[row] * v_unit;
+                const float v_unit = __uint_as_float((uint32_t)(127 + kVUp - exponent) << 23);
+                auto there = [&](int row) { return whole || (row < valid && !(bad >> (row >> 4) & 1)); };
+                auto row_factor = [&](int row, __half2 &hi, __half2 &lo) {
+                    const float v = raw_scale[128 + row], f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
                     hi = __float2half2_rn(f);
                     lo = __float2half2_rn(f - __low2float(hi));
                 };
@@ -876,69 +889,68 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     st_shared_v4(at + ((c8 ^ (row & 7u)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
                     st_shared_v4(at + (((c8 + 1u) ^ (row & 7u)) << 4), make_uint4(u[4], u[5], u[6], u[7]));
                 };
-                auto keep = [&](uint4 in, int row) {   // nothing of a token that is not there
-                    return row < valid && !(bad >> (row >> 4) & 1) ? in : make_uint4(0, 0, 0, 0);
+                // nothing of a token that is not there
+                auto load = [&](int row, int ch, int width) {
+                    const uint4 in = ld_shared_v4(src + (uint32_t)(row * width + ch) * 16u);
+                    return there(row) ? in : make_uint4(0, 0, 0, 0);
                 };
-                float ks = 0.f, vs = 0.f;
-                if (!is_v && t < valid) {
-                    // a token whose value scale (or page) is no number carries its NaN in the key's
-                    // scale alone: where it is masked, its zero values must not become 0 times NaN
-                    const float *rs = reinterpret_cast<const float *>(gen + L::kRawAt + slot * L::kRawBytes + 128 * DP);
-                    ks = rs[t] * up;
-                    vs = rs[128 + t];
-                    if ((bad >> (t >> 4) & 1) || !(vs <= 3.4028235e38f)) ks = __int_as_float(0x7fffffff), vs = 0.f;
+                if (!is_v) {
+                    // the tile's key scales (of scores in log2 units), for the softmax groups; a token whose
+                    // value scale (or page) is no number carries its NaN in the key's alone: where it is
+                    // masked, its zero values must not become 0 times NaN
+                    float ks = 0.f;
+                    if (t < valid)
+                        ks = there(t) && raw_scale[128 + t] <= 3.4028235e38f ? raw_scale[t] * up : __int_as_float(0x7fffffff);
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!(mask >> w & 1)) continue;
+                        const uint32_t i = (group_tiles >> (16 * w)) % kScaleSlots;
+                        reinterpret_cast<float *>(gen + L::kScale)[(w * kScaleSlots + i) * 128 + t] = ks;
+                        if (t == 0) exponents[w][i] = exponent;
+                    }
+                    // (counts of 16 bits: the carry of the lower is kept out of the upper)
+                    group_tiles = ((group_tiles + (mask & 1)) & 0xffffu) | ((group_tiles & 0xffff0000u) + ((uint32_t)(mask >> 1) << 16));
                 }
                 if (D == DP) {
-                    constexpr int kEach = DP / 32;
+                    // a row (or two) at a time, the next one's loads under the decoding
+                    constexpr int kRows = DP == 128 ? 4 : 2, kEach = 2;   // steps; 16-code chunks of a step
+                    const int odd = t >> 2 & 1;
+                    auto row_of = [&](int step, int i) {
+                        return DP == 128 ? 2 * ((t >> 3) + 16 * step) + odd : (t >> 2) + 32 * (2 * step + i);
+                    };
+                    auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
+                    uint4 in[kEach];
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) in[i] = load(row_of(0, i), chunk_of(i), DP / 16);
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        uint4 in[kEach];
-                        int row[kEach], ch[kEach];
-#pragma unroll
-                        for (int i = 0; i < kEach; ++i) {
-                            if constexpr (DP == 128) {
-                                const int odd = t >> 2 & 1;
-                                row[i] = 2 * ((t >> 3) + 16 * (2 * part + (i >> 1))) + odd;
-                                ch[i] = (t & 3) + 4 * (odd ^ (i & 1));
-                            } else {
-                                row[i] = (t >> 2) + 32 * (2 * part + i);
-                                ch[i] = t & 3;
-                            }
-                            in[i] = ld_shared_v4(src + (uint32_t)(row[i] * (DP / 16) + ch[i]) * 16u);
+                    for (int step = 0; step < kRows; ++step) {
+                        const uint4 now[kEach] = {in[0], in[1]};
+                        __half2 hi[kEach] = {}, lo[kEach] = {};
+                        if (is_v) {
+                            row_factor(row_of(step, 0), hi[0], lo[0]);
+                            if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
+                            else row_factor(row_of(step, 1), hi[1], lo[1]);
                         }
-                        if (!whole) {
+                        if (step + 1 < kRows) {
 #pragma unroll
-                            for (int i = 0; i < kEach; ++i) in[i] = keep(in[i], row[i]);
-                        }
-                        if (part == 1) {
+                            for (int i = 0; i < kEach; ++i) in[i] = load(row_of(step + 1, i), chunk_of(i), DP / 16);
+                        } else {
                             __syncwarp();
                             if (lane == 0) mbar_arrive(raw_empty(slot));
                         }
-                        __half2 hi = {}, lo = {};
 #pragma unroll
-                        for (int i = 0; i < kEach; ++i) {
-                            if (is_v && (DP == 64 || (i & 1) == 0)) row_factor((uint32_t)row[i], hi, lo);
-                            decode_store(in[i], (uint32_t)row[i], (uint32_t)ch[i], hi, lo);
-                        }
+                        for (int i = 0; i < kEach; ++i)
+                            decode_store(now[i], (uint32_t)row_of(step, i), (uint32_t)chunk_of(i), hi[i], lo[i]);
                     }
                 } else {
                     for (int i = t; i < 128 * cpr; i += 128) {
                         const int row = i / cpr;
                         __half2 hi = {}, lo = {};
-                        if (is_v) row_factor((uint32_t)row, hi, lo);
-                        decode_store(keep(ld_shared_v4(src + (uint32_t)i * 16u), row), (uint32_t)row, (uint32_t)(i - row * cpr), hi, lo);
+                        if (is_v) row_factor(row, hi, lo);
+                        decode_store(load(row, i - row * cpr, cpr), (uint32_t)row, (uint32_t)(i - row * cpr), hi, lo);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty(slot));
-                }
-                if (!is_v) {
-                    // the tile's scales, for the softmax groups
-                    const uint32_t ss = g % kScaleSlots;
-                    float *sc = reinterpret_cast<float *>(gen + L::kScale) + ss * 256;
-                    sc[t] = ks;
-                    sc[128 + t] = vs;
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.f)));
-                    if (lane == 0) vmax[ss][t >> 5] = __uint_as_float(top);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -950,21 +962,17 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             int valid = 0;
             for (uint32_t g = 0; ok; ++g) {
                 const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(2, e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const Tile tile = ring[2][e];
+                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
+                const Tile tile = ring[e];
                 const int valid_v = valid;
                 const bool end = tile.flags & kTileEnd;
-                const Place<kOps> key_v = key;
-                if (!end) {
-                    valid = (&pieces[0][0])[tile.piece].len - tile.token;
-                    key = op;
-                }
+                if (!end) valid = (&pieces[0][0])[tile.piece].len - tile.token;
 #pragma unroll 1
                 for (int v = end ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v)
-                    ok = convert(v, v ? valid_v : valid, v ? g - 1 : g, key_v);
+                    ok = convert(v, v ? valid_v : valid, tile.flags & 3);
                 if (!ok) break;
                 if (tile.flags & kTileEnd) break;
-                if (lane == 0) mbar_arrive(tile_empty(2, e));
+                if (lane == 0) mbar_arrive(tile_empty(e));
             }
             if (!ok && lane == 0) *abort = 1;
         }
@@ -973,61 +981,55 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * (uint32_t)w, my_o = lanes + kColO + 128u * (uint32_t)w;
-        uint32_t pieces_done = 0;
         bool ok = true;
-        // of the piece
-        bool live = false, warp_live = false, rescale_q = false;
-        int sees = 0, ctx = 0, blk = 0, m = 0, mt = 0;
-        uint64_t word = 0;
-        float r = -INFINITY, l = 0.f, lack = 1.f;
-        for (uint32_t n = 0; ok; ++n) {
-            const uint32_t e = n % kRing;
-            if (!warp_wait(tile_full(w, e), (n / kRing) & 1, abort)) { ok = false; break; }
-            const Tile tile = ring[w][e];
-            if (tile.flags & kTileEnd) break;
-            const Piece &p = (&pieces[0][0])[tile.piece];
-            const bool first = tile.flags & kTileFirst, pair = (tile.flags & 3) == 3;
-            if (first) {
-                float *qscale = reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(pieces_done & 1) * 128;
-                const int rows = pair ? min(p.rows - w * 128, 128) : p.rows;
-                mt = pair ? w * 128 + row : row;             // row of the row tile
-                live = row < rows;
-                warp_live = (warp & 3) * 32 < rows;
-                m = p.m0 + mt;
-                blk = m / group;
-                // what this row sees of the list: tokens below `sees`, and with a mask word those of its bits
-                ctx = sees = p.ctx;
-                word = 0;
-                if (p.request >= 0) {
-                    if (a.row_mask) {
-                        if (live) word = a.row_mask[p.row_base + blk];
-                        if (p.n < 64) word &= (1ull << p.n) - 1;
-                    } else {
-                        sees = a.mask == DSPARK_MASK_CAUSAL ? ctx + min(blk, p.n - 1) + 1 : p.len;
-                    }
-                }
-                r = -INFINITY;
-                l = 0.f;
-                if (pair) {
-                    if (!warp_wait(q_empty(w), (pieces_done & 1) ^ 1, abort)) { ok = false; break; }
-                    load_q<T, DP>(a, p, w * 128, warp & 3, 4, group, base + L::kQ + (uint32_t)w * L::kTileBytes, qscale, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full(w));
+        uint32_t n = 0;       // tiles of the group so far
+        for (uint32_t k = 0; ok; ++k) {
+            if (!warp_wait(piece_full(w, k % kRing), (k / kRing) & 1, abort)) { ok = false; break; }
+            const int told = group_pieces[w][k % kRing], flags = told >> 16;
+            if (flags & kTileEnd) break;
+            const Piece &p = (&pieces[0][0])[told & 0xffff];
+            const bool pair = (flags & 3) == 3;
+            float *qscale = reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(k & 1) * 128;
+            const int rows = pair ? min(p.rows - w * 128, 128) : p.rows;
+            const int mt = pair ? w * 128 + row : row;       // row of the row tile
+            const bool live = row < rows, warp_live = (warp & 3) * 32 < rows;
+            const int m = p.m0 + mt, blk = m / group;
+            // what this row sees of the list: tokens below `sees`, and with a mask word those of its bits
+            const int ctx = p.ctx, tiles = p.tiles;
+            int sees = ctx, token = p.first * plan::kTile;
+            uint64_t word = 0;
+            if (p.request >= 0) {
+                if (a.row_mask) {
+                    if (live) word = a.row_mask[p.row_base + blk];
+                    if (p.n < 64) word &= (1ull << p.n) - 1;
+                } else {
+                    sees = a.mask == DSPARK_MASK_CAUSAL ? ctx + min(blk, p.n - 1) + 1 : p.len;
                 }
             }
+            if (pair) {
+                if (!warp_wait(q_empty(w), (k & 1) ^ 1, abort)) { ok = false; break; }
+                load_q<T, DP>(a, p, w * 128, warp & 3, 4, group, base + L::kQ + (uint32_t)w * L::kTileBytes, qscale, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(w));
+            }
+            float r = -INFINITY, l = 0.f, lack = 1.f;
+            bool rescale_q = false;
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j, ++n, token += plan::kTile) {
+            const bool first = j == 0;
             if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
             tc_fence_after();
             if (first) {
-                lack = live ? (reinterpret_cast<const float *>(gen + L::kQScale))[w * 256 + (int)(pieces_done & 1) * 128 + row] : 1.f;
+                lack = live ? qscale[row] : 1.f;
                 rescale_q = __any_sync(0xffffffffu, lack != 1.f);
             }
             if (warp_live) {
-                const uint32_t ss = (uint32_t)tile.number % kScaleSlots;
-                const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + ss * 256;
-                const int lv = scale_exponent(vmax[ss]);
+                const uint32_t ss = n % kScaleSlots;
+                const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 128;
+                const int lv = exponents[w][ss];
                 const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
-                const bool masked = tile.token > ctx - plan::kTile;   // some row does not see some token of this tile
+                const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
                 float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
                 __syncwarp();
                 // the row's scores 32 columns at a time: holding more of them spills, and with this
@@ -1038,7 +1040,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     bool some_hidden = false;
                     tmem_ld32(my_s + 32u * (uint32_t)q, x);
                     if (masked) {
-                        const int from_t = tile.token + 32 * q, full = min(max(sees - from_t, 0), 32);
+                        const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
                         bits = full == 32 ? 0xffffffffu : (1u << full) - 1u;
                         const int sh = from_t - ctx;   // block token of the first column
                         if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
@@ -1145,10 +1147,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready(w));
-            if (tile.flags & kTileLast) {
+            }
+            if (!ok) break;
+            {
                 // ---- the piece's result
-                if (!warp_wait(o_full(w), pieces_done & 1, abort)) { ok = false; break; }
-                ++pieces_done;
+                if (!warp_wait(o_full(w), k & 1, abort)) { ok = false; break; }
                 tc_fence_after();
                 __syncwarp();
                 if (warp_live) {
@@ -1195,10 +1198,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(o_free(w));
+                if (lane == 0) {
+                    mbar_arrive(o_free(w));
+                    mbar_arrive(piece_empty(w, k % kRing));
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tile_empty(w, e));
         }
         if (!ok && lane == 0) *abort = 1;
     }
