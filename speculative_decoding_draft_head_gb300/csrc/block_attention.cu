@@ -19,11 +19,11 @@
 // So the inner terms take two roundings of 2^-11, everything else is fp32.
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
-// 128 tokens a tile.  Roles (16 warps):
+// 128 tokens a tile.  Roles (20 warps):
 //   0-7   two softmax groups of 128 threads, a thread per row (TMEM lane)
-//   8-11  converters: raw codes -> fp16 operands in the swizzled layout
-//   12    producer: plans tiles, loads codes and scales (bulk copies)
-//   13    issues the tensor-core products;  14, 15  load and scale q
+//   8-15  converters: raw codes -> fp16 operands in the swizzled layout
+//   16    producer: plans tiles, loads codes and scales (bulk copies)
+//   17    issues the tensor-core products;  18, 19  load and scale q
 // A pair tile's keys and values serve both groups; single tiles alternate
 // between the groups' own items.  Operands are loaded, converted and used in
 // one order, K0 K1 V0 K2 V1 ..: keys one tile ahead, so that a group's scores
@@ -39,7 +39,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+// warps of the roles (the softmax groups are warps 0 .. 7)
+constexpr int kConvertAt = 8, kConvertWarps = 8, kProducer = 16, kIssuer = 17, kQueries = 18;
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // tiles planned ahead
 constexpr int kScaleSlots = 4;    // tiles of a group whose key scales are held
@@ -50,7 +52,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: scores (and P) of t
 
 constexpr float kScaleFloor = 0x1p-100f;   // value scales below it lose precision, not range
 constexpr float kPeak = 7.f;               // log2 of P's largest bound when the reference moves ...
-constexpr float kMost = 32768.f;           // ... which it does when 32 terms of P sum to more than this
+constexpr float kMost = 32768.f;           // ... which it does when 64 terms of P sum to more than this
 constexpr int kVUp = 6;                    // log2 of what V is multiplied by: its codes reach 448 * 2^6 in fp16
 constexpr float kVDown = 0x1p-6f;
 constexpr float kQUp = 16.f;               // what q is multiplied by before it becomes fp16 ...
@@ -160,9 +162,9 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
 // e such that every value scale of a tile is below 2^e: `vs` are the tile's 128
 // scales in shared memory (16-byte aligned), of which the first `valid` exist
 // except for the 16-token chunks in `bad`.  The whole warp, all lanes alike.
-__device__ __forceinline__ int scale_exponent(const float *vs, int valid, int bad, int lane) {
-    const float4 v = *reinterpret_cast<const float4 *>(vs + 4 * lane);
-    const float x[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ int scale_exponent(uint32_t vs, int valid, int bad, int lane) {
+    const uint4 v = ld_shared_v4(vs + 16u * (uint32_t)lane);
+    const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
     float top = kScaleFloor;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -193,6 +195,15 @@ struct Place {
         if (++slot == n) slot = 0, lap ^= 1;
     }
 };
+
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // ------------------------------------------------------------------ the plan --
 // The line as a CTA sees it.
@@ -495,10 +506,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t drain = bar1 + 8u * 12u;
 
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), 4);
-        for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), 4), mbar_init(op_empty(i), 1);
+        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), kConvertWarps);
+        for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), kConvertWarps), mbar_init(op_empty(i), 1);
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 7);
+            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 3 + kConvertWarps);
             for (int w = 0; w < 2; ++w) mbar_init(piece_full(w, i), 1), mbar_init(piece_empty(w, i), 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -511,7 +522,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         misc[0] = misc[1] = 0;
         for (int i = 0; i < 3; ++i) found_request[i] = a.rows.B, found_units[i] = 0;
     }
-    if (warp == 13) {
+    if (warp == kIssuer) {
         tmem_alloc(smem_u32(misc + 2), 512);
         tmem_relinquish();
     }
@@ -605,8 +616,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[2];
 
-    if (warp >= 8) {
-        if (warp == 12) {
+    // the launch's 640 x 96 registers: 128 a softmax thread, 64 a converter's, 96 one of the others
+    if (warp >= kConvertAt) {
+        if (warp == kProducer) {
             // ------------------------------------------------------ producer --
             // `cur` is the stream whose tile comes next, stream `id` of the two: pairs, then the
             // first group's singles, are stream 0's, the second group's singles stream 1's
@@ -725,7 +737,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 for (uint32_t i = loaded > (uint32_t)kRaw ? loaded - kRaw : 0; i < loaded; ++i)
                     mbar_wait(raw_full(i % kRaw), (i / kRaw) & 1, never, kDrainLimit);
             }
-        } else if (warp == 13) {
+        } else if (warp == kIssuer) {
             // ------------------------------------------- tensor-core products --
             // the whole warp walks the loop, so that addresses stay warp-uniform; one lane issues
             const bool leader = elect_one();
@@ -814,7 +826,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 commit(drain);
                 mbar_wait(drain, 0, never, kDrainLimit);
             }
-        } else if (warp >= 14) {
+        } else if (warp >= kQueries) {
             // ------------------------------------------------------------ q --
             // (of single items; a pair's groups load their own)
             uint32_t qc[2] = {0, 0};
@@ -829,7 +841,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     const uint32_t n = w ? qc[1] : qc[0];
                     if (mask != 3) {
                         if (!warp_wait(q_empty(w), (n & 1) ^ 1, abort)) { ok = false; break; }
-                        load_q<T, DP>(a, (&pieces[0][0])[ring[e].piece], 0, warp - 14, 2, group,
+                        load_q<T, DP>(a, (&pieces[0][0])[ring[e].piece], 0, warp - kQueries, 2, group,
                                       base + L::kQ + (uint32_t)w * L::kTileBytes,
                                       reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(n & 1) * 128, lane);
                         fence_proxy_async_smem();
@@ -845,7 +857,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             if (!ok && lane == 0) *abort = 1;
         } else {
             // ---------------------------------------------------- converters --
-            const int t = tid - 256;
+            regs_dec<64>();
+            const int t = tid - kConvertAt * 32;
             const int cpr = D / 16;                      // 16-code chunks of a token
             const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
             Place<kOps> op = {0, 0};
@@ -863,14 +876,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const uint32_t dst = base + L::kOp + op.slot * L::kTileBytes;
                 const int bad = raw_bad[slot];
                 const bool whole = valid >= plan::kTile && bad == 0;
-                const float *raw_scale = reinterpret_cast<const float *>(gen + L::kRawAt + slot * L::kRawBytes + 128 * DP);
-                const int exponent = scale_exponent(raw_scale + 128, valid, bad, lane);
+                const uint32_t raw_scale = src + 128u * DP;   // key scales, then value scales
+                const int exponent = scale_exponent(raw_scale + 512u, valid, bad, lane);
                 // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
                 // leaves the tile's largest below 2^15
                 const float v_unit = __uint_as_float((uint32_t)(127 + kVUp - exponent) << 23);
                 auto there = [&](int row) { return whole || (row < valid && !(bad >> (row >> 4) & 1)); };
                 auto row_factor = [&](int row, __half2 &hi, __half2 &lo) {
-                    const float v = raw_scale[128 + row], f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
+                    const float v = ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)row), f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
                     hi = __float2half2_rn(f);
                     lo = __float2half2_rn(f - __low2float(hi));
                 };
@@ -899,51 +912,47 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     // value scale (or page) is no number carries its NaN in the key's alone: where it is
                     // masked, its zero values must not become 0 times NaN
                     float ks = 0.f;
-                    if (t < valid)
-                        ks = there(t) && raw_scale[128 + t] <= 3.4028235e38f ? raw_scale[t] * up : __int_as_float(0x7fffffff);
+                    if (t < min(valid, plan::kTile))
+                        ks = there(t) && ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)t) <= 3.4028235e38f
+                                 ? ld_shared_f32(raw_scale + 4u * (uint32_t)t) * up
+                                 : __int_as_float(0x7fffffff);
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        if (!(mask >> w & 1)) continue;
+                        if (!(mask >> w & 1) || t >= plan::kTile) continue;
                         const uint32_t i = (group_tiles >> (16 * w)) % kScaleSlots;
-                        reinterpret_cast<float *>(gen + L::kScale)[(w * kScaleSlots + i) * 128 + t] = ks;
+                        st_shared_f32(base + L::kScale + ((uint32_t)(w * kScaleSlots) + i) * 512u + 4u * (uint32_t)t, ks);
                         if (t == 0) exponents[w][i] = exponent;
                     }
                     // (counts of 16 bits: the carry of the lower is kept out of the upper)
                     group_tiles = ((group_tiles + (mask & 1)) & 0xffffu) | ((group_tiles & 0xffff0000u) + ((uint32_t)(mask >> 1) << 16));
                 }
                 if (D == DP) {
-                    // a row (or two) at a time, the next one's loads under the decoding
-                    constexpr int kRows = DP == 128 ? 4 : 2, kEach = 2;   // steps; 16-code chunks of a step
+                    constexpr int kSteps = DP / 64;     // two chunks each: of one row (D = 128), of two rows
                     const int odd = t >> 2 & 1;
-                    auto row_of = [&](int step, int i) {
-                        return DP == 128 ? 2 * ((t >> 3) + 16 * step) + odd : (t >> 2) + 32 * (2 * step + i);
-                    };
-                    auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
-                    uint4 in[kEach];
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) in[i] = load(row_of(0, i), chunk_of(i), DP / 16);
 #pragma unroll 1
-                    for (int step = 0; step < kRows; ++step) {
-                        const uint4 now[kEach] = {in[0], in[1]};
-                        __half2 hi[kEach] = {}, lo[kEach] = {};
-                        if (is_v) {
-                            row_factor(row_of(step, 0), hi[0], lo[0]);
-                            if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
-                            else row_factor(row_of(step, 1), hi[1], lo[1]);
-                        }
-                        if (step + 1 < kRows) {
+                    for (int step = 0; step < kSteps; ++step) {
+                        uint4 in[2];
+                        __half2 hi[2] = {}, lo[2] = {};
+                        auto row_of = [&](int i) {
+                            return DP == 128 ? 2 * ((t >> 3) + 32 * step) + odd : (t >> 2) + 64 * i;
+                        };
+                        auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
 #pragma unroll
-                            for (int i = 0; i < kEach; ++i) in[i] = load(row_of(step + 1, i), chunk_of(i), DP / 16);
-                        } else {
+                        for (int i = 0; i < 2; ++i) {
+                            in[i] = load(row_of(i), chunk_of(i), DP / 16);
+                            if (is_v && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
+                        }
+                        if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
+                        if (step + 1 == kSteps) {
                             __syncwarp();
                             if (lane == 0) mbar_arrive(raw_empty(slot));
                         }
 #pragma unroll
-                        for (int i = 0; i < kEach; ++i)
-                            decode_store(now[i], (uint32_t)row_of(step, i), (uint32_t)chunk_of(i), hi[i], lo[i]);
+                        for (int i = 0; i < 2; ++i)
+                            decode_store(in[i], (uint32_t)row_of(i), (uint32_t)chunk_of(i), hi[i], lo[i]);
                     }
                 } else {
-                    for (int i = t; i < 128 * cpr; i += 128) {
+                    for (int i = t; i < 128 * cpr; i += 32 * kConvertWarps) {
                         const int row = i / cpr;
                         __half2 hi = {}, lo = {};
                         if (is_v) row_factor(row, hi, lo);
@@ -978,6 +987,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         }
     } else {
         // -------------------------------------------------------------- softmax --
+        regs_inc<128>();
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * (uint32_t)w, my_o = lanes + kColO + 128u * (uint32_t)w;
@@ -1032,50 +1042,55 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
                 float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
                 __syncwarp();
-                // the row's scores 32 columns at a time: holding more of them spills, and with this
-                // much shared memory a spilled register comes back from L2
+                // the row's scores 64 columns at a time: more would spill, and with this much shared
+                // memory a spilled register comes back from L2
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[32], pr[16], bits = 0xffffffffu;
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t pr[32];
+                    uint64_t bits = ~0ull;
                     bool some_hidden = false;
-                    tmem_ld32(my_s + 32u * (uint32_t)q, x);
                     if (masked) {
-                        const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
-                        bits = full == 32 ? 0xffffffffu : (1u << full) - 1u;
+                        const int from_t = token + 64 * q, full = min(max(sees - from_t, 0), 64);
+                        bits = full == 64 ? ~0ull : (1ull << full) - 1;
                         const int sh = from_t - ctx;   // block token of the first column
-                        if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
-                        some_hidden = __any_sync(0xffffffffu, bits != 0xffffffffu);
-                    }
-                    tmem_ld_wait32(x);
-                    if (masked && !__any_sync(0xffffffffu, live && bits != 0)) {
+                        if (sh > -64 && sh < 64) bits |= sh >= 0 ? word >> sh : word << -sh;
+                        some_hidden = __any_sync(0xffffffffu, bits != ~0ull);
+                        if (!__any_sync(0xffffffffu, live && bits != 0)) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pr[i] = 0;
-                        tmem_st16(my_s + 16u * (uint32_t)q, pr);
-                        continue;
+                            for (int i = 0; i < 32; ++i) pr[i] = 0;
+                            tmem_st32(my_s + 32u * (uint32_t)q, pr);
+                            continue;
+                        }
                     }
-                    if (rescale_q) {
+                    // 32 columns' sums, with the row's own factor
+                    auto load_x = [&](int h, uint32_t (&x)[32]) { tmem_ld32(my_s + 64u * (uint32_t)q + 32u * (uint32_t)h, x); };
+                    auto wait_x = [&](uint32_t (&x)[32]) {
+                        tmem_ld_wait32(x);
+                        if (rescale_q) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * lack);
-                    }
-                    // scores in log2 units less `ref2`; those the row does not see -inf
-                    auto four = [&](int i, uint64_t ref2, float (&y)[4], auto hidden) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + i);
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * lack);
+                        }
+                    };
+                    // scores in log2 units less `ref2` of four columns; those the row does not see -inf
+                    auto four = [&](const uint32_t *x, int h, int i, uint64_t ref2, float (&y)[4], auto hidden) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 64 * q + 32 * h + i);
                         unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pack2(k4.x, k4.y), ref2), y[0], y[1]);
                         unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), pack2(k4.z, k4.w), ref2), y[2], y[3]);
                         if constexpr (decltype(hidden)::value) {
+                            const uint32_t seen = (uint32_t)(bits >> (32 * h));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
+                                if (!(seen >> (i + k) & 1u)) y[k] = -INFINITY;
                         }
                     };
-                    // the 32 terms, and their sum
-                    auto terms = [&](auto hidden) {
+                    // the 64 terms to `pr`, and their sum
+                    auto terms = [&](const uint32_t *xa, const uint32_t *xb, auto hidden) {
                         const uint64_t ref2 = pack2(-ref, -ref);
                         uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+                        for (int i = 0; i < 64; i += 4) {
                             float y[4];
-                            four(i, ref2, y, hidden);
+                            four(i < 32 ? xa : xb, i >> 5, i & 31, ref2, y, hidden);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
                             sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
@@ -1090,17 +1105,30 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     float s;
 #pragma unroll 1
                     for (int again = 0;; ++again) {
-                        s = some_hidden ? terms(std::true_type{}) : terms(std::false_type{});
-                        // the reference has to move when a term could pass 2^15 (the sum of 32 says so), or
+                        {
+                            uint32_t xa[32], xb[32];
+                            load_x(0, xa);
+                            load_x(1, xb);
+                            wait_x(xa);
+                            wait_x(xb);
+                            s = some_hidden ? terms(xa, xb, std::true_type{}) : terms(xa, xb, std::false_type{});
+                        }
+                        // the reference has to move when a term could pass 2^15 (the sum of 64 says so), or
                         // when there is none yet
                         const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
                         if (again || !__any_sync(0xffffffffu, moves)) break;
                         float top = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t x[32];
+                            load_x(h, x);
+                            wait_x(x);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float y[4];
-                            four(i, 0, y, std::true_type{});
-                            top = max3(max3(top, y[0], y[1]), y[2], y[3]);
+                            for (int i = 0; i < 32; i += 4) {
+                                float y[4];
+                                four(x, h, i, 0, y, std::true_type{});
+                                top = max3(max3(top, y[0], y[1]), y[2], y[3]);
+                            }
                         }
                         float f = 1.f;
                         if (moves && top != -INFINITY) {     // (-inf: there is no number)
@@ -1126,7 +1154,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         const __half2 f2 = __float2half2_rn(f);
                         tmem_st_wait();
 #pragma unroll 1
-                        for (int i = 0; i < q; ++i) {
+                        for (int i = 0; i < 2 * q; ++i) {
                             uint32_t o[16];
                             tmem_ld16(my_s + 16u * (uint32_t)i, o);
                             tmem_ld_wait16(o);
@@ -1139,8 +1167,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         }
                     }
                     l = fmaf(s, unit, l);
-                    // P's 16 columns lie below the scores still to be read
-                    tmem_st16(my_s + 16u * (uint32_t)q, pr);
+                    // P's 32 columns lie below the scores still to be read
+                    tmem_st32(my_s + 32u * (uint32_t)q, pr);
                 }
                 tmem_st_wait();
             }
@@ -1209,7 +1237,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 13) tmem_dealloc(tmem, 512);
+    if (warp == kIssuer) tmem_dealloc(tmem, 512);
     if (tid == 0 && *abort) atomicOr(c.flags, kFlagTimeout);
 }
 
