@@ -19,15 +19,19 @@
 // So the inner terms take two roundings of 2^-11, everything else is fp32.
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
-// 128 tokens a tile.  Roles (20 warps):
-//   0-7   two softmax groups of 128 threads, a thread per row (TMEM lane)
-//   8-15  converters: raw codes -> fp16 operands in the swizzled layout
-//   16    producer: plans tiles, loads codes and scales (bulk copies)
-//   17    issues the tensor-core products;  18, 19  load and scale q
+// 128 tokens a tile.  Roles (18 warps):
+//   0-7    two softmax groups of 128 threads, a thread per row (TMEM lane)
+//   8-11   queries and keys to fp16 operands in the swizzled layout;  12-15  values
+//   16     producer: plans tiles, loads codes and scales (bulk copies)
+//   17     issues the tensor-core products
 // A pair tile's keys and values serve both groups; single tiles alternate
 // between the groups' own items.  Operands are loaded, converted and used in
 // one order, K0 K1 V0 K2 V1 ..: keys one tile ahead, so that a group's scores
-// are ready while the other group's softmax runs.  Every wait is bounded.
+// are ready while the other group's softmax runs.  Every ring is filled in this
+// order by one warp or freed in it, and the two converter teams wait for their
+// operand's place before they look for its codes: so no wait is more than one
+// lap of a ring away from the phase that it tests, whose parity would deceive it.
+// Every wait is bounded.
 #include <type_traits>
 
 #include "attention_plan.h"
@@ -39,9 +43,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 576;
 // warps of the roles (the softmax groups are warps 0 .. 7)
-constexpr int kConvertAt = 8, kConvertWarps = 8, kProducer = 16, kIssuer = 17, kQueries = 18;
+constexpr int kConvertAt = 8, kTeamWarps = 4, kProducer = 16, kIssuer = 17;
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // tiles planned ahead
 constexpr int kScaleSlots = 4;    // tiles of a group whose key scales are held
@@ -186,6 +190,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
         if (*abort || (uint32_t)clock() - t0 > kSpinLimit) break;
     return __all_sync(0xffffffffu, ok);
 }
+
+// A value that all lanes hold, in the form the compiler knows to be so.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Place in a ring of n slots, with the parity of the lap.
 template <int n>
@@ -350,50 +357,78 @@ constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 // tile of its piece has left the ring (the next piece is planned while the last
 // one's tiles are taken, hence more than kRing slots).
 constexpr int kPieces = 2 * kRing;
+// (In shared memory, as there are two and the loop over tiles should be one.)
 struct Stream {
-    int j, tiles, next_tiles, token, page, off;   // tile of the piece, its tiles, the next piece's; page and place of a chunk
-    uint32_t window, count;                        // chunk numbers of the current four tiles; pieces begun
+    int j, tiles, next_tiles, token;   // tile of the piece, its tiles, the next piece's; the tile's first token
+    uint32_t count;                    // pieces begun
+    int page[32], off[32];             // of the next four tiles' chunks, a lane each
+    uint32_t window[32];               // chunk numbers of the current four tiles
+    Walk walk;
+    Piece slots[kPieces];
 
     __device__ __forceinline__ void load_pages(const AttentionArgs &a, const Piece &p, int t, int lane) {
         const int per_page = a.cache.page_size / 16, chunk = (p.first + t) * 8 + lane;
-        off = -1;
-        page = 0;
+        int place = -1, pg = 0;
         if ((int64_t)chunk * 16 < p.len) {
             const int slot = chunk / per_page;
-            off = p.head * per_page + (chunk - slot * per_page);
-            page = p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
+            place = p.head * per_page + (chunk - slot * per_page);
+            pg = p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
         }
-    }
-    // the next tile (tiles > 0): its chunk numbers in lanes 0 .. 7 (and again in 8 .. 15 and so on)
-    __device__ __forceinline__ uint32_t take(const AttentionArgs &a, const Line &z, Walk &walk, Piece *slots, Tile &t, int lane) {
-        if ((j & 3) == 0) {
-            window = off < 0 ? kNoChunk
-                             : (page < 0 || page >= a.cache.n_pages)
-                                   ? kBadChunk
-                                   : (uint32_t)page * (uint32_t)(a.cache.n_kv_heads * (a.cache.page_size / 16)) + (uint32_t)off;
-            const Piece *p = slots + count % kPieces;
-            if (j == 0) token = p->first * plan::kTile;
-            int from = j + 4;
-            if (from >= tiles) {
-                p = slots + (count + 1) % kPieces;
-                next_tiles = walk_next(a, z, walk, slots[(count + 1) % kPieces], lane);
-                from = 0;
-            }
-            if (from || next_tiles) load_pages(a, *p, from, lane);
-        }
-        const uint32_t ids = __shfl_sync(0xffffffffu, window, ((j & 3) << 3) + (lane & 7));
-        t.token = token;
-        t.piece = (int)(count % kPieces);
-        t.flags = (j == 0 ? kTileFirst : 0) | (j + 1 == tiles ? kTileLast : 0);
-        token += plan::kTile;
-        if (++j == tiles) {
-            tiles = next_tiles;
-            j = 0;
-            ++count;
-        }
-        return ids;
+        page[lane] = pg;
+        off[lane] = place;
     }
 };
+
+__device__ __noinline__ void stream_begin(const AttentionArgs &a, const Line &z, Stream &s, int cls, int64_t lo, int64_t to,
+                                          int b0, int64_t own0, int lane) {
+    walk_begin(a, z, s.walk, cls, lo, to, b0, own0, lane);
+    Piece &p = s.slots[s.count % kPieces];
+    const int tiles = walk_next(a, z, s.walk, p, lane);
+    s.tiles = tiles;
+    s.next_tiles = s.j = 0;
+    if (tiles) s.load_pages(a, p, 0, lane);
+    __syncwarp();
+}
+
+// the next tile (s.tiles > 0): its chunk numbers in lanes 0 .. 7 (and again in 8 .. 15 and so on)
+__device__ __noinline__ uint32_t stream_take(const AttentionArgs &a, const Line &z, Stream &s, Tile &t, int lane) {
+    const int j = s.j, tiles = s.tiles;
+    const uint32_t count = s.count;
+    int token = s.token, next_tiles = s.next_tiles;
+    __syncwarp();
+    if ((j & 3) == 0) {
+        const int off = s.off[lane], page = s.page[lane];
+        s.window[lane] = off < 0 ? kNoChunk
+                         : (page < 0 || page >= a.cache.n_pages)
+                             ? kBadChunk
+                             : (uint32_t)page * (uint32_t)(a.cache.n_kv_heads * (a.cache.page_size / 16)) + (uint32_t)off;
+        const Piece *p = s.slots + count % kPieces;
+        if (j == 0) token = p->first * plan::kTile;
+        int from = j + 4;
+        if (from >= tiles) {
+            next_tiles = walk_next(a, z, s.walk, s.slots[(count + 1) % kPieces], lane);
+            p = s.slots + (count + 1) % kPieces;
+            from = 0;
+        }
+        if (from || next_tiles) s.load_pages(a, *p, from, lane);
+        __syncwarp();
+    }
+    const uint32_t ids = s.window[((j & 3) << 3) + (lane & 7)];
+    t.token = token;
+    t.piece = (int)(count % kPieces);
+    t.flags = (j == 0 ? kTileFirst : 0) | (j + 1 == tiles ? kTileLast : 0);
+    const bool last = j + 1 == tiles;
+    __syncwarp();
+    s.token = token + plan::kTile;
+    s.next_tiles = next_tiles;
+    s.j = last ? 0 : j + 1;
+    if (last) {
+        s.tiles = next_tiles;
+        s.count = count + 1;
+    }
+    __syncwarp();
+    return ids;
+}
 
 // ------------------------------------------------------------------------- q --
 // Up to 128 rows of a row tile, from its row t0 on, to fp16 in the swizzled
@@ -468,23 +503,23 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 6 * kRing + 16];
     __shared__ int group_pieces[2][kRing];          // pieces of the softmax groups: slot, flags
-    __shared__ Piece pieces[2][kPieces];
+    __shared__ Stream streams[2];
     __shared__ __align__(16) Tile ring[kRing];      // tiles, for the other roles
     __shared__ int exponents[2][kScaleSlots];       // of the value scales of the groups' tiles
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
     __shared__ Line line;
-    __shared__ Walk walks[2];
     __shared__ int64_t found_units[3], from_s[3], to_s[3];   // of the workers: pairs, and each group's singles
     __shared__ int found_request[3];
     __shared__ int misc[3];       // abort, a word that stays 0, TMEM address
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const dspark_kv_cache &c = a.cache;
     const int D = c.head_dim, group = a.n_q_heads / c.n_kv_heads;
     const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
     unsigned char *gen = dyn + (base - smem_u32(dyn));
     volatile int *abort = misc, *never = misc + 1;
+    auto piece_at = [&](int i) -> const Piece & { return streams[i / kPieces].slots[i % kPieces]; };
 
     // barriers
     const uint32_t bar0 = smem_u32(bars);
@@ -506,14 +541,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t drain = bar1 + 8u * 12u;
 
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), kConvertWarps);
-        for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), kConvertWarps), mbar_init(op_empty(i), 1);
+        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), kTeamWarps);
+        for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), kTeamWarps), mbar_init(op_empty(i), 1);
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 3 + kConvertWarps);
+            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 1 + 2 * kTeamWarps);
             for (int w = 0; w < 2; ++w) mbar_init(piece_full(w, i), 1), mbar_init(piece_empty(w, i), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), 4), mbar_init(q_empty(i), 1);
+            mbar_init(q_full(i), kTeamWarps), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
             mbar_init(o_full(i), 1), mbar_init(o_free(i), 4);
         }
@@ -614,97 +649,226 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)misc[2];
+    const uint32_t tmem = (uint32_t)uniform(misc[2]);
 
-    // the launch's 640 x 96 registers: 128 a softmax thread, 64 a converter's, 96 one of the others
+    // Loads the keys or values of a tile, chunk `mine` in lanes 0 .. 7 (and again in 8 .. 15 and so
+    // on), to place `position` of the order of operands, in runs of tokens that share a page.  (Copies
+    // by the warp's own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
+    const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
+    auto load = [&](uint32_t mine, bool is_v, uint32_t position) {
+        const int i = lane & 7;
+        const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
+        const bool good = i < runs && id < kBadChunk;
+        const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
+        const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
+        const uint32_t slot = position % kRaw;
+        if (!warp_wait(raw_empty(slot), ((position / kRaw) & 1) ^ 1, abort)) return false;
+        const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
+        if (lane == 0) {
+            raw_bad[slot] = (int)bad;
+            mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D + 4 : D + 8)));
+        }
+        __syncwarp();
+        const bool leader = elect_one();
+#pragma unroll 1
+        for (int r = 0; r < runs; ++r) {
+            const uint32_t from = (uint32_t)uniform((int)__shfl_sync(0xffffffffu, mine, r * (run / 16)));
+            if (from >= kBadChunk || !leader) continue;
+            const uint64_t first = (uint64_t)from * 16u;      // head row of the run's first token
+            bulk_load(at + (uint32_t)(r * run * D), static_cast<const unsigned char *>(is_v ? c.v : c.k) + first * (uint32_t)D,
+                      (uint32_t)(run * D), raw_full(slot));
+            bulk_load(at + 128u * DP + 512u + (uint32_t)(r * run * 4), c.v_scale + first, (uint32_t)(run * 4), raw_full(slot));
+            if (!is_v)
+                bulk_load(at + 128u * DP + (uint32_t)(r * run * 4), c.k_scale + first, (uint32_t)(run * 4), raw_full(slot));
+        }
+        __syncwarp();
+        if (bad && lane == 0) atomicOr(c.flags, kFlagBadPage);
+        return true;
+    };
+    // a loader that gives up waits for the last copies: they must land before the block's memory goes
+    auto drain_copies = [&](uint32_t position) {
+        for (uint32_t i = 0; i < (uint32_t)kRaw && i <= position; ++i)
+            mbar_wait(raw_full((position - i) % kRaw), ((position - i) / kRaw) & 1, never, kDrainLimit);
+    };
+
+    // One team of converters: the keys (and queries) or the values of all tiles.  The lanes of a quarter
+    // warp take four chunks each of the lower and the upper 64 columns of an even and an odd row:
+    // neither their loads nor their stores (the swizzle takes even chunks of an odd row to odd places)
+    // meet in a bank.
+    auto convert_all = [&](auto team) {
+        constexpr bool kIsV = decltype(team)::value;
+        const int t = tid - (kConvertAt + (kIsV ? kTeamWarps : 0)) * 32;
+        const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
+        uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
+        uint32_t group_pieces_seen = 0;              // parity of the groups' pieces
+        int valid = 0;
+        for (uint32_t g = 0;; ++g) {
+            const uint32_t e = g % kRing;
+            if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) return false;
+            const int flags = uniform(ring[e].flags), valid_v = valid;
+            const bool end = flags & kTileEnd;
+            if (kIsV) {
+                if (!end) valid = uniform(piece_at(ring[e].piece).len - ring[e].token);
+                __syncwarp();
+                if (!end && lane == 0) mbar_arrive(tile_empty(e));
+                if (g == 0) {
+                    if (end) return true;
+                    continue;
+                }
+            } else {
+                if (end) return true;
+                const Piece &p = piece_at(uniform(ring[e].piece));
+                valid = uniform(p.len) - uniform(ring[e].token);
+                if (flags & kTileFirst) {
+                    // the piece's queries
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) {
+                        if (!(flags >> w & 1)) continue;
+                        const uint32_t seen = group_pieces_seen >> w & 1;
+                        if (!warp_wait(q_empty(w), seen ^ 1, abort)) return false;
+                        load_q<T, DP>(a, p, (flags & 3) == 3 ? w * 128 : 0, warp - kConvertAt, kTeamWarps, group,
+                                      base + L::kQ + (uint32_t)w * L::kTileBytes,
+                                      reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)seen * 128, lane);
+                        group_pieces_seen ^= 1u << w;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q_full(w));
+                    }
+                }
+            }
+            // the operand: keys of tile g, or values of tile g - 1
+            const int there_are = kIsV ? valid_v : valid;
+            const uint32_t position = kIsV ? (end ? 2 * g - 1 : 2 * g) : (g == 0 ? 0 : 2 * g - 1);
+            const uint32_t slot = position % kRaw, op = position % kOps;
+            if (!warp_wait(op_empty(op), ((position / kOps) & 1) ^ 1, abort)) return false;
+            if (!warp_wait(raw_full(slot), (position / kRaw) & 1, abort)) return false;
+            const uint32_t src = base + L::kRawAt + slot * L::kRawBytes, dst = base + L::kOp + op * L::kTileBytes;
+            const uint32_t raw_scale = src + 128u * DP;   // key scales, then value scales
+            const int bad = uniform(raw_bad[slot]);
+            const bool whole = there_are >= plan::kTile && bad == 0;
+            const int exponent = scale_exponent(raw_scale + 512u, there_are, bad, lane);
+            auto there = [&](int row) { return whole || (row < there_are && !(bad >> (row >> 4) & 1)); };
+            // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
+            // leaves the tile's largest below 2^15
+            const float v_unit = __uint_as_float((uint32_t)(127 + kVUp - exponent) << 23);
+            auto row_factor = [&](int row, __half2 &hi, __half2 &lo) {
+                const float v = ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)row), f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
+                hi = __float2half2_rn(f);
+                lo = __float2half2_rn(f - __low2float(hi));
+            };
+            auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch, __half2 hi, __half2 lo) {
+                __half2 h[8];
+                decode4<kFormat>(in.x, h[0], h[1]);
+                decode4<kFormat>(in.y, h[2], h[3]);
+                decode4<kFormat>(in.z, h[4], h[5]);
+                decode4<kFormat>(in.w, h[6], h[7]);
+                if constexpr (kIsV) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = __hfma2(h[i], hi, __hmul2(h[i], lo));
+                }
+                const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
+                const uint32_t at = dst + (ch >> 2) * (128u * 128u) + row * 128u, c8 = (ch & 3u) * 2u;
+                st_shared_v4(at + ((c8 ^ (row & 7u)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+                st_shared_v4(at + (((c8 + 1u) ^ (row & 7u)) << 4), make_uint4(u[4], u[5], u[6], u[7]));
+            };
+            // nothing of a token that is not there
+            auto read = [&](int row, int ch, int width) {
+                const uint4 in = ld_shared_v4(src + (uint32_t)(row * width + ch) * 16u);
+                return there(row) ? in : make_uint4(0, 0, 0, 0);
+            };
+            if constexpr (!kIsV) {
+                // the tile's key scales (of scores in log2 units), for the softmax groups; a token whose
+                // value scale (or page) is no number carries its NaN in the key's alone: where it is
+                // masked, its zero values must not become 0 times NaN
+                float ks = 0.f;
+                if (t < there_are)
+                    ks = there(t) && ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)t) <= 3.4028235e38f
+                             ? ld_shared_f32(raw_scale + 4u * (uint32_t)t) * up
+                             : __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!(flags >> w & 1)) continue;
+                    const uint32_t i = (group_tiles >> (16 * w)) % kScaleSlots;
+                    st_shared_f32(base + L::kScale + ((uint32_t)(w * kScaleSlots) + i) * 512u + 4u * (uint32_t)t, ks);
+                    if (t == 0) exponents[w][i] = exponent;
+                }
+                // (counts of 16 bits: the carry of the lower is kept out of the upper)
+                group_tiles = ((group_tiles + (flags & 1)) & 0xffffu) | ((group_tiles & 0xffff0000u) + ((uint32_t)(flags >> 1 & 1) << 16));
+            }
+            if (D == DP) {
+                constexpr int kSteps = DP / 32;     // two chunks each: of one row (D = 128), of two rows
+                const int odd = t >> 2 & 1;
+#pragma unroll 1
+                for (int step = 0; step < kSteps; ++step) {
+                    uint4 in[2];
+                    __half2 hi[2] = {}, lo[2] = {};
+                    auto row_of = [&](int i) {
+                        return DP == 128 ? 2 * ((t >> 3) + 16 * step) + odd : (t >> 2) + 32 * (2 * step + i);
+                    };
+                    auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        in[i] = read(row_of(i), chunk_of(i), DP / 16);
+                        if (kIsV && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
+                    }
+                    if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
+                    if (step + 1 == kSteps) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty(slot));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) decode_store(in[i], (uint32_t)row_of(i), (uint32_t)chunk_of(i), hi[i], lo[i]);
+                }
+            } else {
+                const int width = D / 16;
+#pragma unroll 1
+                for (int i = t; i < 128 * width; i += 32 * kTeamWarps) {
+                    const int row = i / width;
+                    __half2 hi = {}, lo = {};
+                    if (kIsV) row_factor(row, hi, lo);
+                    decode_store(read(row, i - row * width, width), (uint32_t)row, (uint32_t)(i - row * width), hi, lo);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_empty(slot));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(op_full(op));
+                if (!kIsV) mbar_arrive(tile_empty(e));
+            }
+            if (kIsV && end) return true;
+        }
+    };
+
     if (warp >= kConvertAt) {
         if (warp == kProducer) {
             // ------------------------------------------------------ producer --
-            // `cur` is the stream whose tile comes next, stream `id` of the two: pairs, then the
-            // first group's singles, are stream 0's, the second group's singles stream 1's
-            Stream cur, oth;
-            cur.count = oth.count = 0;
-            int id = 0;
-            auto start = [&](Stream &s, int k, int i) {
-                walk_begin(a, line, walks[k], i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
-                           found_units[i], lane);
-                s.tiles = walk_next(a, line, walks[k], pieces[k][s.count % kPieces], lane);
-                s.next_tiles = s.j = 0;
-                if (s.tiles) s.load_pages(a, pieces[k][s.count % kPieces], 0, lane);
-            };
+            // pairs, then the first group's singles, are stream 0's tiles, the second group's singles stream 1's
+            if (lane < 2) streams[lane].count = 0;
+            __syncwarp();
             bool ok = true, pairing = true;
-            oth.tiles = 0;
+            int id = 0;             // the stream of the last tile
 #pragma unroll 1
-            for (int i = 2; i >= 0; i -= 2) {     // the second group's singles, then the pairs
-                start(cur, id = i >> 1, i);
-                if (i == 2) {
-                    const Stream x = cur;
-                    cur = oth;
-                    oth = x;
-                }
-            }
-            Place<kRaw> raw = {0, 0};            // operand tiles loaded
-            uint32_t loaded = 0;
+            for (int i = 2; i >= 0; i -= 2)
+                stream_begin(a, line, streams[i >> 1], i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
+                             found_units[i], lane);
             uint32_t ids = kNoChunk, ids_v = kNoChunk;
-            bool flagged = false, turn = false;
-            // A tile is loaded in runs of tokens that share a page: lanes 0 .. 7 copy a run of codes
-            // each, lanes 8 .. 15 (with the keys) and 16 .. 23 the runs' scales.  (Copies by the warp's
-            // own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
-            const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
-            auto load = [&](uint32_t mine, bool is_v) {
-                const int i = lane & 7;
-                const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
-                const bool good = i < runs && id < kBadChunk;
-                const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
-                const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
-                const uint32_t slot = raw.slot;
-                if (!warp_wait(raw_empty(slot), raw.lap ^ 1, abort)) return false;
-                const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
-                if (lane == 0) {
-                    raw_bad[slot] = (int)bad;
-                    mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D + 4 : D + 8)));
-                }
-                __syncwarp();
-                if (good && lane < 24 && !(is_v && (lane & 8))) {
-                    uint32_t to, bytes;
-                    const unsigned char *src;
-                    if (lane < 8) {
-                        src = static_cast<const unsigned char *>(is_v ? c.v : c.k) + (uint64_t)id * (uint32_t)(16 * D);
-                        to = at + (uint32_t)(i * run * D);
-                        bytes = (uint32_t)(run * D);
-                    } else {
-                        src = reinterpret_cast<const unsigned char *>((lane < 16 ? c.k_scale : c.v_scale) + (uint64_t)id * 16u);
-                        to = at + 128u * DP + (lane < 16 ? 0u : 512u) + (uint32_t)(i * run * 4);
-                        bytes = (uint32_t)(run * 4);
-                    }
-                    bulk_load(to, src, bytes, raw_full(slot));
-                }
-                flagged |= bad != 0;
-                raw.step();
-                ++loaded;
-                return true;
-            };
             uint32_t taken = 0;                  // pieces given to the groups, modulo 2^16 (a multiple of the ring's laps)
             for (uint32_t g = 0; ok; ++g) {
                 Tile t;
                 t.flags = kTileEnd;
-                t.token = t.piece = t.pad = 0;
+                t.token = t.piece = 0;
                 const uint32_t e = g % kRing;
                 if (!warp_wait(tile_empty(e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
-                if (pairing && cur.tiles == 0) {
+                if (pairing && streams[0].tiles == 0) {
                     pairing = false;
-                    start(cur, 0, 1);
+                    stream_begin(a, line, streams[0], plan::kSingle, from_s[1], to_s[1], found_request[1], found_units[1], lane);
                 }
-                if (!pairing && oth.tiles && (cur.tiles == 0 || turn)) {   // the other group's turn
-                    const Stream x = cur;
-                    cur = oth;
-                    oth = x;
-                    id ^= 1;
-                }
-                turn = true;
+                if (!pairing && streams[id ^ 1].tiles) id ^= 1;    // the other group's turn
                 ids_v = ids;
-                if (cur.tiles) {
-                    ids = cur.take(a, line, walks[id], pieces[id], t, lane);
+                if (streams[id].tiles) {
+                    ids = stream_take(a, line, streams[id], t, lane);
                     t.flags |= pairing ? 3 : 1 << id;
                     t.piece += id * kPieces;
                 }
@@ -723,20 +887,22 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 if (!ok) break;
                 if (lane == 0) {
-                    ring[e] = t;
+                    ring[e].flags = t.flags;
+                    ring[e].token = t.token;
+                    ring[e].piece = t.piece;
                     mbar_arrive(tile_full(e));
                 }
+                // its keys, and the values of the tile before it
+                const bool end = t.flags & kTileEnd;
 #pragma unroll 1
-                for (int v = (t.flags & kTileEnd) ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v) ok = load(v ? ids_v : ids, v);
-                if (t.flags & kTileEnd) break;
+                for (int v = end ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v) {
+                    const uint32_t position = v ? (end ? 2 * g - 1 : 2 * g) : g == 0 ? 0 : 2 * g - 1;
+                    ok = load(v ? ids_v : ids, v, position);
+                    if (!ok) drain_copies(position);
+                }
+                if (end) break;
             }
-            if (flagged && lane == 0) atomicOr(c.flags, kFlagBadPage);
-            if (!ok) {
-                if (lane == 0) *abort = 1;
-                // copies in flight must land before the block's memory goes
-                for (uint32_t i = loaded > (uint32_t)kRaw ? loaded - kRaw : 0; i < loaded; ++i)
-                    mbar_wait(raw_full(i % kRaw), (i / kRaw) & 1, never, kDrainLimit);
-            }
+            if (!ok && lane == 0) *abort = 1;
         } else if (warp == kIssuer) {
             // ------------------------------------------- tensor-core products --
             // the whole warp walks the loop, so that addresses stay warp-uniform; one lane issues
@@ -800,7 +966,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             for (uint32_t g = 0; ok && !(now & kTileEnd); ++g) {
                 const uint32_t e = g % kRing;
                 if (!wait(tile_full(e), (g / kRing) & 1)) break;
-                const int nxt = ring[e].flags, next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
+                const int nxt = uniform(ring[e].flags), next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
                 const Place<kOps> ki = op;
                 if (next_mask) op.step();
                 const Place<kOps> vi = op;
@@ -814,11 +980,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     if (ok && (next_mask >> w & 1) && has == late) qk(w, ki, nxt);
                 }
                 if (!ok) break;
+                if (next_mask) commit(op_empty(ki.slot));
                 if (mask) {
                     commit(op_empty(vi.slot));
                     if (lane == 0) mbar_arrive(tile_empty((g - 1) % kRing));
                 }
-                if (next_mask) commit(op_empty(ki.slot));
                 now = nxt;
             }
             if (!ok) {
@@ -826,167 +992,15 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 commit(drain);
                 mbar_wait(drain, 0, never, kDrainLimit);
             }
-        } else if (warp >= kQueries) {
-            // ------------------------------------------------------------ q --
-            // (of single items; a pair's groups load their own)
-            uint32_t qc[2] = {0, 0};
-            bool ok = true;
-            for (uint32_t g = 0; ok; ++g) {
-                const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const int flags = ring[e].flags;
-                if (flags & kTileEnd) break;
-                if (flags & kTileFirst) {
-                    const int mask = flags & 3, w = mask == 2 ? 1 : 0;
-                    const uint32_t n = w ? qc[1] : qc[0];
-                    if (mask != 3) {
-                        if (!warp_wait(q_empty(w), (n & 1) ^ 1, abort)) { ok = false; break; }
-                        load_q<T, DP>(a, (&pieces[0][0])[ring[e].piece], 0, warp - kQueries, 2, group,
-                                      base + L::kQ + (uint32_t)w * L::kTileBytes,
-                                      reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(n & 1) * 128, lane);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane < 2) mbar_arrive(q_full(w));
-                    }
-                    qc[0] += mask & 1;
-                    qc[1] += mask >> 1;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tile_empty(e));
-            }
-            if (!ok && lane == 0) *abort = 1;
         } else {
             // ---------------------------------------------------- converters --
             regs_dec<64>();
-            const int t = tid - kConvertAt * 32;
-            const int cpr = D / 16;                      // 16-code chunks of a token
-            const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
-            Place<kOps> op = {0, 0};
-            Place<kRaw> raw = {0, 0};
-            uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
-            bool ok = true;
-            // One operand tile.  The lanes of a quarter warp take four chunks each of the lower and
-            // the upper 64 columns of an even and an odd row: neither their loads nor their
-            // stores (the swizzle takes even chunks of an odd row to odd places) meet in a bank.
-            auto convert = [&](bool is_v, int valid, int mask) {
-                if (!warp_wait(op_empty(op.slot), op.lap ^ 1, abort)) return false;
-                const uint32_t slot = raw.slot;
-                if (!warp_wait(raw_full(slot), raw.lap, abort)) return false;
-                const uint32_t src = base + L::kRawAt + slot * L::kRawBytes;
-                const uint32_t dst = base + L::kOp + op.slot * L::kTileBytes;
-                const int bad = raw_bad[slot];
-                const bool whole = valid >= plan::kTile && bad == 0;
-                const uint32_t raw_scale = src + 128u * DP;   // key scales, then value scales
-                const int exponent = scale_exponent(raw_scale + 512u, valid, bad, lane);
-                // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
-                // leaves the tile's largest below 2^15
-                const float v_unit = __uint_as_float((uint32_t)(127 + kVUp - exponent) << 23);
-                auto there = [&](int row) { return whole || (row < valid && !(bad >> (row >> 4) & 1)); };
-                auto row_factor = [&](int row, __half2 &hi, __half2 &lo) {
-                    const float v = ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)row), f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
-                    hi = __float2half2_rn(f);
-                    lo = __float2half2_rn(f - __low2float(hi));
-                };
-                auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch, __half2 hi, __half2 lo) {
-                    __half2 h[8];
-                    decode4<kFormat>(in.x, h[0], h[1]);
-                    decode4<kFormat>(in.y, h[2], h[3]);
-                    decode4<kFormat>(in.z, h[4], h[5]);
-                    decode4<kFormat>(in.w, h[6], h[7]);
-                    if (is_v) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = __hfma2(h[i], hi, __hmul2(h[i], lo));
-                    }
-                    const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
-                    const uint32_t at = dst + (ch >> 2) * (128u * 128u) + row * 128u, c8 = (ch & 3u) * 2u;
-                    st_shared_v4(at + ((c8 ^ (row & 7u)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
-                    st_shared_v4(at + (((c8 + 1u) ^ (row & 7u)) << 4), make_uint4(u[4], u[5], u[6], u[7]));
-                };
-                // nothing of a token that is not there
-                auto load = [&](int row, int ch, int width) {
-                    const uint4 in = ld_shared_v4(src + (uint32_t)(row * width + ch) * 16u);
-                    return there(row) ? in : make_uint4(0, 0, 0, 0);
-                };
-                if (!is_v) {
-                    // the tile's key scales (of scores in log2 units), for the softmax groups; a token whose
-                    // value scale (or page) is no number carries its NaN in the key's alone: where it is
-                    // masked, its zero values must not become 0 times NaN
-                    float ks = 0.f;
-                    if (t < min(valid, plan::kTile))
-                        ks = there(t) && ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)t) <= 3.4028235e38f
-                                 ? ld_shared_f32(raw_scale + 4u * (uint32_t)t) * up
-                                 : __int_as_float(0x7fffffff);
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (!(mask >> w & 1) || t >= plan::kTile) continue;
-                        const uint32_t i = (group_tiles >> (16 * w)) % kScaleSlots;
-                        st_shared_f32(base + L::kScale + ((uint32_t)(w * kScaleSlots) + i) * 512u + 4u * (uint32_t)t, ks);
-                        if (t == 0) exponents[w][i] = exponent;
-                    }
-                    // (counts of 16 bits: the carry of the lower is kept out of the upper)
-                    group_tiles = ((group_tiles + (mask & 1)) & 0xffffu) | ((group_tiles & 0xffff0000u) + ((uint32_t)(mask >> 1) << 16));
-                }
-                if (D == DP) {
-                    constexpr int kSteps = DP / 64;     // two chunks each: of one row (D = 128), of two rows
-                    const int odd = t >> 2 & 1;
-#pragma unroll 1
-                    for (int step = 0; step < kSteps; ++step) {
-                        uint4 in[2];
-                        __half2 hi[2] = {}, lo[2] = {};
-                        auto row_of = [&](int i) {
-                            return DP == 128 ? 2 * ((t >> 3) + 32 * step) + odd : (t >> 2) + 64 * i;
-                        };
-                        auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            in[i] = load(row_of(i), chunk_of(i), DP / 16);
-                            if (is_v && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
-                        }
-                        if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
-                        if (step + 1 == kSteps) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(raw_empty(slot));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            decode_store(in[i], (uint32_t)row_of(i), (uint32_t)chunk_of(i), hi[i], lo[i]);
-                    }
-                } else {
-                    for (int i = t; i < 128 * cpr; i += 32 * kConvertWarps) {
-                        const int row = i / cpr;
-                        __half2 hi = {}, lo = {};
-                        if (is_v) row_factor(row, hi, lo);
-                        decode_store(load(row, i - row * cpr, cpr), (uint32_t)row, (uint32_t)(i - row * cpr), hi, lo);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(raw_empty(slot));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(op_full(op.slot));
-                op.step();
-                raw.step();
-                return true;
-            };
-            int valid = 0;
-            for (uint32_t g = 0; ok; ++g) {
-                const uint32_t e = g % kRing;
-                if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) { ok = false; break; }
-                const Tile tile = ring[e];
-                const int valid_v = valid;
-                const bool end = tile.flags & kTileEnd;
-                if (!end) valid = (&pieces[0][0])[tile.piece].len - tile.token;
-#pragma unroll 1
-                for (int v = end ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v)
-                    ok = convert(v, v ? valid_v : valid, tile.flags & 3);
-                if (!ok) break;
-                if (tile.flags & kTileEnd) break;
-                if (lane == 0) mbar_arrive(tile_empty(e));
-            }
+            const bool ok = warp < kConvertAt + kTeamWarps ? convert_all(std::false_type{}) : convert_all(std::true_type{});
             if (!ok && lane == 0) *abort = 1;
         }
     } else {
         // -------------------------------------------------------------- softmax --
+        // the launch's 576 x 96 registers, shared out: 128 a softmax thread, 64 a converter's, 96 the other two warps'
         regs_inc<128>();
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
@@ -995,18 +1009,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         uint32_t n = 0;       // tiles of the group so far
         for (uint32_t k = 0; ok; ++k) {
             if (!warp_wait(piece_full(w, k % kRing), (k / kRing) & 1, abort)) { ok = false; break; }
-            const int told = group_pieces[w][k % kRing], flags = told >> 16;
+            const int told = uniform(group_pieces[w][k % kRing]), flags = told >> 16;
             if (flags & kTileEnd) break;
-            const Piece &p = (&pieces[0][0])[told & 0xffff];
+            const Piece &p = piece_at(told & 0xffff);
             const bool pair = (flags & 3) == 3;
-            float *qscale = reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(k & 1) * 128;
-            const int rows = pair ? min(p.rows - w * 128, 128) : p.rows;
+            const float *qscale = reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)(k & 1) * 128;
+            const int rows = uniform(pair ? min(p.rows - w * 128, 128) : p.rows);
             const int mt = pair ? w * 128 + row : row;       // row of the row tile
             const bool live = row < rows, warp_live = (warp & 3) * 32 < rows;
             const int m = p.m0 + mt, blk = m / group;
             // what this row sees of the list: tokens below `sees`, and with a mask word those of its bits
-            const int ctx = p.ctx, tiles = p.tiles;
-            int sees = ctx, token = p.first * plan::kTile;
+            const int ctx = uniform(p.ctx), tiles = uniform(p.tiles);
+            int sees = ctx, token = uniform(p.first) * plan::kTile;
             uint64_t word = 0;
             if (p.request >= 0) {
                 if (a.row_mask) {
@@ -1015,13 +1029,6 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 } else {
                     sees = a.mask == DSPARK_MASK_CAUSAL ? ctx + min(blk, p.n - 1) + 1 : p.len;
                 }
-            }
-            if (pair) {
-                if (!warp_wait(q_empty(w), (k & 1) ^ 1, abort)) { ok = false; break; }
-                load_q<T, DP>(a, p, w * 128, warp & 3, 4, group, base + L::kQ + (uint32_t)w * L::kTileBytes, qscale, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full(w));
             }
             float r = -INFINITY, l = 0.f, lack = 1.f;
             bool rescale_q = false;
@@ -1037,7 +1044,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             if (warp_live) {
                 const uint32_t ss = n % kScaleSlots;
                 const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 128;
-                const int lv = exponents[w][ss];
+                const int lv = uniform(exponents[w][ss]);
                 const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
                 const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
                 float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
