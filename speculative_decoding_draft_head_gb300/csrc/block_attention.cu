@@ -19,19 +19,21 @@
 // So the inner terms take two roundings of 2^-11, everything else is fp32.
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
-// 128 tokens a tile.  Roles (18 warps):
+// 128 tokens a tile.  Roles (20 warps):
 //   0-7    two softmax groups of 128 threads, a thread per row (TMEM lane)
 //   8-11   queries and keys to fp16 operands in the swizzled layout;  12-15  values
-//   16     producer: plans tiles, loads codes and scales (bulk copies)
+//   16     plans: rounds of up to four tiles for each group
 //   17     issues the tensor-core products
+//   18     loads codes, 19 scales (bulk copies)
 // A pair tile's keys and values serve both groups; single tiles alternate
 // between the groups' own items.  Operands are loaded, converted and used in
-// one order, K0 K1 V0 K2 V1 ..: keys one tile ahead, so that a group's scores
-// are ready while the other group's softmax runs.  Every ring is filled in this
-// order by one warp or freed in it, and the two converter teams wait for their
-// operand's place before they look for its codes: so no wait is more than one
-// lap of a ring away from the phase that it tests, whose parity would deceive it.
-// Every wait is bounded.
+// one order: of pairs K0 V0 K1 V1 .., so that a tile's values are converted
+// under the products of the tile before; of singles K0 K1 V0 K2 V1 .., keys one
+// tile ahead, so that a group's scores are ready while the other group's softmax
+// runs.  Every ring is filled in this order or freed in it, and the converter
+// teams wait for their operand's place before they look for its codes: so no
+// wait is more than one lap of a ring away from the phase that it tests, whose
+// parity would deceive it.  Every wait is bounded.
 #include <type_traits>
 
 #include "attention_plan.h"
@@ -43,11 +45,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 576;
-// warps of the roles (the softmax groups are warps 0 .. 7)
-constexpr int kConvertAt = 8, kTeamWarps = 4, kProducer = 16, kIssuer = 17;
+constexpr int kThreads = 640;
+// warps of the roles (the softmax groups are warps 0 .. 7, the scales' loader the last)
+constexpr int kConvertAt = 8, kTeamWarps = 4, kPlanner = 16, kIssuer = 17, kCodes = 18;
 constexpr int kCtas = kNumSMs;
-constexpr int kRing = 8;          // tiles planned ahead
+constexpr int kRing = 8;          // pieces of a group told ahead
+constexpr int kRounds = 4;        // rounds planned ahead
 constexpr int kScaleSlots = 4;    // tiles of a group whose key scales are held
 constexpr uint32_t kSpinLimit = 2000000000u;    // ~1 s of clock cycles (below the 32-bit clock's lap)
 constexpr long long kDrainLimit = 200000000LL;  // ~0.1 s: products in flight after a timeout
@@ -94,8 +97,28 @@ struct Piece {
     int out;            // kDirect, kFirst, kContinued
     int pad;
 };
-struct Tile {
-    int flags, token, piece, pad;   // first token; where its piece is
+// Up to four tiles of each group, taken in turns: 0 of the first, 0 of the
+// second, 1 of the first ..; pairs as tiles of the first.
+struct Round {
+    int flags;                    // kRoundPair, kRoundEnd; bits 2 s, 2 s + 1: the first / last tile of stream s's piece is here
+    int n[2], token[2], piece[2]; // of the streams: tiles, first token, place of the piece
+    uint32_t chunks[2][32];       // where the tokens are, 16 a chunk, 8 chunks a tile
+};
+enum { kRoundPair = 16, kRoundEnd = 32 };
+
+// The order of operands: places of the keys of tile after tile, and of the values
+// that go with them (of the same pair, or of the single before).
+struct Order {
+    uint32_t tile, k, v;
+    bool has_v, single;           // values at `v`; the last tile was a single
+    __device__ __forceinline__ void step(int flags) {
+        const bool end = flags & kTileEnd, pair = (flags & 3) == 3;
+        k = 2 * tile - (!pair && single ? 1 : 0);
+        v = pair ? 2 * tile + 1 : end ? 2 * tile - 1 : 2 * tile;
+        has_v = pair || single;
+        single = !pair;
+        ++tile;
+    }
 };
 
 // Device workspace: where partial results go
@@ -193,15 +216,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // A value that all lanes hold, in the form the compiler knows to be so.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// Place in a ring of n slots, with the parity of the lap.
-template <int n>
-struct Place {
-    uint32_t slot, lap;
-    __device__ __forceinline__ void step() {
-        if (++slot == n) slot = 0, lap ^= 1;
-    }
-};
 
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() {
@@ -354,15 +368,14 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
 // one a lane, their pages loaded four tiles before they are needed.
 constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 // Pieces a stream's tiles refer to: a slot is written again only after every
-// tile of its piece has left the ring (the next piece is planned while the last
+// tile of its piece has left the rings (the next piece is planned while the last
 // one's tiles are taken, hence more than kRing slots).
 constexpr int kPieces = 2 * kRing;
 // (In shared memory, as there are two and the loop over tiles should be one.)
 struct Stream {
-    int j, tiles, next_tiles, token;   // tile of the piece, its tiles, the next piece's; the tile's first token
+    int j, tiles;                      // next tile of the piece, its tiles (0: no more pieces)
     uint32_t count;                    // pieces begun
     int page[32], off[32];             // of the next four tiles' chunks, a lane each
-    uint32_t window[32];               // chunk numbers of the current four tiles
     Walk walk;
     Piece slots[kPieces];
 
@@ -385,49 +398,39 @@ __device__ __noinline__ void stream_begin(const AttentionArgs &a, const Line &z,
     Piece &p = s.slots[s.count % kPieces];
     const int tiles = walk_next(a, z, s.walk, p, lane);
     s.tiles = tiles;
-    s.next_tiles = s.j = 0;
+    s.j = 0;
     if (tiles) s.load_pages(a, p, 0, lane);
     __syncwarp();
 }
 
-// the next tile (s.tiles > 0): its chunk numbers in lanes 0 .. 7 (and again in 8 .. 15 and so on)
-__device__ __noinline__ uint32_t stream_take(const AttentionArgs &a, const Line &z, Stream &s, Tile &t, int lane) {
-    const int j = s.j, tiles = s.tiles;
+// up to four tiles of the stream (s.tiles > 0) to stream `id` of a round; the round's bits of it
+__device__ __noinline__ int stream_round(const AttentionArgs &a, const Line &z, Stream &s, Round &r, int id, int lane) {
+    const int j = s.j, tiles = s.tiles, n = min(tiles - j, 4);
     const uint32_t count = s.count;
-    int token = s.token, next_tiles = s.next_tiles;
-    __syncwarp();
-    if ((j & 3) == 0) {
-        const int off = s.off[lane], page = s.page[lane];
-        s.window[lane] = off < 0 ? kNoChunk
+    const int off = s.off[lane], page = s.page[lane];
+    r.chunks[id][lane] = off < 0 ? kNoChunk
                          : (page < 0 || page >= a.cache.n_pages)
                              ? kBadChunk
                              : (uint32_t)page * (uint32_t)(a.cache.n_kv_heads * (a.cache.page_size / 16)) + (uint32_t)off;
-        const Piece *p = s.slots + count % kPieces;
-        if (j == 0) token = p->first * plan::kTile;
-        int from = j + 4;
-        if (from >= tiles) {
-            next_tiles = walk_next(a, z, s.walk, s.slots[(count + 1) % kPieces], lane);
-            p = s.slots + (count + 1) % kPieces;
-            from = 0;
-        }
-        if (from || next_tiles) s.load_pages(a, *p, from, lane);
-        __syncwarp();
+    const bool last = j + n == tiles;
+    const Piece *p = s.slots + count % kPieces;
+    if (lane == 0) {
+        r.n[id] = n;
+        r.token[id] = (p->first + j) * plan::kTile;
+        r.piece[id] = id * kPieces + (int)(count % kPieces);
     }
-    const uint32_t ids = s.window[((j & 3) << 3) + (lane & 7)];
-    t.token = token;
-    t.piece = (int)(count % kPieces);
-    t.flags = (j == 0 ? kTileFirst : 0) | (j + 1 == tiles ? kTileLast : 0);
-    const bool last = j + 1 == tiles;
     __syncwarp();
-    s.token = token + plan::kTile;
-    s.next_tiles = next_tiles;
-    s.j = last ? 0 : j + 1;
+    int next = tiles;
     if (last) {
-        s.tiles = next_tiles;
-        s.count = count + 1;
+        p = s.slots + (count + 1) % kPieces;
+        next = walk_next(a, z, s.walk, s.slots[(count + 1) % kPieces], lane);
     }
+    s.j = last ? 0 : j + n;
+    s.tiles = next;
+    s.count = count + (last ? 1 : 0);
+    if (next) s.load_pages(a, *p, last ? 0 : j + n, lane);
     __syncwarp();
-    return ids;
+    return (j == 0 ? 1 << (2 * id) : 0) | (last ? 2 << (2 * id) : 0);
 }
 
 // ------------------------------------------------------------------------- q --
@@ -501,10 +504,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     using L = Layout<DP>;
     constexpr int kOps = L::kOps, kRaw = L::kRaw;
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 6 * kRing + 16];
+    __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kOps + 4 * kRing + 2 * kRounds + 16];
     __shared__ int group_pieces[2][kRing];          // pieces of the softmax groups: slot, flags
     __shared__ Stream streams[2];
-    __shared__ __align__(16) Tile ring[kRing];      // tiles, for the other roles
+    __shared__ Round rounds[kRounds];
     __shared__ int exponents[2][kScaleSlots];       // of the value scales of the groups' tiles
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
@@ -529,9 +532,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     auto op_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + kOps + i); };
     auto piece_full = [&](int w, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)w * kRing + i); };
     auto piece_empty = [&](int w, uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + (uint32_t)(w + 2) * kRing + i); };
-    auto tile_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 4 * kRing + i); };
-    auto tile_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 5 * kRing + i); };
-    const uint32_t bar1 = bar0 + 8u * (uint32_t)(2 * kRaw + 2 * kOps + 6 * kRing);
+    auto round_full = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 4 * kRing + i); };
+    auto round_empty = [&](uint32_t i) { return bar0 + 8u * (2 * kRaw + 2 * kOps + 4 * kRing + kRounds + i); };
+    const uint32_t bar1 = bar0 + 8u * (uint32_t)(2 * kRaw + 2 * kOps + 4 * kRing + 2 * kRounds);
     auto q_full = [&](int i) { return bar1 + 8u * (uint32_t)i; };
     auto q_empty = [&](int i) { return bar1 + 8u * (uint32_t)(2 + i); };
     auto s_full = [&](int i) { return bar1 + 8u * (uint32_t)(4 + i); };
@@ -541,12 +544,11 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     const uint32_t drain = bar1 + 8u * 12u;
 
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 1), mbar_init(raw_empty(i), kTeamWarps);
+        for (int i = 0; i < kRaw; ++i) mbar_init(raw_full(i), 2), mbar_init(raw_empty(i), kTeamWarps);
         for (int i = 0; i < kOps; ++i) mbar_init(op_full(i), kTeamWarps), mbar_init(op_empty(i), 1);
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(tile_full(i), 1), mbar_init(tile_empty(i), 1 + 2 * kTeamWarps);
+        for (int i = 0; i < kRounds; ++i) mbar_init(round_full(i), 1), mbar_init(round_empty(i), 3 + 2 * kTeamWarps);
+        for (int i = 0; i < kRing; ++i)
             for (int w = 0; w < 2; ++w) mbar_init(piece_full(w, i), 1), mbar_init(piece_empty(w, i), 4);
-        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), kTeamWarps), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
@@ -651,11 +653,40 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform(misc[2]);
 
+    // Walks the planned tiles: body(flags, stream, number in the round, round) for each, and for the end;
+    // false when it or a wait gives up.
+    auto for_tiles = [&](auto body) {
+#pragma unroll 1
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t e = k % kRounds;
+            if (!warp_wait(round_full(e), (k / kRounds) & 1, abort)) return false;
+            const Round &r = rounds[e];
+            const int bits = uniform(r.flags);
+            const int n0 = uniform(r.n[0]), n1 = uniform(r.n[1]);
+            const int turns = (bits & kRoundEnd) ? 1 : 2 * max(n0, n1);
+#pragma unroll 1
+            for (int x = 0; x < turns; ++x) {
+                const int id = x & 1, i = x >> 1, n = id ? n1 : n0;
+                int flags = kTileEnd;
+                if (!(bits & kRoundEnd)) {
+                    if (i >= n) continue;
+                    flags = ((bits & kRoundPair) ? 3 : 1 << id) | (i == 0 && (bits >> (2 * id) & 1) ? kTileFirst : 0) |
+                            (i + 1 == n && (bits >> (2 * id + 1) & 1) ? kTileLast : 0);
+                }
+                if (!body(flags, id, i, r)) return false;
+            }
+            if (bits & kRoundEnd) return true;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(round_empty(e));
+        }
+    };
+
     // Loads the keys or values of a tile, chunk `mine` in lanes 0 .. 7 (and again in 8 .. 15 and so
-    // on), to place `position` of the order of operands, in runs of tokens that share a page.  (Copies
-    // by the warp's own cp.async, 512 bytes at a time, held it up: 2300 clocks a tile.)
+    // on), to place `position` of the order of operands, in runs of tokens that share a page: their
+    // codes or (another warp) their scales.  (Copies by the warp's own cp.async, 512 bytes at a time,
+    // held it up: 2300 clocks a tile.)
     const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
-    auto load = [&](uint32_t mine, bool is_v, uint32_t position) {
+    auto load = [&](uint32_t mine, bool is_v, uint32_t position, bool codes) {
         const int i = lane & 7;
         const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
         const bool good = i < runs && id < kBadChunk;
@@ -665,8 +696,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         if (!warp_wait(raw_empty(slot), ((position / kRaw) & 1) ^ 1, abort)) return false;
         const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
         if (lane == 0) {
-            raw_bad[slot] = (int)bad;
-            mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (is_v ? D + 4 : D + 8)));
+            if (codes) raw_bad[slot] = (int)bad;
+            mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (codes ? D : is_v ? 4 : 8)));
         }
         __syncwarp();
         const bool leader = elect_one();
@@ -675,14 +706,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const uint32_t from = (uint32_t)uniform((int)__shfl_sync(0xffffffffu, mine, r * (run / 16)));
             if (from >= kBadChunk || !leader) continue;
             const uint64_t first = (uint64_t)from * 16u;      // head row of the run's first token
-            bulk_load(at + (uint32_t)(r * run * D), static_cast<const unsigned char *>(is_v ? c.v : c.k) + first * (uint32_t)D,
-                      (uint32_t)(run * D), raw_full(slot));
-            bulk_load(at + 128u * DP + 512u + (uint32_t)(r * run * 4), c.v_scale + first, (uint32_t)(run * 4), raw_full(slot));
-            if (!is_v)
-                bulk_load(at + 128u * DP + (uint32_t)(r * run * 4), c.k_scale + first, (uint32_t)(run * 4), raw_full(slot));
+            if (codes) {
+                bulk_load(at + (uint32_t)(r * run * D),
+                          static_cast<const unsigned char *>(is_v ? c.v : c.k) + first * (uint32_t)D, (uint32_t)(run * D),
+                          raw_full(slot));
+            } else {
+                const uint32_t to = at + 128u * DP + (uint32_t)(r * run * 4), bytes = (uint32_t)(run * 4);
+                bulk_load(to + 512u, c.v_scale + first, bytes, raw_full(slot));
+                if (!is_v) bulk_load(to, c.k_scale + first, bytes, raw_full(slot));
+            }
         }
         __syncwarp();
-        if (bad && lane == 0) atomicOr(c.flags, kFlagBadPage);
+        if (codes && bad && lane == 0) atomicOr(c.flags, kFlagBadPage);
         return true;
     };
     // a loader that gives up waits for the last copies: they must land before the block's memory goes
@@ -701,32 +736,23 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
         uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
         uint32_t group_pieces_seen = 0;              // parity of the groups' pieces
-        int valid = 0;
-        for (uint32_t g = 0;; ++g) {
-            const uint32_t e = g % kRing;
-            if (!warp_wait(tile_full(e), (g / kRing) & 1, abort)) return false;
-            const int flags = uniform(ring[e].flags), valid_v = valid;
-            const bool end = flags & kTileEnd;
-            if (kIsV) {
-                if (!end) valid = uniform(piece_at(ring[e].piece).len - ring[e].token);
-                __syncwarp();
-                if (!end && lane == 0) mbar_arrive(tile_empty(e));
-                if (g == 0) {
-                    if (end) return true;
-                    continue;
-                }
-            } else {
-                if (end) return true;
-                const Piece &p = piece_at(uniform(ring[e].piece));
-                valid = uniform(p.len) - uniform(ring[e].token);
-                if (flags & kTileFirst) {
+        int valid = 0;                               // tokens of the tile that exist (128 or more: all)
+        Order order = {0, 0, 0, false, false};
+        return for_tiles([&](int flags, int id, int i, const Round &r) {
+            const bool end = flags & kTileEnd, pair = (flags & 3) == 3;
+            const int valid_before = valid;
+            order.step(flags);
+            if (!end) {
+                const Piece &p = piece_at(uniform(r.piece[id]));
+                valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
+                if (!kIsV && (flags & kTileFirst)) {
                     // the piece's queries
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         if (!(flags >> w & 1)) continue;
                         const uint32_t seen = group_pieces_seen >> w & 1;
                         if (!warp_wait(q_empty(w), seen ^ 1, abort)) return false;
-                        load_q<T, DP>(a, p, (flags & 3) == 3 ? w * 128 : 0, warp - kConvertAt, kTeamWarps, group,
+                        load_q<T, DP>(a, p, pair ? w * 128 : 0, warp - kConvertAt, kTeamWarps, group,
                                       base + L::kQ + (uint32_t)w * L::kTileBytes,
                                       reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)seen * 128, lane);
                         group_pieces_seen ^= 1u << w;
@@ -736,9 +762,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     }
                 }
             }
-            // the operand: keys of tile g, or values of tile g - 1
-            const int there_are = kIsV ? valid_v : valid;
-            const uint32_t position = kIsV ? (end ? 2 * g - 1 : 2 * g) : (g == 0 ? 0 : 2 * g - 1);
+            if (kIsV ? !order.has_v : end) return true;
+            // the operand: the tile's keys, or the values whose turn it is
+            const int there_are = kIsV && !pair ? valid_before : valid;
+            const uint32_t position = kIsV ? order.v : order.k;
             const uint32_t slot = position % kRaw, op = position % kOps;
             if (!warp_wait(op_empty(op), ((position / kOps) & 1) ^ 1, abort)) return false;
             if (!warp_wait(raw_full(slot), (position / kRaw) & 1, abort)) return false;
@@ -833,75 +860,79 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(op_full(op));
-                if (!kIsV) mbar_arrive(tile_empty(e));
-            }
-            if (kIsV && end) return true;
-        }
+            if (lane == 0) mbar_arrive(op_full(op));
+            return true;
+        });
     };
 
     if (warp >= kConvertAt) {
-        if (warp == kProducer) {
-            // ------------------------------------------------------ producer --
+        if (warp == kPlanner) {
+            // -------------------------------------------------------- planner --
             // pairs, then the first group's singles, are stream 0's tiles, the second group's singles stream 1's
             if (lane < 2) streams[lane].count = 0;
             __syncwarp();
             bool ok = true, pairing = true;
-            int id = 0;             // the stream of the last tile
 #pragma unroll 1
             for (int i = 2; i >= 0; i -= 2)
                 stream_begin(a, line, streams[i >> 1], i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
                              found_units[i], lane);
-            uint32_t ids = kNoChunk, ids_v = kNoChunk;
             uint32_t taken = 0;                  // pieces given to the groups, modulo 2^16 (a multiple of the ring's laps)
-            for (uint32_t g = 0; ok; ++g) {
-                Tile t;
-                t.flags = kTileEnd;
-                t.token = t.piece = 0;
-                const uint32_t e = g % kRing;
-                if (!warp_wait(tile_empty(e), ((g / kRing) & 1) ^ 1, abort)) { ok = false; break; }
+#pragma unroll 1
+            for (uint32_t k = 0; ok; ++k) {
                 if (pairing && streams[0].tiles == 0) {
                     pairing = false;
                     stream_begin(a, line, streams[0], plan::kSingle, from_s[1], to_s[1], found_request[1], found_units[1], lane);
                 }
-                if (!pairing && streams[id ^ 1].tiles) id ^= 1;    // the other group's turn
-                ids_v = ids;
-                if (streams[id].tiles) {
-                    ids = stream_take(a, line, streams[id], t, lane);
-                    t.flags |= pairing ? 3 : 1 << id;
-                    t.piece += id * kPieces;
-                }
-                // a new piece (or the end) is told to the groups it is for
-                const int mask = (t.flags & kTileEnd) ? 3 : (t.flags & kTileFirst) ? t.flags & 3 : 0;
+                const uint32_t e = k % kRounds;
+                if (!warp_wait(round_empty(e), ((k / kRounds) & 1) ^ 1, abort)) { ok = false; break; }
+                Round &r = rounds[e];
+                int bits = pairing ? kRoundPair : 0;
+                if (lane < 2) r.n[lane] = 0;
+                __syncwarp();
 #pragma unroll 1
-                for (int w = 0; w < 2; ++w) {
-                    if (!(mask >> w & 1)) continue;
+                for (int id = 0; id < (pairing ? 1 : 2); ++id)
+                    if (streams[id].tiles) bits |= stream_round(a, line, streams[id], r, id, lane);
+                __syncwarp();
+                const bool end = r.n[0] + r.n[1] == 0;
+                // a new piece (or the end) is told to the groups it is for
+#pragma unroll 1
+                for (int w = 0; w < 2 && ok; ++w) {
+                    const int id = pairing ? 0 : w;
+                    if (!end && !(bits >> (2 * id) & 1)) continue;
                     const uint32_t n = w ? taken >> 16 : taken & 0xffffu, i = n % kRing;
-                    if (ok) ok = warp_wait(piece_empty(w, i), ((n / kRing) & 1) ^ 1, abort);
+                    ok = warp_wait(piece_empty(w, i), ((n / kRing) & 1) ^ 1, abort);
                     if (ok && lane == 0) {
-                        group_pieces[w][i] = t.piece | t.flags << 16;
+                        group_pieces[w][i] = end ? kTileEnd << 16 : r.piece[id] | (pairing ? 3 : 1 << w) << 16;
                         mbar_arrive(piece_full(w, i));
                     }
                     taken = w ? taken + 0x10000u : (taken & 0xffff0000u) | ((taken + 1) & 0xffffu);
                 }
                 if (!ok) break;
                 if (lane == 0) {
-                    ring[e].flags = t.flags;
-                    ring[e].token = t.token;
-                    ring[e].piece = t.piece;
-                    mbar_arrive(tile_full(e));
-                }
-                // its keys, and the values of the tile before it
-                const bool end = t.flags & kTileEnd;
-#pragma unroll 1
-                for (int v = end ? 1 : 0; v < (g > 0 ? 2 : 1) && ok; ++v) {
-                    const uint32_t position = v ? (end ? 2 * g - 1 : 2 * g) : g == 0 ? 0 : 2 * g - 1;
-                    ok = load(v ? ids_v : ids, v, position);
-                    if (!ok) drain_copies(position);
+                    r.flags = end ? kRoundEnd : bits;
+                    mbar_arrive(round_full(e));
                 }
                 if (end) break;
             }
+            if (!ok && lane == 0) *abort = 1;
+        } else if (warp >= kCodes) {
+            // -------------------------------------------------------- loaders --
+            uint32_t ids = kNoChunk;
+            Order order = {0, 0, 0, false, false};
+            const bool ok = for_tiles([&](int flags, int id, int i, const Round &r) {
+                const bool end = flags & kTileEnd, pair = (flags & 3) == 3;
+                const uint32_t before = ids;
+                order.step(flags);
+                if (!end) ids = r.chunks[id][i * 8 + (lane & 7)];
+#pragma unroll 1
+                for (int v = end ? 1 : 0; v < (order.has_v ? 2 : 1); ++v) {
+                    const uint32_t position = v ? order.v : order.k;
+                    if (load(v && !pair ? before : ids, v, position, warp == kCodes)) continue;
+                    drain_copies(position);
+                    return false;
+                }
+                return true;
+            });
             if (!ok && lane == 0) *abort = 1;
         } else if (warp == kIssuer) {
             // ------------------------------------------- tensor-core products --
@@ -911,7 +942,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const uint32_t id_qk = idesc_f16_f32(128, 128, false), id_pv = idesc_f16_f32(128, D, true);
             constexpr uint32_t kAtom = 128 * 128;  // bytes of a 64-column atom of a 128-row tile
             const int k_steps = D / 16;
-            Place<kOps> op = {0, 0};
+            Order order = {0, 0, 0, false, false};
             uint32_t laps = 0;      // bits: parity of the next q, P and result of the groups; 6, 7: a group has had a result
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -923,14 +954,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (leader) umma_commit(bar);
             };
             // scores of group w for a tile: waits for the item's q with its first tile, gives it back with its last
-            auto qk = [&](int w, Place<kOps> k, int flags) {
+            auto qk = [&](int w, uint32_t k, int flags) {
                 if (flags & kTileFirst) {
                     if (!wait(q_full(w), laps >> w & 1)) return;
                     laps ^= 1u << w;
                 }
-                if (!wait(op_full(k.slot), k.lap)) return;
+                if (!wait(op_full(k % kOps), (k / kOps) & 1)) return;
                 const uint32_t qa = (base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16;
-                const uint32_t ka = (base + L::kOp + k.slot * L::kTileBytes) >> 4 | 1u << 16;
+                const uint32_t ka = (base + L::kOp + (k % kOps) * L::kTileBytes) >> 4 | 1u << 16;
                 const uint32_t d = tmem + kColS + 128u * (uint32_t)w;
                 if (leader) {
 #pragma unroll
@@ -942,14 +973,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     if (flags & kTileLast) umma_commit(q_empty(w));
                 }
             };
-            auto pv = [&](int w, Place<kOps> v, int flags) {
+            auto pv = [&](int w, uint32_t v, int flags) {
                 if (flags & kTileFirst) {
                     if ((laps >> (6 + w) & 1) && !wait(o_free(w), (laps >> (4 + w) & 1) ^ 1)) return;
                     laps = (laps ^ 1u << (4 + w)) | 1u << (6 + w);
                 }
                 if (!wait(p_ready(w), laps >> (2 + w) & 1)) return;
                 laps ^= 1u << (2 + w);
-                const uint32_t va = (base + L::kOp + v.slot * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
+                const uint32_t va = (base + L::kOp + (v % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
                 const uint32_t d = tmem + kColO + 128u * (uint32_t)w, pa = tmem + kColS + 128u * (uint32_t)w;
                 if (leader) {
 #pragma unroll
@@ -962,31 +993,29 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             // Step g: the scores of tile g as soon as a group is free for them (those of the groups that
             // tile g - 1 does not use before tile g - 1's P is waited for), and tile g - 1's output.
             int now = 0;
-#pragma unroll 1
-            for (uint32_t g = 0; ok && !(now & kTileEnd); ++g) {
-                const uint32_t e = g % kRing;
-                if (!wait(tile_full(e), (g / kRing) & 1)) break;
-                const int nxt = uniform(ring[e].flags), next_mask = (nxt & kTileEnd) ? 0 : nxt & 3, mask = now & 3;
-                const Place<kOps> ki = op;
-                if (next_mask) op.step();
-                const Place<kOps> vi = op;
-                if (mask) op.step();
+            uint32_t pair_v = 0;    // place of the last pair's values
+            const bool walked = for_tiles([&](int nxt, int, int, const Round &) {
+                const int next_mask = nxt & 3, mask = now & 3;
+                order.step(nxt);
+                const uint32_t ki = order.k, vi = mask == 3 ? pair_v : order.v;
+                if (next_mask == 3) pair_v = order.v;
                 // passes: 0 and 1 the early scores of the groups, 2 and 3 their outputs and later scores
 #pragma unroll 1
                 for (int i = 0; i < 4 && ok; ++i) {
                     const int w = i & 1, has = mask >> w & 1, late = i >> 1;
-                    if (i == 2 && mask && !wait(op_full(vi.slot), vi.lap)) break;
+                    if (i == 2 && mask && !wait(op_full(vi % kOps), (vi / kOps) & 1)) break;
                     if (late && has) pv(w, vi, now);
                     if (ok && (next_mask >> w & 1) && has == late) qk(w, ki, nxt);
                 }
-                if (!ok) break;
-                if (next_mask) commit(op_empty(ki.slot));
-                if (mask) {
-                    commit(op_empty(vi.slot));
-                    if (lane == 0) mbar_arrive(tile_empty((g - 1) % kRing));
-                }
+                if (!ok) return false;
+                // (in the order of their places)
+                if (mask == 3) commit(op_empty(vi % kOps));
+                if (next_mask) commit(op_empty(ki % kOps));
+                if (mask == 1 || mask == 2) commit(op_empty(vi % kOps));
                 now = nxt;
-            }
+                return true;
+            });
+            ok = ok && walked;
             if (!ok) {
                 if (lane == 0) *abort = 1;
                 commit(drain);
@@ -1000,7 +1029,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         }
     } else {
         // -------------------------------------------------------------- softmax --
-        // the launch's 576 x 96 registers, shared out: 128 a softmax thread, 64 a converter's, 96 the other two warps'
+        // the launch's 640 x 96 registers, shared out: 128 a softmax thread, 64 a converter's, 96 the other four warps'
         regs_inc<128>();
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
