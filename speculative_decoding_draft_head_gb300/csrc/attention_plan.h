@@ -36,7 +36,7 @@ constexpr int kTileRows = 256;    // rows of a row tile
 
 enum Class { kPair = 0, kSingle = 1 };
 DSPARK_HD int tile_units(int cls) { return cls == kPair ? 8 : 5; }
-DSPARK_HD int item_units(int cls) { return cls == kPair ? 12 : 6; }
+DSPARK_HD int item_units(int cls) { return cls == kPair ? 18 : 16; }
 
 DSPARK_HD int row_tiles(int rows) { return (int)(((int64_t)rows + kTileRows - 1) / kTileRows); }
 DSPARK_HD int token_tiles(int tokens) { return (int)(((int64_t)tokens + kTile - 1) / kTile); }

@@ -550,7 +550,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         for (int i = 0; i < kRing; ++i)
             for (int w = 0; w < 2; ++w) mbar_init(piece_full(w, i), 1), mbar_init(piece_empty(w, i), 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), kTeamWarps), mbar_init(q_empty(i), 1);
+            mbar_init(q_full(i), 2 * kTeamWarps), mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1), mbar_init(p_ready(i), 4);
             mbar_init(o_full(i), 1), mbar_init(o_free(i), 4);
         }
@@ -726,13 +726,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             mbar_wait(raw_full((position - i) % kRaw), ((position - i) / kRaw) & 1, never, kDrainLimit);
     };
 
-    // One team of converters: the keys (and queries) or the values of all tiles.  The lanes of a quarter
+    // One team of converters: the keys or the values of all tiles, and half of the queries.  The lanes of a quarter
     // warp take four chunks each of the lower and the upper 64 columns of an even and an odd row:
     // neither their loads nor their stores (the swizzle takes even chunks of an odd row to odd places)
     // meet in a bank.
-    auto convert_all = [&](auto team) {
-        constexpr bool kIsV = decltype(team)::value;
-        const int t = tid - (kConvertAt + (kIsV ? kTeamWarps : 0)) * 32;
+    auto convert_all = [&](const bool is_v) {
+        const int t = (tid - kConvertAt * 32) & (kTeamWarps * 32 - 1);
         const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
         uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
         uint32_t group_pieces_seen = 0;              // parity of the groups' pieces
@@ -745,14 +744,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             if (!end) {
                 const Piece &p = piece_at(uniform(r.piece[id]));
                 valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
-                if (!kIsV && (flags & kTileFirst)) {
-                    // the piece's queries
+                if (flags & kTileFirst) {
+                    // the piece's queries, by both teams
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         if (!(flags >> w & 1)) continue;
                         const uint32_t seen = group_pieces_seen >> w & 1;
                         if (!warp_wait(q_empty(w), seen ^ 1, abort)) return false;
-                        load_q<T, DP>(a, p, pair ? w * 128 : 0, warp - kConvertAt, kTeamWarps, group,
+                        load_q<T, DP>(a, p, pair ? w * 128 : 0, warp - kConvertAt, 2 * kTeamWarps, group,
                                       base + L::kQ + (uint32_t)w * L::kTileBytes,
                                       reinterpret_cast<float *>(gen + L::kQScale) + w * 256 + (int)seen * 128, lane);
                         group_pieces_seen ^= 1u << w;
@@ -762,10 +761,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     }
                 }
             }
-            if (kIsV ? !order.has_v : end) return true;
+            if (is_v ? !order.has_v : end) return true;
             // the operand: the tile's keys, or the values whose turn it is
-            const int there_are = kIsV && !pair ? valid_before : valid;
-            const uint32_t position = kIsV ? order.v : order.k;
+            const int there_are = is_v && !pair ? valid_before : valid;
+            const uint32_t position = is_v ? order.v : order.k;
             const uint32_t slot = position % kRaw, op = position % kOps;
             if (!warp_wait(op_empty(op), ((position / kOps) & 1) ^ 1, abort)) return false;
             if (!warp_wait(raw_full(slot), (position / kRaw) & 1, abort)) return false;
@@ -789,7 +788,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 decode4<kFormat>(in.y, h[2], h[3]);
                 decode4<kFormat>(in.z, h[4], h[5]);
                 decode4<kFormat>(in.w, h[6], h[7]);
-                if constexpr (kIsV) {
+                if (is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) h[i] = __hfma2(h[i], hi, __hmul2(h[i], lo));
                 }
@@ -803,7 +802,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const uint4 in = ld_shared_v4(src + (uint32_t)(row * width + ch) * 16u);
                 return there(row) ? in : make_uint4(0, 0, 0, 0);
             };
-            if constexpr (!kIsV) {
+            if (!is_v) {
                 // the tile's key scales (of scores in log2 units), for the softmax groups; a token whose
                 // value scale (or page) is no number carries its NaN in the key's alone: where it is
                 // masked, its zero values must not become 0 times NaN
@@ -836,7 +835,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         in[i] = read(row_of(i), chunk_of(i), DP / 16);
-                        if (kIsV && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
+                        if (is_v && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
                     }
                     if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
                     if (step + 1 == kSteps) {
@@ -852,7 +851,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 for (int i = t; i < 128 * width; i += 32 * kTeamWarps) {
                     const int row = i / width;
                     __half2 hi = {}, lo = {};
-                    if (kIsV) row_factor(row, hi, lo);
+                    if (is_v) row_factor(row, hi, lo);
                     decode_store(read(row, i - row * width, width), (uint32_t)row, (uint32_t)(i - row * width), hi, lo);
                 }
                 __syncwarp();
@@ -941,7 +940,6 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const uint32_t hi_desc = (uint32_t)(sw128_kmajor_desc(0) >> 32);
             const uint32_t id_qk = idesc_f16_f32(128, 128, false), id_pv = idesc_f16_f32(128, D, true);
             constexpr uint32_t kAtom = 128 * 128;  // bytes of a 64-column atom of a 128-row tile
-            const int k_steps = D / 16;
             Order order = {0, 0, 0, false, false};
             uint32_t laps = 0;      // bits: parity of the next q, P and result of the groups; 6, 7: a group has had a result
             bool ok = true;
@@ -960,14 +958,20 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     laps ^= 1u << w;
                 }
                 if (!wait(op_full(k % kOps), (k / kOps) & 1)) return;
-                const uint32_t qa = (base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16;
-                const uint32_t ka = (base + L::kOp + (k % kOps) * L::kTileBytes) >> 4 | 1u << 16;
-                const uint32_t d = tmem + kColS + 128u * (uint32_t)w;
+                const uint32_t qa = (uint32_t)uniform((int)((base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16));
+                const uint32_t ka = (uint32_t)uniform((int)((base + L::kOp + (k % kOps) * L::kTileBytes) >> 4 | 1u << 16));
+                const uint32_t d = (uint32_t)uniform((int)(tmem + kColS + 128u * (uint32_t)w));
                 if (leader) {
-#pragma unroll
-                    for (int i = 0; i < DP / 16; ++i) {
+                    auto step = [&](int i) {
                         const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
-                        if (i < k_steps) umma_bf16_w(d, qa + off, ka + off, hi_desc, id_qk, i > 0);
+                        umma_bf16_w(d, qa + off, ka + off, hi_desc, id_qk, i > 0);
+                    };
+                    if (D == DP) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i) step(i);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) step(i);
                     }
                     umma_commit(s_full(w));
                     if (flags & kTileLast) umma_commit(q_empty(w));
@@ -980,8 +984,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 if (!wait(p_ready(w), laps >> (2 + w) & 1)) return;
                 laps ^= 1u << (2 + w);
-                const uint32_t va = (base + L::kOp + (v % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
-                const uint32_t d = tmem + kColO + 128u * (uint32_t)w, pa = tmem + kColS + 128u * (uint32_t)w;
+                const uint32_t va = (uint32_t)uniform((int)((base + L::kOp + (v % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16));
+                const uint32_t pa = (uint32_t)uniform((int)(tmem + kColS + 128u * (uint32_t)w)), d = pa + kColO - kColS;
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -1024,7 +1028,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         } else {
             // ---------------------------------------------------- converters --
             regs_dec<64>();
-            const bool ok = warp < kConvertAt + kTeamWarps ? convert_all(std::false_type{}) : convert_all(std::true_type{});
+            const bool ok = convert_all(warp >= kConvertAt + kTeamWarps);
             if (!ok && lane == 0) *abort = 1;
         }
     } else {
