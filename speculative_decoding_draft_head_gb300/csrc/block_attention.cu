@@ -59,7 +59,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: scores (and P) of t
 
 constexpr float kScaleFloor = 0x1p-100f;   // value scales below it lose precision, not range
 constexpr float kPeak = 7.f;               // log2 of P's largest bound when the reference moves ...
-constexpr float kMost = 32768.f;           // ... which it does when 64 terms of P sum to more than this
+constexpr float kMost = 32768.f;           // ... which it does when 32 terms of P sum to more than this
 constexpr int kVUp = 6;                    // log2 of what V is multiplied by: its codes reach 448 * 2^6 in fp16
 constexpr float kVDown = 0x1p-6f;
 constexpr float kQUp = 16.f;               // what q is multiplied by before it becomes fp16 ...
@@ -1082,29 +1082,28 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
                 float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
                 __syncwarp();
-                // the row's scores 64 columns at a time: more would spill, and with this much shared
+                // the row's scores 32 columns at a time: more would spill, and with this much shared
                 // memory a spilled register comes back from L2
 #pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pr[32];
-                    uint64_t bits = ~0ull;
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pr[16], bits = ~0u;
                     bool some_hidden = false;
                     if (masked) {
-                        const int from_t = token + 64 * q, full = min(max(sees - from_t, 0), 64);
-                        bits = full == 64 ? ~0ull : (1ull << full) - 1;
+                        const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
+                        bits = full == 32 ? ~0u : (1u << full) - 1;
                         const int sh = from_t - ctx;   // block token of the first column
-                        if (sh > -64 && sh < 64) bits |= sh >= 0 ? word >> sh : word << -sh;
-                        some_hidden = __any_sync(0xffffffffu, bits != ~0ull);
+                        if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
+                        some_hidden = __any_sync(0xffffffffu, bits != ~0u);
                         if (!__any_sync(0xffffffffu, live && bits != 0)) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) pr[i] = 0;
-                            tmem_st32(my_s + 32u * (uint32_t)q, pr);
+                            for (int i = 0; i < 16; ++i) pr[i] = 0;
+                            tmem_st16(my_s + 16u * (uint32_t)q, pr);
                             continue;
                         }
                     }
-                    // 32 columns' sums, with the row's own factor
-                    auto load_x = [&](int h, uint32_t (&x)[32]) { tmem_ld32(my_s + 64u * (uint32_t)q + 32u * (uint32_t)h, x); };
-                    auto wait_x = [&](uint32_t (&x)[32]) {
+                    // the columns' sums, with the row's own factor
+                    auto load_x = [&](uint32_t (&x)[32]) {
+                        tmem_ld32(my_s + 32u * (uint32_t)q, x);
                         tmem_ld_wait32(x);
                         if (rescale_q) {
 #pragma unroll
@@ -1112,25 +1111,24 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         }
                     };
                     // scores in log2 units less `ref2` of four columns; those the row does not see -inf
-                    auto four = [&](const uint32_t *x, int h, int i, uint64_t ref2, float (&y)[4], auto hidden) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 64 * q + 32 * h + i);
+                    auto four = [&](const uint32_t (&x)[32], int i, uint64_t ref2, float (&y)[4], auto hidden) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + i);
                         unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pack2(k4.x, k4.y), ref2), y[0], y[1]);
                         unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), pack2(k4.z, k4.w), ref2), y[2], y[3]);
                         if constexpr (decltype(hidden)::value) {
-                            const uint32_t seen = (uint32_t)(bits >> (32 * h));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                if (!(seen >> (i + k) & 1u)) y[k] = -INFINITY;
+                                if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
                         }
                     };
-                    // the 64 terms to `pr`, and their sum
-                    auto terms = [&](const uint32_t *xa, const uint32_t *xb, auto hidden) {
+                    // the terms to `pr`, and their sum
+                    auto terms = [&](const uint32_t (&x)[32], auto hidden) {
                         const uint64_t ref2 = pack2(-ref, -ref);
                         uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 64; i += 4) {
+                        for (int i = 0; i < 32; i += 4) {
                             float y[4];
-                            four(i < 32 ? xa : xb, i >> 5, i & 31, ref2, y, hidden);
+                            four(x, i, ref2, y, hidden);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
                             sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
@@ -1145,30 +1143,20 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     float s;
 #pragma unroll 1
                     for (int again = 0;; ++again) {
-                        {
-                            uint32_t xa[32], xb[32];
-                            load_x(0, xa);
-                            load_x(1, xb);
-                            wait_x(xa);
-                            wait_x(xb);
-                            s = some_hidden ? terms(xa, xb, std::true_type{}) : terms(xa, xb, std::false_type{});
-                        }
-                        // the reference has to move when a term could pass 2^15 (the sum of 64 says so), or
+                        uint32_t x[32];
+                        load_x(x);
+                        s = some_hidden ? terms(x, std::true_type{}) : terms(x, std::false_type{});
+                        // the reference has to move when a term could pass 2^15 (their sum says so), or
                         // when there is none yet
                         const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
                         if (again || !__any_sync(0xffffffffu, moves)) break;
                         float top = -INFINITY;
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t x[32];
-                            load_x(h, x);
-                            wait_x(x);
+                        load_x(x);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                float y[4];
-                                four(x, h, i, 0, y, std::true_type{});
-                                top = max3(max3(top, y[0], y[1]), y[2], y[3]);
-                            }
+                        for (int i = 0; i < 32; i += 4) {
+                            float y[4];
+                            four(x, i, 0, y, std::true_type{});
+                            top = max3(max3(top, y[0], y[1]), y[2], y[3]);
                         }
                         float f = 1.f;
                         if (moves && top != -INFINITY) {     // (-inf: there is no number)
@@ -1194,7 +1182,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         const __half2 f2 = __float2half2_rn(f);
                         tmem_st_wait();
 #pragma unroll 1
-                        for (int i = 0; i < 2 * q; ++i) {
+                        for (int i = 0; i < q; ++i) {
                             uint32_t o[16];
                             tmem_ld16(my_s + 16u * (uint32_t)i, o);
                             tmem_ld_wait16(o);
@@ -1207,8 +1195,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         }
                     }
                     l = fmaf(s, unit, l);
-                    // P's 32 columns lie below the scores still to be read
-                    tmem_st32(my_s + 32u * (uint32_t)q, pr);
+                    // P's 16 columns lie below the scores still to be read
+                    tmem_st16(my_s + 16u * (uint32_t)q, pr);
                 }
                 tmem_st_wait();
             }
