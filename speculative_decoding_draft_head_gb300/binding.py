@@ -9,6 +9,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -124,7 +125,7 @@ def load(build_if_missing: bool = True):
 
 
 def _check(status):
-    if status != DSPARK_OK:
+    if status:
         raise DSparkError(status, load().dspark_last_error().decode())
 
 
@@ -184,12 +185,19 @@ class WorkspaceCache:
 
     def __init__(self):
         self._bufs = {}
+        self._attention = {}
 
     def get(self, which, B, G, V, r, device):
         return self._sized(which, workspace_bytes(which, B, G, V, r), device)
 
     def attention(self, B, n_rows, n_q_heads, n_kv_heads, head_dim, device):
-        return self._sized("attention", attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim), device)
+        """Address and bytes of the attention's workspace."""
+        n = attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim)
+        kept = self._attention.get(device)
+        if kept is None or kept[1] < n:
+            buf = self._sized("attention", n, device)
+            kept = self._attention[device] = (buf.data_ptr(), buf.numel())
+        return kept
 
     def _sized(self, which, n, device):
         if n == 0:
@@ -439,8 +447,10 @@ class KVCache:
         self.flags = torch.zeros(64, dtype=torch.int32, device=k.device)
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
+        self._index = k.get_device()
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    self.flags.data_ptr(), *k.shape, _KV_FORMATS[k.dtype])
+        self._ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, *, dtype=torch.float8_e4m3fn, device="cuda"):
@@ -450,26 +460,39 @@ class KVCache:
         return cls(*codes, *[torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)])
 
 
-def _row_stride(t, name, heads, D, device):
+# These calls take some ten microseconds on the device, so their checks are made in one expression each;
+# only a failed one is looked at again for its message.
+def _vec(t, name, dtype, n, cache):
+    if t.dtype is dtype and t.dim() == 1 and t.shape[0] == n and t.get_device() == cache._index and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype=dtype, shape=(n,), device=cache.device)
+    raise ValueError("%s must be on %s" % (name, cache.device))
+
+
+def _row_stride(t, name, heads, cache):
     """Checks packed rows [n, heads, D], whose rows may lie any 16-byte multiple
     apart; returns their distance in elements."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
     n, h, d = t.shape
-    if h != heads or d != D:
-        raise ValueError("%s must have shape (rows, %d, %d), got %s" % (name, heads, D, tuple(t.shape)))
+    if t.get_device() != cache._index:
+        raise ValueError("%s must be on %s" % (name, cache.device))
+    if h != heads or d != cache.head_dim:
+        raise ValueError("%s must have shape (rows, %d, %d), got %s" % (name, heads, cache.head_dim, tuple(t.shape)))
     row, head, elem = t.stride()
-    if elem != 1 or (h > 1 and head != D):
+    if elem != 1 or (h > 1 and head != d):
         raise ValueError("the heads of a row of %s must be contiguous" % name)
-    return row if n > 1 else h * D
+    return row if n > 1 else h * d
 
 
-def _paged(block_table, start, name, row0, device):
+def _paged(block_table, start, name, row0, cache):
     B, max_pages = block_table.shape
-    _need(block_table, "block_table", dtype=torch.int32, device=device)
-    _need(start, name, dtype=torch.int32, shape=(B,), device=device)
-    _need(row0, "row0", dtype=torch.int64, shape=(B + 1,), device=device)
-    return B, max_pages
+    if not (block_table.dtype is torch.int32 and block_table.get_device() == cache._index and block_table.is_contiguous()):
+        _need(block_table, "block_table", dtype=torch.int32, device=cache.device)
+    return (B, max_pages, block_table.data_ptr(), _vec(start, name, torch.int32, B, cache),
+            _vec(row0, "row0", torch.int64, B + 1, cache))
+
+
+def _raw_stream(stream, cache):
+    return torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else stream.cuda_stream
 
 
 def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
@@ -477,38 +500,37 @@ def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
     ``cache``: row i of request b (rows row0[b] .. row0[b+1] - 1, ``row0``
     [B+1] int64) at position start[b] + i of the request's pages
     (``block_table`` [B, max_pages] int32).  See dspark_kv_append."""
-    lib = load()
-    dev = cache.device
-    B, max_pages = _paged(block_table, start, "start", row0, dev)
-    if k.dtype not in _ROW_DTYPES or v.dtype != k.dtype or v.shape != k.shape:
+    lib = _lib or load()
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
+    if k.dtype not in _ROW_DTYPES or v.dtype is not k.dtype or v.shape != k.shape:
         raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
-    ks = _row_stride(k, "k", cache.n_kv_heads, cache.head_dim, dev)
-    vs = _row_stride(v, "v", cache.n_kv_heads, cache.head_dim, dev)
-    _check(lib.dspark_kv_append(cache.struct, k.data_ptr(), v.data_ptr(), ks, vs, _ROW_DTYPES[k.dtype],
-                                row0.data_ptr(), k.shape[0], start.data_ptr(), block_table.data_ptr(), max_pages, B,
-                                _stream(stream)))
+    ks = _row_stride(k, "k", cache.n_kv_heads, cache)
+    vs = _row_stride(v, "v", cache.n_kv_heads, cache)
+    _check(lib.dspark_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, _ROW_DTYPES[k.dtype], row0_p,
+                                k.shape[0], start_p, table_p, max_pages, B, _raw_stream(stream, cache)))
 
 
 def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, out=None, stream=None):
     """Cached tokens as packed rows: row i of request b is position
     start[b] + i.  Returns dict(k, v) of [n_rows, n_kv_heads, head_dim]; an
     ``out`` with only one of them reads that one.  See dspark_kv_read."""
-    lib = load()
+    lib = _lib or load()
     dev = cache.device
-    B, max_pages = _paged(block_table, start, "start", row0, dev)
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
+    if dtype not in _ROW_DTYPES:
+        raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
     if out is None:
         out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev))
-    if dtype not in _ROW_DTYPES:
-        raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
-    for name in out:
-        _need(out[name], name, dtype=dtype, shape=shape, device=dev)
-    _check(lib.dspark_kv_read(cache.struct, row0.data_ptr(), n_rows, start.data_ptr(), block_table.data_ptr(),
-                              max_pages, B, _ROW_DTYPES[dtype], _ptr(out.get("k")), _ptr(out.get("v")),
-                              _stream(stream)))
+    else:
+        for name in out:
+            _need(out[name], name, dtype=dtype, shape=shape, device=dev)
+    _check(lib.dspark_kv_read(cache._ref, row0_p, n_rows, start_p, table_p, max_pages, B, _ROW_DTYPES[dtype],
+                              _ptr(out.get("k")), _ptr(out.get("v")), _raw_stream(stream, cache)))
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) -> int:
     return int(load().dspark_attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim))
 
@@ -524,31 +546,36 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     block; ``scale`` is head_dim ** -0.5 by default.  See dspark_block_attention.
 
     Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
-    lib = load()
+    lib = _lib or load()
     dev = cache.device
-    B, max_pages = _paged(block_table, kv_len, "kv_len", row0, dev)
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    B, max_pages, table_p, len_p, row0_p = _paged(block_table, kv_len, "kv_len", row0, cache)
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise TypeError("q must be bfloat16 or float16, got %s" % q.dtype)
     n, Hq, D = q.shape
-    qs = _row_stride(q, "q", Hq, cache.head_dim, dev)
+    qs = _row_stride(q, "q", Hq, cache)
+    pages_p, n_pages = None, 0
     if prefix_pages is not None:
-        _need(prefix_pages, "prefix_pages", dtype=torch.int32, device=dev)
-    if row_mask is not None:
-        _need(row_mask, "row_mask", dtype=torch.int64, shape=(n,), device=dev)
+        n_pages = prefix_pages.numel()
+        pages_p = _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
+    words_p = None if row_mask is None else _vec(row_mask, "row_mask", torch.int64, n, cache)
     if out is None:
         out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
                    lse=torch.empty((n, Hq), dtype=torch.float32, device=dev))
+        lse_p = out["lse"].data_ptr()
     else:
         _need(out["out"], "out", dtype=q.dtype, shape=(n, Hq, D), device=dev)
+        lse_p = None
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
+            lse_p = out["lse"].data_ptr()
     if workspace is None:
-        workspace = _default_ws.attention(B, n, Hq, cache.n_kv_heads, D, dev)
+        ws_p, ws_n = _default_ws.attention(B, n, Hq, cache.n_kv_heads, D, dev)
+    else:
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel()
     _check(lib.dspark_block_attention(
-        cache.struct, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0.data_ptr(), n, B, block_table.data_ptr(),
-        max_pages, kv_len.data_ptr(), _ptr(prefix_pages), 0 if prefix_pages is None else prefix_pages.numel(),
-        int(prefix_len), _MASKS[mask], _ptr(row_mask), D ** -0.5 if scale is None else float(scale),
-        out["out"].data_ptr(), _ptr(out.get("lse")), _ptr(workspace), workspace.numel(), _stream(stream)))
+        cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
+        int(prefix_len), _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
+        lse_p, ws_p, ws_n, _raw_stream(stream, cache)))
     return out
 
 

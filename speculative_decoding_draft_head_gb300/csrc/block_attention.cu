@@ -48,6 +48,10 @@ using namespace tc;
 constexpr int kThreads = 640;
 // warps of the roles (the softmax groups are warps 0 .. 7, the scales' loader the last)
 constexpr int kConvertAt = 8, kTeamWarps = 4, kPlanner = 16, kIssuer = 17, kCodes = 18;
+// registers a thread: of the launch, and as the roles share them out (a role that asks for more than
+// there is would wait for ever: checked before the launch)
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kConvertRegs = 64;
+static_assert(256 * kSoftmaxRegs + 2 * kTeamWarps * 32 * kConvertRegs + 128 * kLaunchRegs <= kThreads * kLaunchRegs, "");
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // pieces of a group told ahead
 constexpr int kRounds = 4;        // rounds planned ahead
@@ -1027,14 +1031,13 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             }
         } else {
             // ---------------------------------------------------- converters --
-            regs_dec<64>();
+            regs_dec<kConvertRegs>();
             const bool ok = convert_all(warp >= kConvertAt + kTeamWarps);
             if (!ok && lane == 0) *abort = 1;
         }
     } else {
         // -------------------------------------------------------------- softmax --
-        // the launch's 640 x 96 registers, shared out: 128 a softmax thread, 64 a converter's, 96 the other four warps'
-        regs_inc<128>();
+        regs_inc<kSoftmaxRegs>();
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * (uint32_t)w, my_o = lanes + kColO + 128u * (uint32_t)w;
@@ -1384,6 +1387,10 @@ cudaError_t launch_t(const AttentionArgs &a, const Partials &p, cudaStream_t s) 
     static PerDeviceOnce once;
     auto *kernel = attention_kernel<T, kFormat, DP>;
     cudaError_t e = once.run([&] {
+        cudaFuncAttributes attr{};
+        const cudaError_t got = cudaFuncGetAttributes(&attr, kernel);
+        if (got != cudaSuccess) return got;
+        if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<DP>::kBytes);
     });
     if (e != cudaSuccess) return e;
