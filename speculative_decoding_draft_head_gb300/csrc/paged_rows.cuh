@@ -63,17 +63,25 @@ __device__ __forceinline__ void decode4(uint32_t c, __half2 &a, __half2 &b) {
     }
 }
 
-// Two values, already scaled into [-Q, Q], to two codes in the low 16 bits
-// (nearest, ties to even).
+// Four values, already scaled into [-Q, Q], to four codes (nearest, ties to
+// even).
 template <int kFormat>
-__device__ __forceinline__ uint32_t encode2(float a, float b) {
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
     if constexpr (kFormat == DSPARK_KV_E4M3) {
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+        uint32_t r;
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
         return r;
     } else {
-        const int x = min(127, max(-127, __float2int_rn(a))), y = min(127, max(-127, __float2int_rn(b)));
-        return ((uint32_t)x & 0xffu) | (((uint32_t)y & 0xffu) << 8);
+        // at 1.5 * 2^23 a float's steps are 1, and the low byte of its bits is
+        // the rounded value's (|x| stays below 127.5: x * (127 / amax) is off
+        // by less than 127 * 2^-23)
+        const float off = 0x1.8p23f;
+        const uint32_t x = __float_as_uint(__fadd_rn(a, off)), y = __float_as_uint(__fadd_rn(b, off));
+        const uint32_t z = __float_as_uint(__fadd_rn(c, off)), w = __float_as_uint(__fadd_rn(d, off));
+        return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
     }
 }
 
