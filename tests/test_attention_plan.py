@@ -3,7 +3,7 @@
 The header is plain integer arithmetic; a small program built from it walks the
 parts of every worker over random sets of items, and each token tile of each item
 has to be taken exactly once, pieces have to follow the order that the joining
-of partial results relies on, and the joining's own enumeration (first CTA,
+of partial results relies on, and the joining's own enumeration (first worker,
 then those that go on) has to name exactly the pieces that were taken."""
 import os
 import shutil
