@@ -46,8 +46,8 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 640;
-// warps of the roles (the softmax groups are warps 0 .. 7, the scales' loader the last)
-constexpr int kConvertAt = 8, kTeamWarps = 4, kPlanner = 16, kIssuer = 17, kCodes = 18;
+// warps of the roles
+constexpr int kIssuer = 0, kPlanner = 1, kCodes = 2, kSoftmaxAt = 4, kConvertAt = 12, kTeamWarps = 4;
 // registers a thread: of the launch, and as the roles share them out (a role that asks for more than
 // there is would wait for ever: checked before the launch)
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kConvertRegs = 64;
@@ -669,7 +669,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const int n0 = uniform(r.n[0]), n1 = uniform(r.n[1]);
             const int turns = (bits & kRoundEnd) ? 1 : 2 * max(n0, n1);
 #pragma unroll 1
-            for (int x = 0; x < turns; ++x) {
+            for (int x = 0; x < turns; x += (bits & kRoundPair) ? 2 : 1) {
                 const int id = x & 1, i = x >> 1, n = id ? n1 : n0;
                 int flags = kTileEnd;
                 if (!(bits & kRoundEnd)) {
@@ -868,7 +868,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         });
     };
 
-    if (warp >= kConvertAt) {
+    if (warp < kSoftmaxAt || warp >= kConvertAt) {
         if (warp == kPlanner) {
             // -------------------------------------------------------- planner --
             // pairs, then the first group's singles, are stream 0's tiles, the second group's singles stream 1's
@@ -918,7 +918,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (end) break;
             }
             if (!ok && lane == 0) *abort = 1;
-        } else if (warp >= kCodes) {
+        } else if (warp >= kCodes && warp < kSoftmaxAt) {
             // -------------------------------------------------------- loaders --
             uint32_t ids = kNoChunk;
             Order order = {0, 0, 0, false, false};
@@ -962,9 +962,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     laps ^= 1u << w;
                 }
                 if (!wait(op_full(k % kOps), (k / kOps) & 1)) return;
-                const uint32_t qa = (uint32_t)uniform((int)((base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16));
-                const uint32_t ka = (uint32_t)uniform((int)((base + L::kOp + (k % kOps) * L::kTileBytes) >> 4 | 1u << 16));
-                const uint32_t d = (uint32_t)uniform((int)(tmem + kColS + 128u * (uint32_t)w));
+                const uint32_t qa = (base + L::kQ + (uint32_t)w * L::kTileBytes) >> 4 | 1u << 16;
+                const uint32_t ka = (base + L::kOp + (k % kOps) * L::kTileBytes) >> 4 | 1u << 16;
+                const uint32_t d = tmem + kColS + 128u * (uint32_t)w;
                 if (leader) {
                     auto step = [&](int i) {
                         const uint32_t off = ((uint32_t)(i >> 2) * kAtom + (uint32_t)(i & 3) * 32u) >> 4;
@@ -988,8 +988,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 if (!wait(p_ready(w), laps >> (2 + w) & 1)) return;
                 laps ^= 1u << (2 + w);
-                const uint32_t va = (uint32_t)uniform((int)((base + L::kOp + (v % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16));
-                const uint32_t pa = (uint32_t)uniform((int)(tmem + kColS + 128u * (uint32_t)w)), d = pa + kColO - kColS;
+                const uint32_t va = (base + L::kOp + (v % kOps) * L::kTileBytes) >> 4 | (kAtom >> 4) << 16;
+                const uint32_t pa = tmem + kColS + 128u * (uint32_t)w, d = pa + kColO - kColS;
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -1009,7 +1009,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (next_mask == 3) pair_v = order.v;
                 // passes: 0 and 1 the early scores of the groups, 2 and 3 their outputs and later scores
 #pragma unroll 1
-                for (int i = 0; i < 4 && ok; ++i) {
+                for (int i = mask == 3 ? 2 : 0; i < 4 && ok; ++i) {
                     const int w = i & 1, has = mask >> w & 1, late = i >> 1;
                     if (i == 2 && mask && !wait(op_full(vi % kOps), (vi / kOps) & 1)) break;
                     if (late && has) pv(w, vi, now);
@@ -1038,7 +1038,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     } else {
         // -------------------------------------------------------------- softmax --
         regs_inc<kSoftmaxRegs>();
-        const int w = warp >> 2, row = tid & 127;
+        const int w = (warp - kSoftmaxAt) >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 TMEM lanes
         const uint32_t my_s = lanes + kColS + 128u * (uint32_t)w, my_o = lanes + kColO + 128u * (uint32_t)w;
         bool ok = true;
