@@ -63,7 +63,14 @@ DSPARK_HD int64_t head_units(int cls, int rows, int tiles) {
 
 // CTA c of n takes units [cta_begin(c), cta_begin(c + 1)) of `total`
 DSPARK_HD int64_t cta_begin(int64_t c, int64_t total, int n) { return total * c / n; }
-DSPARK_HD int cta_of(int64_t u, int64_t total, int n) { return (int)(((u + 1) * n - 1) / total); }
+// (a guess, off by one at most, and a look: a 64-bit division costs some hundred instructions)
+DSPARK_HD int cta_of(int64_t u, int64_t total, int n) {
+    int c = (int)((float)u * (float)n / (float)total);
+    if (c > n - 1) c = n - 1;
+    while (c > 0 && cta_begin(c, total, n) > u) --c;
+    while (c + 1 < n && cta_begin(c + 1, total, n) <= u) ++c;
+    return c;
+}
 
 // worker v = 2 c + group of the singles takes units [single_begin(v), single_begin(v + 1)), all of
 // them from `pairs`, the units of all pairs, on

@@ -230,6 +230,43 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// ---------------------------------------------------------------- the result --
+// eight floats times f, a whole 32-byte sector at once
+__device__ __forceinline__ void store8(float *to, const uint32_t *x, float f) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(x[i]) * f;
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(y[0]), "f"(y[1]), "f"(y[2]),
+                 "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                 : "memory");
+}
+
+// A row's output from TMEM, times f, to `out` or (when there is none) to `part`; out of line, as it runs once
+// an item.  The whole warp.
+template <typename T>
+__device__ __noinline__ void store_result(uint32_t from, T *out, float *part, int D, bool live, float f) {
+#pragma unroll 1
+    for (int at = 0; at < D; at += 16) {
+        uint32_t o[16];
+        tmem_ld16(from + (uint32_t)at, o);
+        tmem_ld_wait16(o);
+        if (live && out) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = float_to_pair<T>(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+                *reinterpret_cast<uint4 *>(out + at + i) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        } else if (live) {
+            store8(part + at, &o[0], f);
+            store8(part + at + 8, &o[8], f);
+        }
+        __syncwarp();
+    }
+}
+
 // ------------------------------------------------------------------ the plan --
 // The line as a CTA sees it.
 struct Line {
@@ -1223,15 +1260,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                : 2 * all + (int64_t)kCtas * plan::kTileRows + ((int64_t)blockIdx.x * 2 + w) * plan::kHalfRows + mt;
                     const float inv = out_kind == kDirect ? (l == 0.f ? 0.f : kVDown / l) : kVDown;
 #pragma unroll 1
-                    for (int q = 0; q * 32 < D; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(my_o + 32u * (uint32_t)q, o);
-                        tmem_ld_wait32(o);
+                    for (int q = 0; q * 16 < D; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(my_o + 16u * (uint32_t)q, o);
+                        tmem_ld_wait16(o);
                         if (live && out_kind == kDirect) {
-                            T *dst = static_cast<T *>(a.out) + place * D + 32 * q;
+                            T *dst = static_cast<T *>(a.out) + place * D + 16 * q;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                if (32 * q + i >= D) break;
+                            for (int i = 0; i < 16; i += 8) {
                                 uint32_t v[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
@@ -1239,14 +1275,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                 *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         } else if (live) {
-                            float *dst = parts.o + part * D + 32 * q;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                if (32 * q + i >= D) break;
-                                *reinterpret_cast<float4 *>(dst + i) =
-                                    make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                                __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                            }
+                            float *dst = parts.o + part * D + 16 * q;
+                            store8(dst, &o[0], inv);
+                            store8(dst + 8, &o[8], inv);
                         }
                         __syncwarp();
                     }
@@ -1273,14 +1304,20 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 }
 
 // ---------------------------------------------------------------- the joining --
-// One warp per (packed row, query head) adds up the parts of its row: the
-// prefix's and its request's own item's, each cut where a CTA's part of the
-// line ends.  Rows that one CTA finished alone are already written.
-constexpr int kJoinWarps = 8;
+// Adds up the parts of each (packed row, query head): the prefix's and its
+// request's own item's, each cut where a worker's part of the line ends.  Rows
+// that one worker finished alone are already written.
+//
+// A warp takes `per` rows of one kv head and request, one after another: they
+// nearly always belong to the same two items, so that where their parts are is
+// found once, a half of the warp looking at an item and each lane at one of its
+// workers (an item of more than 16 workers is looked at in turns).  What then
+// bounds it is reading the parts.
+constexpr int kJoinWarps = 8, kJoinRows = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) {
+attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials parts, const int per) {
     griddep_wait();
     const int lane = threadIdx.x & 31, b = blockIdx.x;
     const dspark_kv_cache &c = a.cache;
@@ -1294,6 +1331,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         const int last = a.rows.B - 1;
         const Request z = load_request(a, last);
         int64_t end[2];
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
             prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
             end[k] = prefix[k] + parts.unit0[k][last] +
@@ -1302,70 +1340,107 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         pairs = end[0];
         total = end[0] + end[1];
     }
+    const int64_t own0 = parts.unit0[0][b] + prefix[0], own1 = parts.unit0[1][b] + prefix[1];
     const int64_t all = (int64_t)a.rows.n_rows * Hq;
-    const int m_own = q.n * group, own_tiles = plan::token_tiles(q.len);
-    for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < q.n * Hq; i += gridDim.y * kJoinWarps) {
-        const int blk = i / Hq, head = i - blk * Hq, h = head / group, g = head - h * group;
-        const int64_t place = (q.first + blk) * Hq + head;
-        T *out = static_cast<T *>(a.out) + place * D;
-        if (!q.len_ok) {
-            if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-            if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
-            continue;
-        }
-        float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](int64_t part) {
-            const float2 st = parts.stats[part];
-            if (st.x == -INFINITY && st.y == 0.f) return;   // saw nothing
-            const float t = fmaxf(top, st.x);
-            const float f0 = top == -INFINITY && l == 0.f ? 0.f : fast_exp2(top - t), f1 = fast_exp2(st.x - t);
-            l = l * f0 + st.y * f1;
-            top = t;
-            if (lane * 4 < D) {
-                const float4 o = *reinterpret_cast<const float4 *>(parts.o + part * D + lane * 4);
-                acc[0] = acc[0] * f0 + o.x * f1, acc[1] = acc[1] * f0 + o.y * f1;
-                acc[2] = acc[2] * f0 + o.z * f1, acc[3] = acc[3] * f0 + o.w * f1;
-            }
-        };
-        // parts of one item (first unit `start`, row mt of its row tile): its first worker's, then
-        // those of the workers that go on with it
-        auto add_item = [&](int cls, int64_t start, int tiles, int mt, int64_t first_part, bool alone_is_done) {
+    const int own_m = q.n * group, chunks = (own_m + per - 1) / per;
+    // this lane's item (0 the prefix's, 1 the request's own) and its place among the item's workers
+    const int side = lane >> 4, at = lane & 15;
+    const int m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
+    const int tiles = side ? plan::token_tiles(q.len) : prefix_tiles;
+    for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < c.n_kv_heads * chunks; i += gridDim.y * kJoinWarps) {
+        const int h = i / chunks, m0 = (i - h * chunks) * per, m1 = min(m0 + per, own_m);
+        int item = -1;             // the row tile that is looked at
+        bool has = false, first = false, more = false, done = false;
+        int64_t part0 = 0;
+        // the lane's part of the item, when its worker (the `turn`-th 16 of them) has one
+        auto look = [&](int turn) {
+            const int cls = plan::class_of(plan::tile_rows(rows, item));
+            const int64_t start = (!side ? 0 : cls == plan::kPair ? own0 : own1) + (cls == plan::kPair ? 0 : pairs) +
+                                  h * plan::head_units(cls, rows, tiles) +
+                                  (cls == plan::kPair ? item * plan::item_total(cls, tiles) : 0);
             const int64_t end = start + plan::item_total(cls, tiles);
-            const int v0 = plan::worker_of(cls, start + plan::item_units(cls), pairs, total, kCtas);
-            int64_t from = plan::worker_begin(cls, v0 + 1, pairs, total, kCtas);
-            if (alone_is_done && plan::first_tile(cls, from, start, tiles) == tiles) return false;
-            add(first_part);
-            const int workers = cls == plan::kPair ? kCtas : 2 * kCtas, rows = cls == plan::kPair ? plan::kTileRows : plan::kHalfRows;
-            const int64_t slots = 2 * all + (cls == plan::kPair ? 0 : (int64_t)kCtas * plan::kTileRows) + mt;
-            for (int v = v0 + 1; v < workers && from < end; ++v) {
+            const int v0 = plan::worker_of(cls, start + plan::item_units(cls), pairs, total, kCtas), v = v0 + turn * 16 + at;
+            const int workers = cls == plan::kPair ? kCtas : 2 * kCtas;
+            has = first = false;
+            bool go_on = false, alone = false;
+            if (tiles > 0 && v < workers) {
+                const int64_t from = plan::worker_begin(cls, v, pairs, total, kCtas);
                 const int64_t to = plan::worker_begin(cls, v + 1, pairs, total, kCtas);
-                if (plan::first_tile(cls, from, start, tiles) < plan::first_tile(cls, to, start, tiles))
-                    add(slots + (int64_t)v * rows);
-                from = to;
+                const int t = plan::first_tile(cls, to, start, tiles);
+                first = v == v0;
+                has = first || (from < end && plan::first_tile(cls, from, start, tiles) < t);
+                go_on = at == 15 && to < end && v + 1 < workers;
+                alone = first && t == tiles;
             }
-            return true;
+            part0 = first ? (side ? all : 0)
+                          : 2 * all + (cls == plan::kPair ? 0 : (int64_t)kCtas * plan::kTileRows) +
+                                (int64_t)v * (cls == plan::kPair ? plan::kTileRows : plan::kHalfRows);
+            more = __any_sync(0xffffffffu, go_on);
+            if (turn == 0) done = __any_sync(0xffffffffu, side && alone && prefix_tiles == 0);
         };
-        // the item of row m of a list's rows, the list's units of the class beginning at `at`
-        auto add_row = [&](const int64_t (&at)[2], int rows, int tiles, int m, int64_t first_part, bool alone_is_done) {
-            const int rt = m / plan::kTileRows, cls = plan::class_of(plan::tile_rows(rows, rt));
-            const int64_t start = at[cls] + h * plan::head_units(cls, rows, tiles) +
-                                  (cls == plan::kPair ? rt * plan::item_total(cls, tiles) : 0);
-            return add_item(cls, start, tiles, m - rt * plan::kTileRows, first_part, alone_is_done);
-        };
-        if (prefix_tiles > 0) {
-            const int64_t at[2] = {0, pairs};
-            add_row(at, prefix_m, prefix_tiles, (int)(q.first + blk) * group + g, place, false);
+        for (int m = m0; m < m1; ++m) {
+            const int blk = m / group;
+            const int64_t place = (q.first + blk) * Hq + h * group + (m - blk * group);
+            T *out = static_cast<T *>(a.out) + place * D;
+            if (!q.len_ok) {
+                if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+                if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+                continue;
+            }
+            const int mt = m_of + m, now = mt / plan::kTileRows;
+            const bool other = __any_sync(0xffffffffu, now != item);
+            item = now;
+            if (other) look(0);
+            if (done) continue;
+            float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+            int turn = 0;
+            while (true) {
+                const int64_t part = part0 + (first ? place : mt - now * plan::kTileRows);
+                float2 st = make_float2(-INFINITY, 0.f);
+                if (has && mt < rows) st = parts.stats[part];
+                const bool saw = !(st.x == -INFINITY && st.y == 0.f);
+                float t = fmaxf(top, st.x);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                const float keep = top == -INFINITY && l == 0.f ? 0.f : fast_exp2(top - t);
+                const float f = saw ? fast_exp2(st.x - t) : 0.f;
+                float s = saw ? st.y * f : 0.f;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                l = l * keep + s;
+                top = t;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] *= keep;
+                unsigned left = __ballot_sync(0xffffffffu, saw);
+                while (left) {
+                    // two parts at a time
+                    const int x = __ffs(left) - 1;
+                    left &= left - 1;
+                    const int y = left ? __ffs(left) - 1 : x;
+                    const float fx = __shfl_sync(0xffffffffu, f, x), fy = left ? __shfl_sync(0xffffffffu, f, y) : 0.f;
+                    const int64_t px = __shfl_sync(0xffffffffu, part, x), py = __shfl_sync(0xffffffffu, part, y);
+                    if (lane * 4 < D) {
+                        const float4 ox = *reinterpret_cast<const float4 *>(parts.o + px * D + lane * 4);
+                        const float4 oy = left ? *reinterpret_cast<const float4 *>(parts.o + py * D + lane * 4)
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                        acc[0] += ox.x * fx + oy.x * fy, acc[1] += ox.y * fx + oy.y * fy;
+                        acc[2] += ox.z * fx + oy.z * fy, acc[3] += ox.w * fx + oy.w * fy;
+                    }
+                    left &= left - 1;   // (none left: stays 0)
+                }
+                if (!more) break;
+                look(++turn);
+            }
+            if (turn > 0) item = -1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (lane * 4 < D) {
+                uint2 v;
+                v.x = float_to_pair<T>(acc[0] * inv, acc[1] * inv);
+                v.y = float_to_pair<T>(acc[2] * inv, acc[3] * inv);
+                *reinterpret_cast<uint2 *>(out + lane * 4) = v;
+            }
+            if (lane == 0 && a.lse) a.lse[place] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
         }
-        const int64_t at[2] = {prefix[0] + parts.unit0[0][b], pairs + prefix[1] + parts.unit0[1][b]};
-        if (!add_row(at, m_own, own_tiles, blk * group + g, all + place, prefix_tiles == 0)) continue;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (lane * 4 < D) {
-            uint2 v;
-            v.x = float_to_pair<T>(acc[0] * inv, acc[1] * inv);
-            v.y = float_to_pair<T>(acc[2] * inv, acc[3] * inv);
-            *reinterpret_cast<uint2 *>(out + lane * 4) = v;
-        }
-        if (lane == 0 && a.lse) a.lse[place] = l == 0.f ? -INFINITY : kLn2 * (top + log2f(l));
     }
 }
 
@@ -1396,10 +1471,14 @@ cudaError_t launch_t(const AttentionArgs &a, const Partials &p, cudaStream_t s) 
     if (e != cudaSuccess) return e;
     kernel<<<kCtas, kThreads, Layout<DP>::kBytes, s>>>(a, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // enough blocks per request for the rows of an average one
-    const int64_t per = ((int64_t)a.rows.n_rows * a.n_q_heads + a.rows.B - 1) / a.rows.B;
-    const int y = (int)((per + kJoinWarps - 1) / kJoinWarps);
-    return launch_dependent(attention_join_kernel<T>, dim3(a.rows.B, y < 1024 ? y : 1024), dim3(kJoinWarps * 32), 0, s, a, p);
+    // rows a warp: several once that still gives every SM a few warps; and enough blocks per request for
+    // the rows of an average one
+    const int64_t rows = (int64_t)a.rows.n_rows * a.n_q_heads;
+    const int per = rows >= kJoinRows * 16 * kNumSMs ? kJoinRows : 1;
+    const int64_t warps = (rows + (int64_t)a.rows.B * per - 1) / ((int64_t)a.rows.B * per);
+    const int y = (int)((warps + kJoinWarps - 1) / kJoinWarps);
+    return launch_dependent(attention_join_kernel<T>, dim3(a.rows.B, y < 1024 ? y : 1024), dim3(kJoinWarps * 32), 0, s, a, p,
+                            per);
 }
 
 template <typename T>
