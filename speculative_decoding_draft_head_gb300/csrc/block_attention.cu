@@ -1045,12 +1045,16 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 const uint32_t ki = order.k, vi = mask == 3 ? pair_v : order.v;
                 if (next_mask == 3) pair_v = order.v;
                 // passes: 0 and 1 the early scores of the groups, 2 and 3 their outputs and later scores
+                uint32_t work = (uint32_t)(next_mask & ~mask) | (uint32_t)mask << 2;
 #pragma unroll 1
-                for (int i = mask == 3 ? 2 : 0; i < 4 && ok; ++i) {
-                    const int w = i & 1, has = mask >> w & 1, late = i >> 1;
-                    if (i == 2 && mask && !wait(op_full(vi % kOps), (vi / kOps) & 1)) break;
-                    if (late && has) pv(w, vi, now);
-                    if (ok && (next_mask >> w & 1) && has == late) qk(w, ki, nxt);
+                while (work && ok) {
+                    const int i = __ffs((int)work) - 1, w = i & 1;
+                    work &= work - 1;
+                    if (i >= 2) {
+                        if ((i == 2 || mask == 2) && !wait(op_full(vi % kOps), (vi / kOps) & 1)) break;
+                        pv(w, vi, now);
+                    }
+                    if (ok && next_mask >> w & 1) qk(w, ki, nxt);
                 }
                 if (!ok) return false;
                 // (in the order of their places)
