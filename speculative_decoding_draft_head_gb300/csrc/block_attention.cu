@@ -20,11 +20,11 @@
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
 // 128 tokens a tile.  Roles (20 warps):
-//   0-7    two softmax groups of 128 threads, a thread per row (TMEM lane)
-//   8-11   queries and keys to fp16 operands in the swizzled layout;  12-15  values
-//   16     plans: rounds of up to four tiles for each group
-//   17     issues the tensor-core products
-//   18     loads codes, 19 scales (bulk copies)
+//   0      issues the tensor-core products
+//   1      plans: rounds of up to four tiles for each group
+//   2      loads codes, 3 scales (bulk copies)
+//   4-11   two softmax groups of 128 threads, a thread per row (TMEM lane)
+//   12-15  keys to fp16 operands in the swizzled layout, 16-19 values; queries by both
 // A pair tile's keys and values serve both groups; single tiles alternate
 // between the groups' own items.  Operands are loaded, converted and used in
 // one order: of pairs K0 V0 K1 V1 .., so that a tile's values are converted
@@ -34,6 +34,17 @@
 // teams wait for their operand's place before they look for its codes: so no
 // wait is more than one lap of a ring away from the phase that it tests, whose
 // parity would deceive it.  Every wait is bounded.
+//
+// What bounds it (SM clocks): a pair tile takes 5,500 to 5,900 where its products
+// take 2,048 and its exponentials 2,048, a single tile 3,000 to 3,400 where its
+// products take 1,024: the chain of issuer, product, softmax and issuer, as P
+// takes its scores' columns.  An item adds some 10,000 (queries, first reference,
+// result), which is why the plan counts it.  Measured: 153 rows of 32 query
+// heads over 131,000 shared tokens in 405 us (810 TFLOP/s of the rows' products),
+// 64 single tokens of 64 heads over 300,000 own tokens in 272 us (2.3 TB/s).
+// The roles' loops together nearly fill the instruction cache, so less code
+// was faster again and again: 64 scores at a time instead of 32 cost 1 to 10%, two
+// issuing warps 7%, 24 warps with the issuer apart from the converters 15%.
 #include <type_traits>
 
 #include "attention_plan.h"
@@ -619,7 +630,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         for (int k = 0; k < 2; ++k) x[k] = plan::head_units(k, q.n * group, tiles) * c.n_kv_heads;
     };
     int64_t mine[2];
-    request_units(tid, mine);   // the first 512 requests' units stay in registers
+    request_units(tid, mine);   // the first kThreads requests' units stay in registers
     {
         int64_t sum[2] = {mine[0], mine[1]};
         for (int b = tid + kThreads; b < a.rows.B; b += kThreads) {
@@ -1111,142 +1122,142 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             bool rescale_q = false;
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++n, token += plan::kTile) {
-            const bool first = j == 0;
-            if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
-            tc_fence_after();
-            if (first) {
-                lack = live ? qscale[row] : 1.f;
-                rescale_q = __any_sync(0xffffffffu, lack != 1.f);
-            }
-            if (warp_live) {
-                const uint32_t ss = n % kScaleSlots;
-                const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 128;
-                const int lv = uniform(exponents[w][ss]);
-                const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
-                const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
-                float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
-                __syncwarp();
-                // the row's scores 32 columns at a time: more would spill, and with this much shared
-                // memory a spilled register comes back from L2
+                const bool first = j == 0;
+                if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
+                tc_fence_after();
+                if (first) {
+                    lack = live ? qscale[row] : 1.f;
+                    rescale_q = __any_sync(0xffffffffu, lack != 1.f);
+                }
+                if (warp_live) {
+                    const uint32_t ss = n % kScaleSlots;
+                    const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 128;
+                    const int lv = uniform(exponents[w][ss]);
+                    const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
+                    const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
+                    float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
+                    __syncwarp();
+                    // the row's scores 32 columns at a time: more would spill, and with this much shared
+                    // memory a spilled register comes back from L2
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pr[16], bits = ~0u;
-                    bool some_hidden = false;
-                    if (masked) {
-                        const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
-                        bits = full == 32 ? ~0u : (1u << full) - 1;
-                        const int sh = from_t - ctx;   // block token of the first column
-                        if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
-                        some_hidden = __any_sync(0xffffffffu, bits != ~0u);
-                        if (!__any_sync(0xffffffffu, live && bits != 0)) {
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pr[16], bits = ~0u;
+                        bool some_hidden = false;
+                        if (masked) {
+                            const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
+                            bits = full == 32 ? ~0u : (1u << full) - 1;
+                            const int sh = from_t - ctx;   // block token of the first column
+                            if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
+                            some_hidden = __any_sync(0xffffffffu, bits != ~0u);
+                            if (!__any_sync(0xffffffffu, live && bits != 0)) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) pr[i] = 0;
-                            tmem_st16(my_s + 16u * (uint32_t)q, pr);
-                            continue;
+                                for (int i = 0; i < 16; ++i) pr[i] = 0;
+                                tmem_st16(my_s + 16u * (uint32_t)q, pr);
+                                continue;
+                            }
                         }
-                    }
-                    // the columns' sums, with the row's own factor
-                    auto load_x = [&](uint32_t (&x)[32]) {
-                        tmem_ld32(my_s + 32u * (uint32_t)q, x);
-                        tmem_ld_wait32(x);
-                        if (rescale_q) {
+                        // the columns' sums, with the row's own factor
+                        auto load_x = [&](uint32_t (&x)[32]) {
+                            tmem_ld32(my_s + 32u * (uint32_t)q, x);
+                            tmem_ld_wait32(x);
+                            if (rescale_q) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * lack);
-                        }
-                    };
-                    // scores in log2 units less `ref2` of four columns; those the row does not see -inf
-                    auto four = [&](const uint32_t (&x)[32], int i, uint64_t ref2, float (&y)[4], auto hidden) {
-                        const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + i);
-                        unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pack2(k4.x, k4.y), ref2), y[0], y[1]);
-                        unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), pack2(k4.z, k4.w), ref2), y[2], y[3]);
-                        if constexpr (decltype(hidden)::value) {
+                                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * lack);
+                            }
+                        };
+                        // scores in log2 units less `ref2` of four columns; those the row does not see -inf
+                        auto four = [&](const uint32_t (&x)[32], int i, uint64_t ref2, float (&y)[4], auto hidden) {
+                            const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + i);
+                            unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pack2(k4.x, k4.y), ref2), y[0], y[1]);
+                            unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), pack2(k4.z, k4.w), ref2), y[2], y[3]);
+                            if constexpr (decltype(hidden)::value) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
-                        }
-                    };
-                    // the terms to `pr`, and their sum
-                    auto terms = [&](const uint32_t (&x)[32], auto hidden) {
-                        const uint64_t ref2 = pack2(-ref, -ref);
-                        uint64_t sum[4] = {0, 0, 0, 0};
+                                for (int k = 0; k < 4; ++k)
+                                    if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
+                            }
+                        };
+                        // the terms to `pr`, and their sum
+                        auto terms = [&](const uint32_t (&x)[32], auto hidden) {
+                            const uint64_t ref2 = pack2(-ref, -ref);
+                            uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float y[4];
-                            four(x, i, ref2, y, hidden);
+                            for (int i = 0; i < 32; i += 4) {
+                                float y[4];
+                                four(x, i, ref2, y, hidden);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
-                            sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
-                            sum[(i >> 1 & 2) + 1] = add2(sum[(i >> 1 & 2) + 1], pack2(y[2], y[3]));
-                            pr[i >> 1] = half_pair(y[0], y[1]);
-                            pr[(i >> 1) + 1] = half_pair(y[2], y[3]);
-                        }
-                        float s0, s1;
-                        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
-                        return s0 + s1;
-                    };
-                    float s;
+                                for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
+                                sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
+                                sum[(i >> 1 & 2) + 1] = add2(sum[(i >> 1 & 2) + 1], pack2(y[2], y[3]));
+                                pr[i >> 1] = half_pair(y[0], y[1]);
+                                pr[(i >> 1) + 1] = half_pair(y[2], y[3]);
+                            }
+                            float s0, s1;
+                            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                            return s0 + s1;
+                        };
+                        float s;
 #pragma unroll 1
-                    for (int again = 0;; ++again) {
-                        uint32_t x[32];
-                        load_x(x);
-                        s = some_hidden ? terms(x, std::true_type{}) : terms(x, std::false_type{});
-                        // the reference has to move when a term could pass 2^15 (their sum says so), or
-                        // when there is none yet
-                        const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
-                        if (again || !__any_sync(0xffffffffu, moves)) break;
-                        float top = -INFINITY;
-                        load_x(x);
+                        for (int again = 0;; ++again) {
+                            uint32_t x[32];
+                            load_x(x);
+                            s = some_hidden ? terms(x, std::true_type{}) : terms(x, std::false_type{});
+                            // the reference has to move when a term could pass 2^15 (their sum says so), or
+                            // when there is none yet
+                            const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
+                            if (again || !__any_sync(0xffffffffu, moves)) break;
+                            float top = -INFINITY;
+                            load_x(x);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float y[4];
-                            four(x, i, 0, y, std::true_type{});
-                            top = max3(max3(top, y[0], y[1]), y[2], y[3]);
-                        }
-                        float f = 1.f;
-                        if (moves && top != -INFINITY) {     // (-inf: there is no number)
-                            const float r_new = ceilf(top) + (float)lv - kPeak;   // P <= 2^7
-                            f = fast_exp2(r - r_new);
-                            r = r_new;
-                            l *= f;
-                        }
-                        ref = r == -INFINITY ? 0.f : r - (float)lv;
-                        // what is summed so far: the output of earlier tiles (their product has ended, these
-                        // scores came after it) and this tile's P
-                        if (!first) {
+                            for (int i = 0; i < 32; i += 4) {
+                                float y[4];
+                                four(x, i, 0, y, std::true_type{});
+                                top = max3(max3(top, y[0], y[1]), y[2], y[3]);
+                            }
+                            float f = 1.f;
+                            if (moves && top != -INFINITY) {     // (-inf: there is no number)
+                                const float r_new = ceilf(top) + (float)lv - kPeak;   // P <= 2^7
+                                f = fast_exp2(r - r_new);
+                                r = r_new;
+                                l *= f;
+                            }
+                            ref = r == -INFINITY ? 0.f : r - (float)lv;
+                            // what is summed so far: the output of earlier tiles (their product has ended, these
+                            // scores came after it) and this tile's P
+                            if (!first) {
 #pragma unroll 1
-                            for (int i = 0; i < DP / 16; ++i) {
+                                for (int i = 0; i < DP / 16; ++i) {
+                                    uint32_t o[16];
+                                    tmem_ld16(my_o + 16u * (uint32_t)i, o);
+                                    tmem_ld_wait16(o);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                    tmem_st16(my_o + 16u * (uint32_t)i, o);
+                                }
+                            }
+                            const __half2 f2 = __float2half2_rn(f);
+                            tmem_st_wait();
+#pragma unroll 1
+                            for (int i = 0; i < q; ++i) {
                                 uint32_t o[16];
-                                tmem_ld16(my_o + 16u * (uint32_t)i, o);
+                                tmem_ld16(my_s + 16u * (uint32_t)i, o);
                                 tmem_ld_wait16(o);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                tmem_st16(my_o + 16u * (uint32_t)i, o);
+                                for (int k = 0; k < 16; ++k) {
+                                    const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&o[k]), f2);
+                                    o[k] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                                tmem_st16(my_s + 16u * (uint32_t)i, o);
                             }
                         }
-                        const __half2 f2 = __float2half2_rn(f);
-                        tmem_st_wait();
-#pragma unroll 1
-                        for (int i = 0; i < q; ++i) {
-                            uint32_t o[16];
-                            tmem_ld16(my_s + 16u * (uint32_t)i, o);
-                            tmem_ld_wait16(o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&o[k]), f2);
-                                o[k] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
-                            tmem_st16(my_s + 16u * (uint32_t)i, o);
-                        }
+                        l = fmaf(s, unit, l);
+                        // P's 16 columns lie below the scores still to be read
+                        tmem_st16(my_s + 16u * (uint32_t)q, pr);
                     }
-                    l = fmaf(s, unit, l);
-                    // P's 16 columns lie below the scores still to be read
-                    tmem_st16(my_s + 16u * (uint32_t)q, pr);
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready(w));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready(w));
             }
             if (!ok) break;
             {

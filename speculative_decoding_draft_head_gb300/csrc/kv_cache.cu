@@ -3,7 +3,7 @@
 // Both kernels move bytes: 2 D elements in and 2 D codes out per (token, kv
 // head), or the reverse.  What bounds a large call is the memory, as long as an
 // element costs few instructions; what bounds a small one is its launch and the
-// chain row -> request -> page -> token (append of 16 tokens: 7.3 us a call,
+// chain row -> request -> page -> token (append of 32 tokens: 7.4 us a call,
 // the Python call's own time).  A block takes some packed rows: its warps look
 // the rows' places up once, then groups of lanes take one head row each (8
 // elements a lane: 16-byte loads of bf16/fp16, 8-byte stores of codes, both
