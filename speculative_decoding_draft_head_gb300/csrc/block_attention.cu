@@ -36,9 +36,9 @@
 // parity would deceive it.  Every wait is bounded.
 //
 // What bounds it (SM clocks): a pair tile takes 5,500 to 5,900 where its products
-// take 2,048 and its exponentials 2,048, a single tile 3,000 to 3,400 where its
-// products take 1,024: the chain of issuer, product, softmax and issuer, as P
-// takes its scores' columns.  An item adds some 10,000 (queries, first reference,
+// take 2,048, its exponentials 1,024 and all its instructions 3,100 of every
+// scheduler; a single tile 3,000 to 3,400 where its products take 1,024: the
+// chain of issuer, product, softmax and issuer, as P takes its scores' columns.  An item adds some 10,000 (queries, first reference,
 // result), which is why the plan counts it.  Measured: 153 rows of 32 query
 // heads over 131,000 shared tokens in 405 us (810 TFLOP/s of the rows' products),
 // 64 single tokens of 64 heads over 300,000 own tokens in 272 us (2.3 TB/s).

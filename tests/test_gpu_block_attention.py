@@ -82,6 +82,16 @@ def test_shapes(name, fmt, dtype):
     _run(*SHAPES[name], fmt=fmt, dtype=dtype)
 
 
+@pytest.mark.parametrize("rows,prefix,Hq,Hkv,D", [
+    ([7] * 60, 300, 30, 6, 64),              # groups of 5: rows of one request on both sides of a row tile's end
+    ([7] * 60, 0, 30, 6, 64),                # rows that one worker finishes and rows that several share
+    ([1, 0, 6, 33] * 13, 140, 21, 3, 128),
+    ([1] * 331, 0, 30, 30, 48),              # a row a head: nothing to take together
+])
+def test_batches_with_several_rows_a_joining_warp(rows, prefix, Hq, Hkv, D):
+    _run(rows, [(37 * b) % 300 for b in range(len(rows))], prefix, Hq, Hkv, D, 16)
+
+
 @pytest.mark.parametrize("name", ["verify blocks", "prefix and blocks", "more rows than two tiles",
                                   "block longer than a tile"])
 def test_full_block(name):

@@ -96,6 +96,29 @@ def test_append_then_read_is_exact(rows, start, page, Hkv, D, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("Hkv,D", [(3, 64), (1, 16), (9, 32), (5, 80), (11, 128)])
+def test_many_rows_and_heads_that_divide_nothing(Hkv, D, fmt):
+    """More rows than fit a row a block, heads that end inside a step; rows and
+    heads of which no two are alike."""
+    rows, starts = [5001, 0, 1, 4999, 3], [3, 0, 15, 16, 31]
+    gen = torch.Generator().manual_seed(Hkv * D)
+    cache, table, row0, start = _setup(gen, rows, starts, 16, Hkv, D, fmt)
+    R = sum(rows)
+    k, v = [torch.randn((R, Hkv, D), generator=gen).to(torch.bfloat16) for _ in range(2)]
+    k[7, 0, 3], v[5003, Hkv - 1, D - 1] = math.inf, math.nan
+    dev = [t.cuda() for t in (table, start, row0)]
+    binding.kv_append(k.cuda(), v.cuda(), cache, *dev)
+    pg, off = _places(table, row0, start, 16)
+    got = binding.kv_read(cache, *dev, R, dtype=torch.float32)
+    for name, t, codes, scales in (("k", k, cache.k, cache.k_scale), ("v", v, cache.v, cache.v_scale)):
+        want, sc = plain_cache.quantise(t, fmt)
+        assert torch.equal(codes.view(torch.uint8).cpu()[pg, :, off], want.view(torch.uint8))
+        assert _same_floats(scales.cpu()[pg, :, off], sc)
+        assert _same_floats(got[name], want.float() * sc[..., None])
+    assert binding.read_device_flags(cache.flags) == binding.FLAG_NONFINITE
+
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
 def test_every_code_rounds_and_reads_as_defined(fmt):
     """A dense sweep of values in [-Q, Q] against the plain rounding; the row's
     largest element fixes the scale at 1."""
