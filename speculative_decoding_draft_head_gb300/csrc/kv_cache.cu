@@ -234,17 +234,23 @@ kv_read_kernel(dspark_kv_cache c, PagedRows p, T *__restrict__ k_out, T *__restr
     }
 }
 
-// Many rows a block once that still gives every SM four blocks, else one so
-// that a small call spreads over the SMs.
+// Several rows a block, or one so that a small call spreads over the SMs.
+// Measured with 8 heads, cold caches (one / several rows a block, us):
+//   writing   D = 128: 1,200 rows 8.2 / 12.3, 2,400 rows 12.3 / 12.3, 4,864 rows 18.4 / 14.3, 20,000 rows 45 / 31
+//             D =  64: 2,400 rows 10.2 / 14.3, 4,864 rows 14.3 / 14.3, 9,728 rows 22.5 / 16.4, 20,000 rows 39 / 21
+//   reading   D = 128: 600 rows 10.2 / 10.2, 1,200 rows 14.3 / 10.2, 20,000 rows 119 / 29
+//             D =  64: 600 rows 10.2 / 8.2, 1,200 rows 12.3 / 8.2, 20,000 rows 96 / 22
+// so: from two blocks an SM on for writing, from a block on every fourth SM on for reading.
 constexpr int kReadRows = 16;
-bool many(int n_rows, int rows) { return n_rows >= 4 * rows * kNumSMs; }
+bool append_many(int n_rows, int rows) { return n_rows >= 2 * rows * kNumSMs; }
+bool read_many(int n_rows) { return n_rows >= kReadRows * kNumSMs / 4; }
 
 template <typename T, int kFormat, int kLanes>
 void append_rows(const dspark_kv_cache &c, const PagedRows &p, const void *k, const void *v, int64_t ks, int64_t vs,
                  cudaStream_t s) {
     const T *kt = static_cast<const T *>(k), *vt = static_cast<const T *>(v);
     constexpr int kRows = 128 / kLanes;
-    if (many(p.n_rows, kRows))
+    if (append_many(p.n_rows, kRows))
         kv_append_kernel<T, kFormat, kLanes, true>
             <<<(p.n_rows + kRows - 1) / kRows, kAppendThreads, 0, s>>>(c, p, kt, vt, ks, vs);
     else
@@ -254,7 +260,7 @@ void append_rows(const dspark_kv_cache &c, const PagedRows &p, const void *k, co
 template <typename T, int kFormat, int kLanes>
 void read_rows(const dspark_kv_cache &c, const PagedRows &p, void *k, void *v, cudaStream_t s) {
     T *kt = static_cast<T *>(k), *vt = static_cast<T *>(v);
-    if (many(p.n_rows, kReadRows))
+    if (read_many(p.n_rows))
         kv_read_kernel<T, kFormat, kLanes, kReadRows>
             <<<(p.n_rows + kReadRows - 1) / kReadRows, kReadThreads, 0, s>>>(c, p, kt, vt);
     else
