@@ -190,13 +190,18 @@ class WorkspaceCache:
     def get(self, which, B, G, V, r, device):
         return self._sized(which, workspace_bytes(which, B, G, V, r), device)
 
-    def attention(self, B, n_rows, n_q_heads, n_kv_heads, head_dim, device):
-        """Address and bytes of the attention's workspace."""
-        n = attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim)
-        kept = self._attention.get(device)
-        if kept is None or kept[1] < n:
-            buf = self._sized("attention", n, device)
-            kept = self._attention[device] = (buf.data_ptr(), buf.numel())
+    def attention(self, n, device, stream, raw):
+        """An attention workspace of ``n`` bytes for a call on ``stream`` (None: the current one), whose handle is
+        ``raw``: address, bytes and the tensor to hold until the call is enqueued.  One per stream, as calls on two
+        streams may run at once; in a graph's capture one of the graph's own, which no later call can replace."""
+        kept = self._attention.get((device, raw))
+        capturing = torch.cuda.is_current_stream_capturing()
+        if capturing or kept is None or kept[1] < n:
+            with torch.cuda.stream(stream):      # (its memory is reused in that stream's order)
+                buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+            kept = (buf.data_ptr() + (-buf.data_ptr()) % 256, n, buf)
+            if not capturing:
+                self._attention[(device, raw)] = kept
         return kept
 
     def _sized(self, which, n, device):
@@ -543,7 +548,8 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     and over the request's own kv_len[b] cached tokens, the last ones of which
     are the block itself.  ``mask`` ("causal" or "full") or ``row_mask``
     ([n_rows] int64, bit t: the row sees token t of its block) rules inside the
-    block; ``scale`` is head_dim ** -0.5 by default.  See dspark_block_attention.
+    block; ``scale`` is head_dim ** -0.5 by default.  Without a ``workspace``
+    (attention_workspace_bytes, 256-byte aligned) one is kept per stream.  See dspark_block_attention.
 
     Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
     lib = _lib or load()
@@ -568,14 +574,15 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
             lse_p = out["lse"].data_ptr()
+    raw = _raw_stream(stream, cache)
     if workspace is None:
-        ws_p, ws_n = _default_ws.attention(B, n, Hq, cache.n_kv_heads, D, dev)
+        ws_p, ws_n, workspace = _default_ws.attention(attention_workspace_bytes(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
     else:
         ws_p, ws_n = workspace.data_ptr(), workspace.numel()
     _check(lib.dspark_block_attention(
         cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
         int(prefix_len), _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
-        lse_p, ws_p, ws_n, _raw_stream(stream, cache)))
+        lse_p, ws_p, ws_n, raw))
     return out
 
 

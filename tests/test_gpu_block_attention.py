@@ -277,6 +277,38 @@ def test_repeats_are_bit_equal_and_a_batch_does_not_change_a_request():
         assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
 
 
+def test_calls_on_two_streams_at_once_keep_apart():
+    """Calls without a workspace of their own on two streams, whose parts would meet in a shared one; and a captured
+    call, replayed after a larger call has wanted a larger workspace."""
+    shapes = [([6] * 50, [700] * 50, 1500, 8, 2, 64, 16), ([5] * 64, [300] * 64, 2100, 8, 2, 64, 16)]
+    calls = []
+    for i, (rows, ctx, prefix, Hq, Hkv, D, page) in enumerate(shapes):
+        want, q, pool, row0, lens = _run(rows, ctx, prefix, Hq, Hkv, D, page, seed=i, check=False)
+        kw = dict(q=q.cuda(), cache=pool.cache(binding), block_table=pool.table.cuda(),
+                  kv_len=torch.tensor(lens, dtype=torch.int32).cuda(), row0=row0.cuda(),
+                  prefix_pages=pool.prefix_pages.cuda(), prefix_len=prefix)
+        calls.append((kw, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(8):
+        for i, (kw, _) in enumerate(calls):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(binding.block_attention(**kw))
+    torch.cuda.synchronize()
+    for i, (_, want) in enumerate(calls):
+        for g in got[i]:
+            assert torch.equal(g["out"], want["out"]) and torch.equal(g["lse"], want["lse"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        out = binding.block_attention(**calls[0][0])
+    _run([2] * 90, [40] * 90, 64, 32, 4, 64, 16, check=False)
+    filler = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["out"], calls[0][1]["out"]) and all(int(f[0]) == 255 for f in filler)
+
+
 def test_a_captured_graph_follows_lengths_and_pages_on_its_own_stream():
     gen = torch.Generator().manual_seed(11)
     rows = [4, 1, 6]
