@@ -495,10 +495,12 @@ DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_he
  * give a NaN out and lse to the rows that see them and to no other.
  * Statistics and sums are fp32.  The operands of the tensor cores are fp16:
  * codes exactly, q scaled by a power of two (exact to 2^-25 of its row's
- * largest element), the softmax terms, and the values with their scale; the
- * last two are rounded (2^-11 each).
+ * largest element), and the softmax terms times the value scales, rounded once
+ * (2^-11; a token whose share falls 2^-32 below the largest of its row's is
+ * lost).  What a row does not see has no influence on it, whatever its size.
  * Limits: head_dim a multiple of 16 up to 128, page_size a multiple of 16,
- * scale finite and > 0, kv scales >= 0 (below 2^100).
+ * scale finite and > 0, kv scales >= 0 (below 2^100; value scales below 2^-100
+ * lose precision).
  */
 DSPARK_API dspark_status dspark_block_attention(
     const dspark_kv_cache *cache, const void *q, int64_t q_stride, dspark_dtype dtype, int n_q_heads,

@@ -10,13 +10,15 @@
 //   q . k~   codes are exact in fp16, and so is q after a power-of-two scaling (to
 //            2^-25 of its row's largest element); ks_j stays in fp32 and multiplies
 //            the sums, since rounding keys would err by 2^-11 of every score.
-//   P . V    V = v~_j vs_j 2^(6 - e) rounded to fp16 (2^e the power of two above the
-//            tile's largest vs, so a value scale costs the softmax nothing and
-//            no range), P = 2^(s_j - r + e) rounded to fp16.  r follows
-//            max_j s_j + e; it is an integer and moves only when P could pass
-//            2^15 of fp16's 2^16, then starting again at 2^7, and O is scaled by
-//            an exact power of two.
-// So the inner terms take two roundings of 2^-11, everything else is fp32.
+//   P . V    codes are exact again; P = 2^(s_j - r) (2^12 vs_j) rounded to fp16, from
+//            fp32 factors.  r is an integer, the row's own: it follows the largest
+//            s_j + log2 vs_j of the tokens that the row sees, whatever values
+//            others hold, and moves only when a P passes fp16's range, then
+//            starting again at 2^7, and O is scaled by an exact power of two.
+// So the inner terms take one rounding of 2^-11, everything else is fp32.
+// (The 2^12 sets where a term of l lies in fp32's range: the largest is 2^-105 for value
+// scales of 2^100 and 2^95 for those of 2^-100.  The reference also moves when 32 terms pass
+// 2^105, which those of values near 0 could without P showing it.)
 //
 // One CTA per SM walks its part of the plan's line of tiles (attention_plan.h),
 // 128 tokens a tile.  Roles (20 warps):
@@ -66,17 +68,19 @@ static_assert(256 * kSoftmaxRegs + 2 * kTeamWarps * 32 * kConvertRegs + 128 * kL
 constexpr int kCtas = kNumSMs;
 constexpr int kRing = 8;          // pieces of a group told ahead
 constexpr int kRounds = 4;        // rounds planned ahead
-constexpr int kScaleSlots = 4;    // tiles of a group whose key scales are held
+constexpr int kScaleSlots = 3;    // tiles of a group whose scales are held: the keys of tile t wait for a place that the
+                                  // values of tile t - 3 (or later ones) have left, so for the end of its softmax
 constexpr uint32_t kSpinLimit = 2000000000u;    // ~1 s of clock cycles (below the 32-bit clock's lap)
 constexpr long long kDrainLimit = 200000000LL;  // ~0.1 s: products in flight after a timeout
 
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: scores (and P) of the groups, then their outputs
 
-constexpr float kScaleFloor = 0x1p-100f;   // value scales below it lose precision, not range
+constexpr float kVUp = 0x1p12f, kVDown = 0x1p-12f;   // what value scales are multiplied by, and its inverse
+constexpr float kVLeast = -88.f;           // log2 of the least of these that the reference counts: value scales
+                                           // below 2^-100 lose precision, not range
 constexpr float kPeak = 7.f;               // log2 of P's largest bound when the reference moves ...
-constexpr float kMost = 32768.f;           // ... which it does when 32 terms of P sum to more than this
-constexpr int kVUp = 6;                    // log2 of what V is multiplied by: its codes reach 448 * 2^6 in fp16
-constexpr float kVDown = 0x1p-6f;
+constexpr uint32_t kPast = 0x7c00u;        // ... which it does when a P reaches these bits, fp16's infinity,
+constexpr float kSumMost = 0x1p105f;       // or when 32 terms of l sum to more than this
 constexpr float kQUp = 16.f;               // what q is multiplied by before it becomes fp16 ...
 constexpr int kQLow = -4, kQHigh = 11;     // ... when its row's largest element lies in [2^-4, 2^11)
 
@@ -90,12 +94,12 @@ struct Layout {
     static constexpr int kOps = 3;                    // fp16 operand ring (K and V tiles)
     static constexpr int kRaw = DP == 128 ? 3 : 6;    // ring of tiles as loaded
     static constexpr uint32_t kTileBytes = 128 * DP * 2;
-    static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales, with the values theirs
+    static constexpr uint32_t kRawBytes = 128 * DP + 1024;  // codes; with the keys both scales
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kOp = kQ + 2 * kTileBytes;
     static constexpr uint32_t kRawAt = kOp + kOps * kTileBytes;
-    static constexpr uint32_t kScale = kRawAt + kRaw * kRawBytes;        // [groups][slots][128] key scales
-    static constexpr uint32_t kQScale = kScale + 2 * kScaleSlots * 512;  // [groups][2 pieces][128]
+    static constexpr uint32_t kScale = kRawAt + kRaw * kRawBytes;         // [groups][slots][2][128] scales: keys', values'
+    static constexpr uint32_t kQScale = kScale + 2 * kScaleSlots * 1024;  // [groups][2 pieces][128]
     static constexpr uint32_t kBytes = kQScale + 2048 + 1024;            // + alignment slack
 };
 
@@ -180,6 +184,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -195,25 +204,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float fast_log2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
     return r;
 }
-
-// e such that every value scale of a tile is below 2^e: `vs` are the tile's 128
-// scales in shared memory (16-byte aligned), of which the first `valid` exist
-// except for the 16-token chunks in `bad`.  The whole warp, all lanes alike.
-__device__ __forceinline__ int scale_exponent(uint32_t vs, int valid, int bad, int lane) {
-    const uint4 v = ld_shared_v4(vs + 16u * (uint32_t)lane);
-    const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
-    float top = kScaleFloor;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (4 * lane + i < valid && x[i] <= 3.4028235e38f) top = fmaxf(top, x[i]);
-    if (bad >> (lane >> 2) & 1) top = kScaleFloor;
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    return min((int)(bits >> 23) - 126, 120);
+// x * 2^d for a whole d <= 0 (or -inf), in two steps: references lie up to some 200 apart, and what is far
+// below a new one can be of any size in l
+__device__ __forceinline__ float scale_down(float x, float d) {
+    const float a = fmaxf(d, -120.f);
+    return x * fast_exp2(a) * fast_exp2(d - a);
 }
 
 // Bounded wait of a whole warp on one barrier: false when it took longer than
@@ -560,7 +565,6 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     __shared__ int group_pieces[2][kRing];          // pieces of the softmax groups: slot, flags
     __shared__ Stream streams[2];
     __shared__ Round rounds[kRounds];
-    __shared__ int exponents[2][kScaleSlots];       // of the value scales of the groups' tiles
     __shared__ int raw_bad[kRaw];
     __shared__ int64_t scan[2][kThreads / 32];
     __shared__ Line line;
@@ -735,8 +739,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 
     // Loads the keys or values of a tile, chunk `mine` in lanes 0 .. 7 (and again in 8 .. 15 and so
     // on), to place `position` of the order of operands, in runs of tokens that share a page: their
-    // codes or (another warp) their scales.  (Copies by the warp's own cp.async, 512 bytes at a time,
-    // held it up: 2300 clocks a tile.)
+    // codes or (another warp) with the keys the scales of both.  (Copies by the warp's own cp.async,
+    // 512 bytes at a time, held it up: 2300 clocks a tile.)
     const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
     auto load = [&](uint32_t mine, bool is_v, uint32_t position, bool codes) {
         const int i = lane & 7;
@@ -749,7 +753,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
         if (lane == 0) {
             if (codes) raw_bad[slot] = (int)bad;
-            mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (codes ? D : is_v ? 4 : 8)));
+            mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (codes ? D : is_v ? 0 : 8)));
         }
         __syncwarp();
         const bool leader = elect_one();
@@ -762,10 +766,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 bulk_load(at + (uint32_t)(r * run * D),
                           static_cast<const unsigned char *>(is_v ? c.v : c.k) + first * (uint32_t)D, (uint32_t)(run * D),
                           raw_full(slot));
-            } else {
+            } else if (!is_v) {
                 const uint32_t to = at + 128u * DP + (uint32_t)(r * run * 4), bytes = (uint32_t)(run * 4);
                 bulk_load(to + 512u, c.v_scale + first, bytes, raw_full(slot));
-                if (!is_v) bulk_load(to, c.k_scale + first, bytes, raw_full(slot));
+                bulk_load(to, c.k_scale + first, bytes, raw_full(slot));
             }
         }
         __syncwarp();
@@ -785,7 +789,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     auto convert_all = [&](const bool is_v) {
         const int t = (tid - kConvertAt * 32) & (kTeamWarps * 32 - 1);
         const float up = a.scale * kLog2e / kQUp;    // scores in log2 units: folded into the keys' scales
-        uint32_t group_tiles = 0;                    // tiles of the groups so far, 16 bits each
+        uint32_t scale_slots = 0;                    // where the groups' next scales go, 8 bits each
         uint32_t group_pieces_seen = 0;              // parity of the groups' pieces
         int valid = 0;                               // tokens of the tile that exist (128 or more: all)
         Order order = {0, 0, 0, false, false};
@@ -821,29 +825,16 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             if (!warp_wait(op_empty(op), ((position / kOps) & 1) ^ 1, abort)) return false;
             if (!warp_wait(raw_full(slot), (position / kRaw) & 1, abort)) return false;
             const uint32_t src = base + L::kRawAt + slot * L::kRawBytes, dst = base + L::kOp + op * L::kTileBytes;
-            const uint32_t raw_scale = src + 128u * DP;   // key scales, then value scales
+            const uint32_t raw_scale = src + 128u * DP;   // with the keys: key scales, then value scales
             const int bad = uniform(raw_bad[slot]);
             const bool whole = there_are >= plan::kTile && bad == 0;
-            const int exponent = scale_exponent(raw_scale + 512u, there_are, bad, lane);
             auto there = [&](int row) { return whole || (row < there_are && !(bad >> (row >> 4) & 1)); };
-            // values: times their scale as hi + lo, so that the product is rounded once; 2^(kVUp - e)
-            // leaves the tile's largest below 2^15
-            const float v_unit = __uint_as_float((uint32_t)(127 + kVUp - exponent) << 23);
-            auto row_factor = [&](int row, __half2 &hi, __half2 &lo) {
-                const float v = ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)row), f = v <= 3.4028235e38f && there(row) ? v * v_unit : 0.f;
-                hi = __float2half2_rn(f);
-                lo = __float2half2_rn(f - __low2float(hi));
-            };
-            auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch, __half2 hi, __half2 lo) {
+            auto decode_store = [&](uint4 in, uint32_t row, uint32_t ch) {
                 __half2 h[8];
                 decode4<kFormat>(in.x, h[0], h[1]);
                 decode4<kFormat>(in.y, h[2], h[3]);
                 decode4<kFormat>(in.z, h[4], h[5]);
                 decode4<kFormat>(in.w, h[6], h[7]);
-                if (is_v) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = __hfma2(h[i], hi, __hmul2(h[i], lo));
-                }
                 const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
                 const uint32_t at = dst + (ch >> 2) * (128u * 128u) + row * 128u, c8 = (ch & 3u) * 2u;
                 st_shared_v4(at + ((c8 ^ (row & 7u)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
@@ -855,23 +846,25 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 return there(row) ? in : make_uint4(0, 0, 0, 0);
             };
             if (!is_v) {
-                // the tile's key scales (of scores in log2 units), for the softmax groups; a token whose
-                // value scale (or page) is no number carries its NaN in the key's alone: where it is
-                // masked, its zero values must not become 0 times NaN
-                float ks = 0.f;
-                if (t < there_are)
-                    ks = there(t) && ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)t) <= 3.4028235e38f
-                             ? ld_shared_f32(raw_scale + 4u * (uint32_t)t) * up
-                             : __int_as_float(0x7fffffff);
+                // the tile's scales for the softmax groups: keys' (of scores in log2 units) and values'; a token
+                // whose value scale (or page) is no number carries its NaN in the key's alone: where it is
+                // masked, its zero weight must not become 0 times NaN
+                float ks = 0.f, vs = 0.f;
+                if (t < there_are) {
+                    const float v = ld_shared_f32(raw_scale + 512u + 4u * (uint32_t)t);
+                    const bool good = there(t) && v <= 3.4028235e38f;
+                    ks = good ? ld_shared_f32(raw_scale + 4u * (uint32_t)t) * up : __int_as_float(0x7fffffff);
+                    vs = good ? fminf(v * kVUp, 3.4028235e38f) : 0.f;
+                }
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (!(flags >> w & 1)) continue;
-                    const uint32_t i = (group_tiles >> (16 * w)) % kScaleSlots;
-                    st_shared_f32(base + L::kScale + ((uint32_t)(w * kScaleSlots) + i) * 512u + 4u * (uint32_t)t, ks);
-                    if (t == 0) exponents[w][i] = exponent;
+                    const uint32_t i = scale_slots >> (8 * w) & 3u;
+                    const uint32_t to = base + L::kScale + ((uint32_t)(w * kScaleSlots) + i) * 1024u + 4u * (uint32_t)t;
+                    st_shared_f32(to, ks);
+                    st_shared_f32(to + 512u, vs);
+                    scale_slots += i + 1 == kScaleSlots ? 0u - (i << (8 * w)) : 1u << (8 * w);
                 }
-                // (counts of 16 bits: the carry of the lower is kept out of the upper)
-                group_tiles = ((group_tiles + (flags & 1)) & 0xffffu) | ((group_tiles & 0xffff0000u) + ((uint32_t)(flags >> 1 & 1) << 16));
             }
             if (D == DP) {
                 constexpr int kSteps = DP / 32;     // two chunks each: of one row (D = 128), of two rows
@@ -879,32 +872,25 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll 1
                 for (int step = 0; step < kSteps; ++step) {
                     uint4 in[2];
-                    __half2 hi[2] = {}, lo[2] = {};
                     auto row_of = [&](int i) {
                         return DP == 128 ? 2 * ((t >> 3) + 16 * step) + odd : (t >> 2) + 32 * (2 * step + i);
                     };
                     auto chunk_of = [&](int i) { return (t & 3) + (DP == 128 ? 4 * (odd ^ i) : 0); };
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        in[i] = read(row_of(i), chunk_of(i), DP / 16);
-                        if (is_v && (DP == 64 || i == 0)) row_factor(row_of(i), hi[i], lo[i]);
-                    }
-                    if (DP == 128) hi[1] = hi[0], lo[1] = lo[0];
+                    for (int i = 0; i < 2; ++i) in[i] = read(row_of(i), chunk_of(i), DP / 16);
                     if (step + 1 == kSteps) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(raw_empty(slot));
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) decode_store(in[i], (uint32_t)row_of(i), (uint32_t)chunk_of(i), hi[i], lo[i]);
+                    for (int i = 0; i < 2; ++i) decode_store(in[i], (uint32_t)row_of(i), (uint32_t)chunk_of(i));
                 }
             } else {
                 const int width = D / 16;
 #pragma unroll 1
                 for (int i = t; i < 128 * width; i += 32 * kTeamWarps) {
                     const int row = i / width;
-                    __half2 hi = {}, lo = {};
-                    if (is_v) row_factor(row, hi, lo);
-                    decode_store(read(row, i - row * width, width), (uint32_t)row, (uint32_t)(i - row * width), hi, lo);
+                    decode_store(read(row, i - row * width, width), (uint32_t)row, (uint32_t)(i - row * width));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty(slot));
@@ -1131,11 +1117,9 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 }
                 if (warp_live) {
                     const uint32_t ss = n % kScaleSlots;
-                    const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 128;
-                    const int lv = uniform(exponents[w][ss]);
-                    const float unit = __uint_as_float((uint32_t)(127 - lv) << 23);   // a term of P in units of l
+                    const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 256, *vs = ks + 128;
                     const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
-                    float ref = r == -INFINITY ? 0.f : r - (float)lv;     // P's reference
+                    float ref = r == -INFINITY ? 0.f : r;
                     __syncwarp();
                     // the row's scores 32 columns at a time: more would spill, and with this much shared
                     // memory a spilled register comes back from L2
@@ -1176,7 +1160,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                     if (!(bits >> (i + k) & 1u)) y[k] = -INFINITY;
                             }
                         };
-                        // the terms to `pr`, and their sum
+                        // the softmax terms' sum; to `pr` what they weigh the values' codes with
                         auto terms = [&](const uint32_t (&x)[32], auto hidden) {
                             const uint64_t ref2 = pack2(-ref, -ref);
                             uint64_t sum[4] = {0, 0, 0, 0};
@@ -1186,8 +1170,12 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                 four(x, i, ref2, y, hidden);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) y[k] = fast_exp2(y[k]);
-                                sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], pack2(y[0], y[1]));
-                                sum[(i >> 1 & 2) + 1] = add2(sum[(i >> 1 & 2) + 1], pack2(y[2], y[3]));
+                                const uint64_t y01 = pack2(y[0], y[1]), y23 = pack2(y[2], y[3]);
+                                sum[i >> 1 & 2] = add2(sum[i >> 1 & 2], y01);
+                                sum[(i >> 1 & 2) + 1] = add2(sum[(i >> 1 & 2) + 1], y23);
+                                const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * q + i);
+                                unpack2(mul2(y01, pack2(v4.x, v4.y)), y[0], y[1]);
+                                unpack2(mul2(y23, pack2(v4.z, v4.w)), y[2], y[3]);
                                 pr[i >> 1] = half_pair(y[0], y[1]);
                                 pr[(i >> 1) + 1] = half_pair(y[2], y[3]);
                             }
@@ -1201,9 +1189,13 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             uint32_t x[32];
                             load_x(x);
                             s = some_hidden ? terms(x, std::true_type{}) : terms(x, std::false_type{});
-                            // the reference has to move when a term could pass 2^15 (their sum says so), or
-                            // when there is none yet
-                            const bool moves = live && (s > kMost || (r == -INFINITY && bits != 0));
+                            // the reference has to move when a P or the sum has passed its bound, or when there
+                            // is none yet (never for a row that is NaN already)
+                            uint32_t most = 0;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) most = __vimax3_u16x2(most, pr[i], pr[i + 1]);
+                            const bool past = max(most & 0xffffu, most >> 16) >= kPast || s > kSumMost;
+                            const bool moves = live && l == l && (past || (r == -INFINITY && bits != 0));
                             if (again || !__any_sync(0xffffffffu, moves)) break;
                             float top = -INFINITY;
                             load_x(x);
@@ -1211,16 +1203,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                             for (int i = 0; i < 32; i += 4) {
                                 float y[4];
                                 four(x, i, 0, y, std::true_type{});
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) y[k] += fmaxf(fast_log2(vs[32 * q + i + k]), kVLeast);
                                 top = max3(max3(top, y[0], y[1]), y[2], y[3]);
                             }
                             float f = 1.f;
                             if (moves && top != -INFINITY) {     // (-inf: there is no number)
-                                const float r_new = ceilf(top) + (float)lv - kPeak;   // P <= 2^7
-                                f = fast_exp2(r - r_new);
+                                const float r_new = ceilf(top) - kPeak;   // P <= 2^7
+                                f = scale_down(1.f, r - r_new);
+                                l = scale_down(l, r - r_new);
                                 r = r_new;
-                                l *= f;
                             }
-                            ref = r == -INFINITY ? 0.f : r - (float)lv;
+                            ref = r == -INFINITY ? 0.f : r;
                             // what is summed so far: the output of earlier tiles (their product has ended, these
                             // scores came after it) and this tile's P
                             if (!first) {
@@ -1249,7 +1243,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                                 tmem_st16(my_s + 16u * (uint32_t)i, o);
                             }
                         }
-                        l = fmaf(s, unit, l);
+                        l += s;
                         // P's 16 columns lie below the scores still to be read
                         tmem_st16(my_s + 16u * (uint32_t)q, pr);
                     }
@@ -1417,12 +1411,12 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
                 float t = fmaxf(top, st.x);
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-                const float keep = top == -INFINITY && l == 0.f ? 0.f : fast_exp2(top - t);
-                const float f = saw ? fast_exp2(st.x - t) : 0.f;
-                float s = saw ? st.y * f : 0.f;
+                const float keep = top == -INFINITY && l == 0.f ? 0.f : scale_down(1.f, top - t);
+                const float f = saw ? scale_down(1.f, st.x - t) : 0.f;
+                float s = saw ? scale_down(st.y, st.x - t) : 0.f;
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                l = l * keep + s;
+                l = (top == -INFINITY && l == 0.f ? 0.f : scale_down(l, top - t)) + s;
                 top = t;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[k] *= keep;

@@ -80,7 +80,7 @@ def block_sees(mask, words, n):
     return t[None, :] <= t[:, None] if mask == "causal" else torch.ones((n, n), dtype=torch.bool)
 
 
-def attention(q, pool, row0, lens, mask="causal", words=None, scale=None):
+def attention(q, pool, row0, lens, mask="causal", words=None, scale=None, terms=2.0 ** -10):
     """out, lse and their bounds, in 64 bits.
 
     With p_j the softmax, A = max_j scale sum_d |q_d k_jd| and n seen tokens:
@@ -93,6 +93,7 @@ def attention(q, pool, row0, lens, mask="causal", words=None, scale=None):
       q of fp16 or bf16 is exact in fp16 after a power-of-two scaling, but for
         elements 2^-14 below the row's largest: 2^-24 max|q| sum_d |k_jd|
       sums: fp32 over n terms in many partial sums: 2^-18
+      (`terms` bounds the fp16 roundings: 2^-10 for the two above, 2^-11 for one)
       output: eps / 2 relative, and half the least subnormal."""
     R, Hq, D = q.shape
     scale = D ** -0.5 if scale is None else scale
@@ -132,7 +133,7 @@ def attention(q, pool, row0, lens, mask="causal", words=None, scale=None):
             out[r:r + n, g] = o
             lse[r:r + n, g] = torch.logsumexp(s, -1)
             tol_out[r:r + n, g] = (half * o.abs().nan_to_num(0) * (1 + 2.0 ** -8)
-                                   + (2 * ds + 2.0 ** -10 + 2.0 ** -18)[:, None] * spread
+                                   + (2 * ds + terms + 2.0 ** -18)[:, None] * spread
                                    + (sees.sum(1) * 2.0 ** -30 * vmax)[:, None]
                                    + torch.finfo(q.dtype).smallest_normal * torch.finfo(q.dtype).eps / 2)
             tol_lse[r:r + n, g] = ds + 2.0 ** -18 + 2.0 ** -22 * lse[r:r + n, g].abs().nan_to_num(0, posinf=0)
