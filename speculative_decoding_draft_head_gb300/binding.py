@@ -8,6 +8,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -139,6 +140,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call's own tensors are made: in the order of the stream that writes them (None: the current one).  Memory
+    of another stream's order might still be read there, or be given away again before the call has run."""
+    return _AS_IT_IS if stream is None else torch.cuda.stream(stream)
+
+
 def _dtype_code(t):
     if t.dtype == torch.bfloat16:
         return DSPARK_BF16
@@ -197,7 +207,7 @@ class WorkspaceCache:
         kept = self._attention.get((device, raw))
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing or kept is None or kept[1] < n:
-            with torch.cuda.stream(stream):      # (its memory is reused in that stream's order)
+            with _on(stream):
                 buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
             kept = (buf.data_ptr() + (-buf.data_ptr()) % 256, n, buf)
             if not capturing:
@@ -233,11 +243,12 @@ def draft_sample(base, e_in, w_out, anchor, temperature, request_id=None, seed=0
     _need(temperature, "temperature", dtype=torch.float32, shape=(B,), device=dev)
     rid = _rid(request_id, B, dev)
     if out is None:
-        out = dict(tokens=torch.empty((B, G), dtype=torch.int32, device=dev),
-                   lse=torch.empty((B, G), dtype=torch.float32, device=dev),
-                   logq=torch.empty((B, G), dtype=torch.float32, device=dev))
-        if store_logits:
-            out["logits"] = torch.empty((B, G, V), dtype=torch.float32, device=dev)
+        with _on(stream):
+            out = dict(tokens=torch.empty((B, G), dtype=torch.int32, device=dev),
+                       lse=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       logq=torch.empty((B, G), dtype=torch.float32, device=dev))
+            if store_logits:
+                out["logits"] = torch.empty((B, G, V), dtype=torch.float32, device=dev)
     ws = workspace if workspace is not None else _default_ws.get(WS_DRAFT, B, G, V, r, dev)
     _check(lib.dspark_draft_sample(
         _ptr(base), _ptr(e_in), _ptr(w_out), _ptr(anchor), _ptr(temperature), _ptr(rid),
@@ -265,13 +276,14 @@ def draft_sample_rnn(base, e_in, w_h, w_out, anchor, temperature, request_id=Non
     _need(temperature, "temperature", dtype=torch.float32, shape=(B,), device=dev)
     rid = _rid(request_id, B, dev)
     if out is None:
-        out = dict(tokens=torch.empty((B, G), dtype=torch.int32, device=dev),
-                   lse=torch.empty((B, G), dtype=torch.float32, device=dev),
-                   logq=torch.empty((B, G), dtype=torch.float32, device=dev))
-        if store_logits:
-            out["logits"] = torch.empty((B, G, V), dtype=torch.float32, device=dev)
-        if store_states:
-            out["h"] = torch.empty((B, G, r), dtype=torch.bfloat16, device=dev)
+        with _on(stream):
+            out = dict(tokens=torch.empty((B, G), dtype=torch.int32, device=dev),
+                       lse=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       logq=torch.empty((B, G), dtype=torch.float32, device=dev))
+            if store_logits:
+                out["logits"] = torch.empty((B, G, V), dtype=torch.float32, device=dev)
+            if store_states:
+                out["h"] = torch.empty((B, G, r), dtype=torch.bfloat16, device=dev)
     ws = workspace if workspace is not None else _default_ws.get(WS_DRAFT_RNN, B, G, V, r, dev)
     _check(lib.dspark_draft_sample_rnn(
         _ptr(base), _ptr(e_in), _ptr(w_h), _ptr(w_out), _ptr(anchor), _ptr(temperature), _ptr(rid),
@@ -298,10 +310,11 @@ def schedule_prefix(conf_logits, pos_temp, sps, L_min, L_max, *, policy=SCHED_EA
     _need(pos_temp, "pos_temp", dtype=torch.float32, shape=(G,), device=dev)
     _need(sps, "sps", dtype=torch.float32, device=dev)
     if out is None:
-        out = dict(conf=torch.empty((B, G), dtype=torch.float32, device=dev),
-                   cum_conf=torch.empty((B, G), dtype=torch.float32, device=dev),
-                   verify_len=torch.empty((B,), dtype=torch.int32, device=dev),
-                   theta=torch.empty((1,), dtype=torch.float64, device=dev))
+        with _on(stream):
+            out = dict(conf=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       cum_conf=torch.empty((B, G), dtype=torch.float32, device=dev),
+                       verify_len=torch.empty((B,), dtype=torch.int32, device=dev),
+                       theta=torch.empty((1,), dtype=torch.float64, device=dev))
     ws = workspace if workspace is not None else _default_ws.get(WS_SCHEDULE, B, G, 8, 1, dev)
     _check(lib.dspark_schedule_policy(
         _ptr(conf_logits), _ptr(pos_temp), _ptr(sps), sps.numel(), B, G, int(L_min), int(L_max),
@@ -337,7 +350,8 @@ class LaggedScheduler:
         res = schedule_prefix(src, self.pos_temp, self.sps, self.L_min, self.L_max, policy=self.policy,
                               threshold=self.threshold, out=out, stream=stream)
         if self.lag > 0:
-            self._ring.append(conf_logits.clone())
+            with _on(stream):
+                self._ring.append(conf_logits.clone())
             if len(self._ring) > self.lag:
                 self._ring.pop(0)
         return res
@@ -378,11 +392,12 @@ def verify(target, base, e_in, w_out, anchor, draft, verify_len, temperature, re
     _need(temperature, "temperature", dtype=torch.float32, shape=(B,), device=dev)
     rid = _rid(request_id, B, dev)
     if out is None:
-        out = dict(accept_len=torch.empty((B,), dtype=torch.int32, device=dev),
-                   out_tokens=torch.empty((B, G + 1), dtype=torch.int32, device=dev),
-                   num_out=torch.empty((B,), dtype=torch.int32, device=dev),
-                   target_lse=torch.empty((B, G + 1), dtype=torch.float32, device=dev),
-                   logp=torch.empty((B, G), dtype=torch.float32, device=dev))
+        with _on(stream):
+            out = dict(accept_len=torch.empty((B,), dtype=torch.int32, device=dev),
+                       out_tokens=torch.empty((B, G + 1), dtype=torch.int32, device=dev),
+                       num_out=torch.empty((B,), dtype=torch.int32, device=dev),
+                       target_lse=torch.empty((B, G + 1), dtype=torch.float32, device=dev),
+                       logp=torch.empty((B, G), dtype=torch.float32, device=dev))
     ws = workspace if workspace is not None else _default_ws.get(WS_VERIFY, B, G, V, r, dev)
     args = (_ptr(base), _ptr(e_in), _ptr(w_out), _ptr(draft_logits), _ptr(anchor),
             _ptr(draft["tokens"]), _ptr(draft["lse"]), _ptr(draft["logq"]), _ptr(verify_len),
@@ -415,9 +430,10 @@ def pack_target(target, verify_len, *, out=None, stream=None):
     if verify_len is not None:
         _need(verify_len, "verify_len", dtype=torch.int32, shape=(B,), device=dev)
     if out is None:
-        out = dict(target=torch.empty((B * G1, V), dtype=target.dtype, device=dev),
-                   row0=torch.empty((B,), dtype=torch.int64, device=dev),
-                   n_rows=torch.empty((1,), dtype=torch.int64, device=dev))
+        with _on(stream):
+            out = dict(target=torch.empty((B * G1, V), dtype=target.dtype, device=dev),
+                       row0=torch.empty((B,), dtype=torch.int64, device=dev),
+                       n_rows=torch.empty((1,), dtype=torch.int64, device=dev))
     _check(lib.dspark_pack_target(_ptr(target), _ptr(verify_len), B, G1 - 1, V, _dtype_code(target),
                                   _ptr(out["target"]), _ptr(out["row0"]), _ptr(out.get("n_rows")),
                                   _stream(stream)))
@@ -526,7 +542,8 @@ def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, ou
         raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
     if out is None:
-        out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev))
+        with _on(stream):
+            out = dict(k=torch.empty(shape, dtype=dtype, device=dev), v=torch.empty(shape, dtype=dtype, device=dev))
     else:
         for name in out:
             _need(out[name], name, dtype=dtype, shape=shape, device=dev)
@@ -565,8 +582,9 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
         pages_p = _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
     words_p = None if row_mask is None else _vec(row_mask, "row_mask", torch.int64, n, cache)
     if out is None:
-        out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
-                   lse=torch.empty((n, Hq), dtype=torch.float32, device=dev))
+        with _on(stream):
+            out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
+                       lse=torch.empty((n, Hq), dtype=torch.float32, device=dev))
         lse_p = out["lse"].data_ptr()
     else:
         _need(out["out"], "out", dtype=q.dtype, shape=(n, Hq, D), device=dev)
@@ -600,11 +618,12 @@ def verify_noalloc(target, base, e_in, w_out, anchor, draft, verify_len, tempera
     _need(target, "target", device=dev)
     r = e_in.shape[1] if e_in is not None else 16
     if out is None:
-        out = dict(accept_len=torch.empty((B,), dtype=torch.int32, device=dev),
-                   out_tokens=torch.empty((B, G + 1), dtype=torch.int32, device=dev),
-                   num_out=torch.empty((B,), dtype=torch.int32, device=dev),
-                   target_lse=torch.empty((B, G + 1), dtype=torch.float32, device=dev),
-                   logp=torch.empty((B, G), dtype=torch.float32, device=dev))
+        with _on(stream):
+            out = dict(accept_len=torch.empty((B,), dtype=torch.int32, device=dev),
+                       out_tokens=torch.empty((B, G + 1), dtype=torch.int32, device=dev),
+                       num_out=torch.empty((B,), dtype=torch.int32, device=dev),
+                       target_lse=torch.empty((B, G + 1), dtype=torch.float32, device=dev),
+                       logp=torch.empty((B, G), dtype=torch.float32, device=dev))
     rid = _rid(request_id, B, dev)
     _check(lib.dspark_verify_noalloc(
         _ptr(target), _ptr(base), _ptr(e_in), _ptr(w_out), _ptr(draft_logits), _ptr(anchor),
