@@ -134,7 +134,17 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _on_current_device(index, stream):
+    """The library launches on the current device: a call's tensors, on device ``index``, and its stream have to be there."""
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % index)
+    if stream is not None and getattr(stream, "device_index", index) != index:
+        raise ValueError("the stream is of cuda:%d, the tensors are on cuda:%d" % (stream.device_index, index))
+
+
+def _stream(stream, device=None):
+    if device is not None:
+        _on_current_device(device.index, stream)
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
@@ -254,7 +264,7 @@ def draft_sample(base, e_in, w_out, anchor, temperature, request_id=None, seed=0
         _ptr(base), _ptr(e_in), _ptr(w_out), _ptr(anchor), _ptr(temperature), _ptr(rid),
         B, G, V, r, _dtype_code(base), int(seed) & 0xFFFFFFFFFFFFFFFF,
         _ptr(out["tokens"]), _ptr(out["lse"]), _ptr(out["logq"]), _ptr(out.get("logits")),
-        _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(ws), ws.numel(), _stream(stream, dev)))
     return out
 
 
@@ -289,7 +299,7 @@ def draft_sample_rnn(base, e_in, w_h, w_out, anchor, temperature, request_id=Non
         _ptr(base), _ptr(e_in), _ptr(w_h), _ptr(w_out), _ptr(anchor), _ptr(temperature), _ptr(rid),
         B, G, V, r, DSPARK_BF16, int(seed) & 0xFFFFFFFFFFFFFFFF,
         _ptr(out["tokens"]), _ptr(out["lse"]), _ptr(out["logq"]), _ptr(out.get("logits")),
-        _ptr(out.get("h")), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(out.get("h")), _ptr(ws), ws.numel(), _stream(stream, dev)))
     return out
 
 
@@ -320,7 +330,7 @@ def schedule_prefix(conf_logits, pos_temp, sps, L_min, L_max, *, policy=SCHED_EA
         _ptr(conf_logits), _ptr(pos_temp), _ptr(sps), sps.numel(), B, G, int(L_min), int(L_max),
         int(policy), float(threshold),
         _ptr(out["conf"]), _ptr(out["cum_conf"]), _ptr(out["verify_len"]), _ptr(out.get("theta")),
-        _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(ws), ws.numel(), _stream(stream, dev)))
     return out
 
 
@@ -405,7 +415,7 @@ def verify(target, base, e_in, w_out, anchor, draft, verify_len, temperature, re
             int(seed) & 0xFFFFFFFFFFFFFFFF,
             _ptr(out["accept_len"]), _ptr(out["out_tokens"]), _ptr(out["num_out"]),
             _ptr(out.get("target_lse")), _ptr(out.get("logp")), _ptr(ws), ws.numel(),
-            _stream(stream))
+            _stream(stream, dev))
     if target_row0 is None:
         _check(lib.dspark_verify(_ptr(target), *args))
     else:
@@ -436,7 +446,7 @@ def pack_target(target, verify_len, *, out=None, stream=None):
                        n_rows=torch.empty((1,), dtype=torch.int64, device=dev))
     _check(lib.dspark_pack_target(_ptr(target), _ptr(verify_len), B, G1 - 1, V, _dtype_code(target),
                                   _ptr(out["target"]), _ptr(out["row0"]), _ptr(out.get("n_rows")),
-                                  _stream(stream)))
+                                  _stream(stream, dev)))
     return out
 
 
@@ -513,7 +523,10 @@ def _paged(block_table, start, name, row0, cache):
 
 
 def _raw_stream(stream, cache):
-    return torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else stream.cuda_stream
+    if stream is None and torch._C._cuda_getDevice() == cache._index:
+        return torch._C._cuda_getCurrentRawStream(cache._index)
+    _on_current_device(cache._index, stream)
+    return stream.cuda_stream
 
 
 def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
@@ -522,13 +535,14 @@ def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
     [B+1] int64) at position start[b] + i of the request's pages
     (``block_table`` [B, max_pages] int32).  See dspark_kv_append."""
     lib = _lib or load()
+    raw = _raw_stream(stream, cache)
     B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
     if k.dtype not in _ROW_DTYPES or v.dtype is not k.dtype or v.shape != k.shape:
         raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
     ks = _row_stride(k, "k", cache.n_kv_heads, cache)
     vs = _row_stride(v, "v", cache.n_kv_heads, cache)
     _check(lib.dspark_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, _ROW_DTYPES[k.dtype], row0_p,
-                                k.shape[0], start_p, table_p, max_pages, B, _raw_stream(stream, cache)))
+                                k.shape[0], start_p, table_p, max_pages, B, raw))
 
 
 def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, out=None, stream=None):
@@ -537,6 +551,7 @@ def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, ou
     ``out`` with only one of them reads that one.  See dspark_kv_read."""
     lib = _lib or load()
     dev = cache.device
+    raw = _raw_stream(stream, cache)
     B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
     if dtype not in _ROW_DTYPES:
         raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
@@ -548,7 +563,7 @@ def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, ou
         for name in out:
             _need(out[name], name, dtype=dtype, shape=shape, device=dev)
     _check(lib.dspark_kv_read(cache._ref, row0_p, n_rows, start_p, table_p, max_pages, B, _ROW_DTYPES[dtype],
-                              _ptr(out.get("k")), _ptr(out.get("v")), _raw_stream(stream, cache)))
+                              _ptr(out.get("k")), _ptr(out.get("v")), raw))
     return out
 
 
@@ -571,6 +586,7 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
     lib = _lib or load()
     dev = cache.device
+    raw = _raw_stream(stream, cache)
     B, max_pages, table_p, len_p, row0_p = _paged(block_table, kv_len, "kv_len", row0, cache)
     if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise TypeError("q must be bfloat16 or float16, got %s" % q.dtype)
@@ -592,10 +608,10 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
             lse_p = out["lse"].data_ptr()
-    raw = _raw_stream(stream, cache)
     if workspace is None:
         ws_p, ws_n, workspace = _default_ws.attention(attention_workspace_bytes(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
     else:
+        _need(workspace, "workspace", device=dev)
         ws_p, ws_n = workspace.data_ptr(), workspace.numel()
     _check(lib.dspark_block_attention(
         cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
@@ -631,7 +647,7 @@ def verify_noalloc(target, base, e_in, w_out, anchor, draft, verify_len, tempera
         _ptr(temperature), _ptr(rid), B, G, V, r, _dtype_code(target),
         int(seed) & 0xFFFFFFFFFFFFFFFF,
         _ptr(out["accept_len"]), _ptr(out["out_tokens"]), _ptr(out["num_out"]),
-        _ptr(out.get("target_lse")), _ptr(out.get("logp")), _stream(stream)))
+        _ptr(out.get("target_lse")), _ptr(out.get("logp")), _stream(stream, dev)))
     return out
 
 
