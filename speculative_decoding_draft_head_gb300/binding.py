@@ -215,7 +215,8 @@ class WorkspaceCache:
         ``raw``: address, bytes and the tensor to hold until the call is enqueued.  One per stream, as calls on two
         streams may run at once; in a graph's capture one of the graph's own, which no later call can replace."""
         kept = self._attention.get((device, raw))
-        capturing = torch.cuda.is_current_stream_capturing()
+        with _on(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
         if capturing or kept is None or kept[1] < n:
             with _on(stream):
                 buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
