@@ -31,7 +31,8 @@
  *    stream).  Calls only enqueue work: they do not synchronise.
  *  - `workspace` is caller-owned device scratch memory of at least
  *    dspark_workspace_bytes(...) bytes, 256-byte aligned.  One workspace must
- *    not be shared by two calls that may run concurrently.
+ *    not be shared by two calls that may run concurrently, nor by host threads
+ *    that do not take turns: a call may be several launches.
  *  - Host-side argument errors return DSPARK_ERR_INVALID_ARG before any launch
  *    and leave the outputs untouched.  CUDA launch errors return
  *    DSPARK_ERR_CUDA.  The message of the last failure on the calling thread

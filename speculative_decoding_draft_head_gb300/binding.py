@@ -206,6 +206,7 @@ class WorkspaceCache:
     def __init__(self):
         self._bufs = {}
         self._attention = {}
+        self.lock = threading.Lock()    # held while a call that shares a buffer is enqueued
 
     def get(self, which, B, G, V, r, device):
         return self._sized(which, workspace_bytes(which, B, G, V, r), device)
@@ -609,15 +610,18 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
             lse_p = out["lse"].data_ptr()
-    if workspace is None:
-        ws_p, ws_n, workspace = _default_ws.attention(attention_workspace_bytes(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
-    else:
-        _need(workspace, "workspace", device=dev)
-        ws_p, ws_n = workspace.data_ptr(), workspace.numel()
-    _check(lib.dspark_block_attention(
-        cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
-        int(prefix_len), _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
-        lse_p, ws_p, ws_n, raw))
+    # (two launches that meet in the workspace: another thread's must not come in between)
+    with _default_ws.lock if workspace is None else _AS_IT_IS:
+        if workspace is None:
+            ws_p, ws_n, workspace = _default_ws.attention(attention_workspace_bytes(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
+        else:
+            _need(workspace, "workspace", device=dev)
+            ws_p, ws_n = workspace.data_ptr(), workspace.numel()
+        status = lib.dspark_block_attention(
+            cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
+            int(prefix_len), _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
+            lse_p, ws_p, ws_n, raw)
+    _check(status)
     return out
 
 

@@ -1,6 +1,7 @@
 """Which workspace an attention call without one gets, and when another call may
 use it (no GPU is used here: the library and the streams are stand-ins)."""
 import contextlib
+import threading
 import types
 
 import pytest
@@ -71,3 +72,41 @@ def test_a_capture_on_a_stream_that_is_not_current_gets_its_own(setting):
     assert captured != kept and binding._default_ws._attention == held
     seen.capturing.clear()
     assert call(5) == kept
+
+
+def test_calls_of_two_threads_are_enqueued_one_after_the_other(setting):
+    """The call's two launches meet in the workspace: while one thread enqueues them, no other may use it."""
+    lib, _, call = setting
+    first_inside, second_inside = threading.Event(), threading.Event()
+    together = []
+
+    def inside(workspace):
+        if not first_inside.is_set():
+            first_inside.set()
+            # (a second caller would come in here, with the same buffer)
+            together.append(second_inside.wait(0.5))
+        else:
+            second_inside.set()
+
+    lib.inside = inside
+    one = threading.Thread(target=call, args=(5,))
+    one.start()
+    assert first_inside.wait(10)
+    two = threading.Thread(target=call, args=(5,))
+    two.start()
+    one.join(10)
+    two.join(10)
+    assert together == [False] and second_inside.is_set() and len(lib.workspaces) == 2
+
+
+def test_a_failing_call_lets_the_next_one_in(setting):
+    lib, _, call = setting
+
+    def fail(workspace):
+        raise RuntimeError("no")
+
+    lib.inside = fail
+    with pytest.raises(RuntimeError):
+        call(5)
+    lib.inside = lambda workspace: None
+    call(5)
