@@ -516,8 +516,12 @@ def _row_stride(t, name, heads, cache):
     return row if n > 1 else h * d
 
 
-def _paged(block_table, start, name, row0, cache):
+def _paged(block_table, start, name, row0, cache, n_rows, n_tokens=0, n_pages=0):
     B, max_pages = block_table.shape
+    # ctypes would pass on the low 32 bits of a larger number (one below 0 the library refuses)
+    if (n_rows | n_tokens | n_pages | B | max_pages) >> 31:
+        if any(not -0x80000000 <= n <= 0x7fffffff for n in (n_rows, n_tokens, n_pages, B, max_pages)):
+            raise ValueError("numbers of requests, pages, rows and tokens must be below 2^31")
     if not (block_table.dtype is torch.int32 and block_table.get_device() == cache._index and block_table.is_contiguous()):
         _need(block_table, "block_table", dtype=torch.int32, device=cache.device)
     return (B, max_pages, block_table.data_ptr(), _vec(start, name, torch.int32, B, cache),
@@ -538,7 +542,7 @@ def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
     (``block_table`` [B, max_pages] int32).  See dspark_kv_append."""
     lib = _lib or load()
     raw = _raw_stream(stream, cache)
-    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache, k.shape[0])
     if k.dtype not in _ROW_DTYPES or v.dtype is not k.dtype or v.shape != k.shape:
         raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
     ks = _row_stride(k, "k", cache.n_kv_heads, cache)
@@ -554,7 +558,7 @@ def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, ou
     lib = _lib or load()
     dev = cache.device
     raw = _raw_stream(stream, cache)
-    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache)
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache, n_rows)
     if dtype not in _ROW_DTYPES:
         raise TypeError("rows must be bf16, fp16 or fp32, got %s" % dtype)
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
@@ -589,15 +593,14 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     lib = _lib or load()
     dev = cache.device
     raw = _raw_stream(stream, cache)
-    B, max_pages, table_p, len_p, row0_p = _paged(block_table, kv_len, "kv_len", row0, cache)
+    prefix_len = int(prefix_len)
+    n_pages = 0 if prefix_pages is None else prefix_pages.numel()
+    B, max_pages, table_p, len_p, row0_p = _paged(block_table, kv_len, "kv_len", row0, cache, q.shape[0], prefix_len, n_pages)
     if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise TypeError("q must be bfloat16 or float16, got %s" % q.dtype)
     n, Hq, D = q.shape
     qs = _row_stride(q, "q", Hq, cache)
-    pages_p, n_pages = None, 0
-    if prefix_pages is not None:
-        n_pages = prefix_pages.numel()
-        pages_p = _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
+    pages_p = None if prefix_pages is None else _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
     words_p = None if row_mask is None else _vec(row_mask, "row_mask", torch.int64, n, cache)
     if out is None:
         with _on(stream):
@@ -619,7 +622,7 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
             ws_p, ws_n = workspace.data_ptr(), workspace.numel()
         status = lib.dspark_block_attention(
             cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
-            int(prefix_len), _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
+            prefix_len, _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
             lse_p, ws_p, ws_n, raw)
     _check(status)
     return out
