@@ -103,5 +103,14 @@ DSPARK_HD int first_tile(int cls, int64_t u, int64_t start, int tiles) {
     return (int)(t < tiles ? t : tiles);
 }
 
+// Places of a ring that a loader has filled, 0, 1, 2 .. in order: those whose
+// copies may still be under way are the last `held` ones.
+struct Filled {
+    uint32_t n;
+    DSPARK_HD void add(uint32_t position) { n = position + 1; }
+    DSPARK_HD uint32_t held(uint32_t ring) const { return n < ring ? n : ring; }
+    DSPARK_HD uint32_t place(uint32_t i) const { return n - 1 - i; }   // the i-th last
+};
+
 }  // namespace plan
 }  // namespace dspark

@@ -776,12 +776,6 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         if (codes && bad && lane == 0) atomicOr(c.flags, kFlagBadPage);
         return true;
     };
-    // a loader that gives up waits for the last copies: they must land before the block's memory goes
-    auto drain_copies = [&](uint32_t position) {
-        for (uint32_t i = 0; i < (uint32_t)kRaw && i <= position; ++i)
-            mbar_wait(raw_full((position - i) % kRaw), ((position - i) / kRaw) & 1, never, kDrainLimit);
-    };
-
     // One team of converters: the keys or the values of all tiles, and half of the queries.  The lanes of a quarter
     // warp take four chunks each of the lower and the upper 64 columns of an even and an odd row:
     // neither their loads nor their stores (the swizzle takes even chunks of an odd row to odd places)
@@ -956,6 +950,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             // -------------------------------------------------------- loaders --
             uint32_t ids = kNoChunk;
             Order order = {0, 0, 0, false, false};
+            plan::Filled filled = {0};
             const bool ok = for_tiles([&](int flags, int id, int i, const Round &r) {
                 const bool end = flags & kTileEnd, pair = (flags & 3) == 3;
                 const uint32_t before = ids;
@@ -964,13 +959,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll 1
                 for (int v = end ? 1 : 0; v < (order.has_v ? 2 : 1); ++v) {
                     const uint32_t position = v ? order.v : order.k;
-                    if (load(v && !pair ? before : ids, v, position, warp == kCodes)) continue;
-                    drain_copies(position);
-                    return false;
+                    if (!load(v && !pair ? before : ids, v, position, warp == kCodes)) return false;
+                    filled.add(position);
                 }
                 return true;
             });
-            if (!ok && lane == 0) *abort = 1;
+            if (!ok) {
+                // whatever failed, the copies under way must land before the block's memory goes (the place that
+                // the other loader has not filled too takes the whole limit)
+                if (lane == 0) *abort = 1;
+                for (uint32_t i = 0; i < filled.held(kRaw); ++i)
+                    mbar_wait(raw_full(filled.place(i) % kRaw), (filled.place(i) / kRaw) & 1, never, kDrainLimit);
+            }
         } else if (warp == kIssuer) {
             // ------------------------------------------- tensor-core products --
             // the whole warp walks the loop, so that addresses stay warp-uniform; one lane issues
