@@ -234,23 +234,33 @@ kv_read_kernel(dspark_kv_cache c, PagedRows p, T *__restrict__ k_out, T *__restr
     }
 }
 
-// Several rows a block, or one so that a small call spreads over the SMs.
-// Measured with 8 heads, cold caches (one / several rows a block, us):
-//   writing   D = 128: 1,200 rows 8.2 / 12.3, 2,400 rows 12.3 / 12.3, 4,864 rows 18.4 / 14.3, 20,000 rows 45 / 31
-//             D =  64: 2,400 rows 10.2 / 14.3, 4,864 rows 14.3 / 14.3, 9,728 rows 22.5 / 16.4, 20,000 rows 39 / 21
-//   reading   D = 128: 600 rows 10.2 / 10.2, 1,200 rows 14.3 / 10.2, 20,000 rows 119 / 29
-//             D =  64: 600 rows 10.2 / 8.2, 1,200 rows 12.3 / 8.2, 20,000 rows 96 / 22
-// so: from two blocks an SM on for writing, from a block on every fourth SM on for reading.
+// Several rows a block, or one so that a small call spreads over the SMs.  A block of several rows works through
+// its heads one after the other, so that the crossing lies the higher the wider a row is.  Measured, cold caches
+// (one / several rows a block, us):
+//   writing bf16  D = 128, 1 head: 1,200 rows 5.2 / 5.0, 4,864 rows 11.2 / 5.8
+//                 D = 128, 8 heads: 2,400 rows 8.4 / 9.6, 4,864 rows 13.3 / 10.9
+//                 D = 128, 32 heads: 4,864 rows 26.5 / 30.0, 9,728 rows 48.2 / 42.3
+//                 D = 64: 1 head 2,400 rows 7.5 / 6.7, 8 heads 4,864 rows 11.7 / 10.1, 32 heads 9,728 rows 30.0 / 31.0
+//   writing fp32  D = 128, 8 heads: 1,200 rows 8.2 / 9.9, 2,400 rows 11.6 / 10.3
+//   reading bf16  D = 128: 1 head 300 rows 5.1 / 5.2, 8 heads 600 rows 8.0 / 7.8, 32 heads 1,200 rows 12.1 / 19.1 and
+//                 2,400 rows 19.4 / 18.9;  D = 64: 8 heads 600 rows 7.7 / 6.3, 32 heads 1,200 rows 10.8 / 10.8
+//   reading fp32  D = 128, 8 heads: 600 rows 8.2 / 10.1, 1,200 rows 11.0 / 10.1
 constexpr int kReadRows = 16;
-bool append_many(int n_rows, int rows) { return n_rows >= 2 * rows * kNumSMs; }
-bool read_many(int n_rows) { return n_rows >= kReadRows * kNumSMs / 4; }
+template <typename T>
+bool append_many(int n_rows, int rows, int heads) {     // `rows`: of a block
+    return (int64_t)n_rows * (sizeof(T) == 4 ? 6 : 4) >= (int64_t)(3 * rows + 6 * heads) * kNumSMs;
+}
+template <typename T>
+bool read_many(int n_rows, int heads, int D) {
+    return (int64_t)n_rows * 1024 >= (1536 + 2 * (int64_t)heads * D * (int64_t)sizeof(T)) * kNumSMs;
+}
 
 template <typename T, int kFormat, int kLanes>
 void append_rows(const dspark_kv_cache &c, const PagedRows &p, const void *k, const void *v, int64_t ks, int64_t vs,
                  cudaStream_t s) {
     const T *kt = static_cast<const T *>(k), *vt = static_cast<const T *>(v);
     constexpr int kRows = 128 / kLanes;
-    if (append_many(p.n_rows, kRows))
+    if (append_many<T>(p.n_rows, kRows, c.n_kv_heads))
         kv_append_kernel<T, kFormat, kLanes, true>
             <<<(p.n_rows + kRows - 1) / kRows, kAppendThreads, 0, s>>>(c, p, kt, vt, ks, vs);
     else
@@ -260,7 +270,7 @@ void append_rows(const dspark_kv_cache &c, const PagedRows &p, const void *k, co
 template <typename T, int kFormat, int kLanes>
 void read_rows(const dspark_kv_cache &c, const PagedRows &p, void *k, void *v, cudaStream_t s) {
     T *kt = static_cast<T *>(k), *vt = static_cast<T *>(v);
-    if (read_many(p.n_rows))
+    if (read_many<T>(p.n_rows, c.n_kv_heads, c.head_dim))
         kv_read_kernel<T, kFormat, kLanes, kReadRows>
             <<<(p.n_rows + kReadRows - 1) / kReadRows, kReadThreads, 0, s>>>(c, p, kt, vt);
     else
