@@ -32,18 +32,20 @@
 // one order: of pairs K0 V0 K1 V1 .., so that a tile's values are converted
 // under the products of the tile before; of singles K0 K1 V0 K2 V1 .., keys one
 // tile ahead, so that a group's scores are ready while the other group's softmax
-// runs.  Every ring is filled in this order or freed in it, and the converter
-// teams wait for their operand's place before they look for its codes: so no
-// wait is more than one lap of a ring away from the phase that it tests, whose
+// runs.  Every ring is filled in this order or freed in it, both loaders arrive on
+// every place of theirs (so that neither can be a lap ahead of the other), and the
+// converter teams wait for their operand's place before they look for its codes: so
+// no wait is more than one lap of a ring away from the phase that it tests, whose
 // parity would deceive it.  Every wait is bounded.
 //
-// What bounds it (SM clocks): a pair tile takes 5,500 to 5,900 where its products
-// take 2,048, its exponentials 1,024 and all its instructions 3,100 of every
-// scheduler; a single tile 3,000 to 3,400 where its products take 1,024: the
-// chain of issuer, product, softmax and issuer, as P takes its scores' columns.  An item adds some 10,000 (queries, first reference,
+// What bounds it (SM clocks): a pair tile takes 5,100 to 5,600 where its products
+// take 2,048, its exponentials 1,024 and all its instructions 2,900 of every
+// scheduler; a single tile 2,700 to 3,000 where its products take 1,024: the
+// chain of issuer, product, softmax and issuer, as P takes its scores' columns.  An
+// item adds some 6,700 to a CTA with two groups at work (queries, first reference,
 // result), which is why the plan counts it.  Measured: 153 rows of 32 query
-// heads over 131,000 shared tokens in 405 us (810 TFLOP/s of the rows' products),
-// 64 single tokens of 64 heads over 300,000 own tokens in 272 us (2.3 TB/s).
+// heads over 131,000 shared tokens in 408 us (805 TFLOP/s of the rows' products),
+// 64 single tokens of 64 heads over 300,000 own tokens in 240 us (2.7 TB/s).
 // The roles' loops together nearly fill the instruction cache, so less code
 // was faster again and again: 64 scores at a time instead of 32 cost 1 to 10%, two
 // issuing warps 7%, 24 warps with the issuer apart from the converters 15%.
@@ -257,32 +259,6 @@ __device__ __forceinline__ void store8(float *to, const uint32_t *x, float f) {
                  : "memory");
 }
 
-// A row's output from TMEM, times f, to `out` or (when there is none) to `part`; out of line, as it runs once
-// an item.  The whole warp.
-template <typename T>
-__device__ __noinline__ void store_result(uint32_t from, T *out, float *part, int D, bool live, float f) {
-#pragma unroll 1
-    for (int at = 0; at < D; at += 16) {
-        uint32_t o[16];
-        tmem_ld16(from + (uint32_t)at, o);
-        tmem_ld_wait16(o);
-        if (live && out) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = float_to_pair<T>(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
-                *reinterpret_cast<uint4 *>(out + at + i) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        } else if (live) {
-            store8(part + at, &o[0], f);
-            store8(part + at + 8, &o[8], f);
-        }
-        __syncwarp();
-    }
-}
-
 // ------------------------------------------------------------------ the plan --
 // The line as a CTA sees it.
 struct Line {
@@ -291,7 +267,7 @@ struct Line {
 };
 
 // Walks one worker's pieces of a class.  Lives in shared memory and is stepped
-// out of line by the producer warp, all lanes alike: it runs once a piece, and
+// out of line by the planner's warp, all lanes alike: it runs once a piece, and
 // its registers and code would burden the loop over tiles.
 struct Walk {
     int64_t u, hi, start;             // cursor, end, first unit of the item at the cursor

@@ -3,8 +3,8 @@
 // Both kernels move bytes: 2 D elements in and 2 D codes out per (token, kv
 // head), or the reverse.  What bounds a large call is the memory, as long as an
 // element costs few instructions; what bounds a small one is its launch and the
-// chain row -> request -> page -> token (append of 32 tokens: 7.4 us a call,
-// the Python call's own time).  A block takes some packed rows: its warps look
+// chain row -> request -> page -> token (append of 32 tokens: 3.1 us on the
+// device, of a Python call's 7.5 us).  A block takes some packed rows: its warps look
 // the rows' places up once, then groups of lanes take one head row each (8
 // elements a lane: 16-byte loads of bf16/fp16, 8-byte stores of codes, both
 // whole lines per head row) with several head rows in flight.
@@ -13,8 +13,9 @@
 namespace dspark {
 namespace {
 
-// Threads a block: writing takes 135 us with 128 and 139 us with 256 (the
-// prompts below), reading 125 us with 256 and 127 us with 128.
+// Threads a block (the kernels alone, on the prompts and contexts below): writing
+// takes 128 us with 128 and 136 us with 256; reading is as fast with either, 116
+// us with 256 and 114 us with 128.
 constexpr int kAppendThreads = 128;
 constexpr int kReadThreads = 256;
 
@@ -109,8 +110,8 @@ __device__ __forceinline__ uint32_t top_of_row(const uint32_t (&top)[4], int sub
 // What bounds a large call after the memory is the issue of instructions, so
 // the work that is one a head row, its maximum's exchange and two divisions,
 // is done for four head rows at once, by a lane each: 125,000 tokens of 8 heads
-// of 128 bf16 elements take 130 us (5.9 TB/s, 88% of a copy's rate) and took
-// 220 us with that work done by every lane.
+// of 128 bf16 elements take 130 us a call (6.0 TB/s, 88% of a copy's rate) and took
+// 220 us with that work done by every lane; fp32 elements 184 us (7.0 TB/s).
 template <typename T, int kFormat, int kLanes, bool kMany>
 __global__ void __launch_bounds__(kAppendThreads)
 kv_append_kernel(dspark_kv_cache c, PagedRows p, const T *__restrict__ k, const T *__restrict__ v, int64_t k_stride,
@@ -177,8 +178,10 @@ kv_append_kernel(dspark_kv_cache c, PagedRows p, const T *__restrict__ k, const 
 }
 
 // Reading.  A group of lanes takes kUnroll head rows at a time; 119,000 tokens
-// of 8 heads of 128 elements to bf16 take 119 us (6.2 TB/s, 91% of a copy's
-// rate) with 16 rows a block and 8 in flight, 125 us with 8 and 4.
+// of 8 heads of 128 elements to bf16 take 119 us a call (6.2 TB/s, 91% of a copy's
+// rate; the kernel alone 116 us with 16 rows a block and 8 in flight, 120 us with
+// 8 and 4).  125,000 tokens to fp32 take 238 us (5.4 TB/s): four of the five bytes
+// that such a call moves are written.
 constexpr int kUnroll = 8;
 template <typename T, int kFormat, int kLanes, int kRows>
 __global__ void __launch_bounds__(kReadThreads)
