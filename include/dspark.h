@@ -489,7 +489,8 @@ DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_he
  *
  * q [n_rows][n_q_heads][head_dim] bf16 or fp16 with rows q_stride elements
  * apart, 16-byte aligned rows; out [n_rows][n_q_heads][head_dim] of the same
- * type, contiguous; lse [n_rows][n_q_heads] fp32 (natural logarithm) or NULL.
+ * type, contiguous, not overlapping q (other rows may still be read when one is
+ * written); lse [n_rows][n_q_heads] fp32 (natural logarithm) or NULL.
  * A request whose kv_len is below n_b or beyond max_pages pages (or, with
  * row_mask, whose n_b passes 64) is flagged and its rows are NaN; a page
  * outside the cache is flagged; its tokens, like those stored with a NaN scale,

@@ -136,6 +136,11 @@ dspark_status dspark_block_attention(const dspark_kv_cache *cache, const void *q
     if (!aligned(workspace, 256)) return fail(DSPARK_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (workspace_bytes < need)
         return fail(DSPARK_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    // (the bytes from the first to the last row of q)
+    const int64_t q_bytes = ((n_rows - 1) * q_stride + (int64_t)n_q_heads * cache->head_dim) * 2;
+    const int64_t out_bytes = (int64_t)n_rows * n_q_heads * cache->head_dim * 2;
+    const char *qb = static_cast<const char *>(q), *ob = static_cast<const char *>(out);
+    if (ob < qb + q_bytes && qb < ob + out_bytes) return fail(DSPARK_ERR_INVALID_ARG, "out must not overlap q");
     const AttentionArgs a{*cache, p, q, q_stride, dtype, n_q_heads, prefix_pages, prefix_len, (int)mask, row_mask, scale,
                           out, lse, static_cast<unsigned char *>(workspace)};
     const cudaError_t e = launch_block_attention(a, static_cast<cudaStream_t>(stream));
