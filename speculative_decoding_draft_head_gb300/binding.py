@@ -542,13 +542,16 @@ def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
     (``block_table`` [B, max_pages] int32).  See dspark_kv_append."""
     lib = _lib or load()
     raw = _raw_stream(stream, cache)
-    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache, k.shape[0])
-    if k.dtype not in _ROW_DTYPES or v.dtype is not k.dtype or v.shape != k.shape:
+    shape, dtype = k.shape, k.dtype
+    n = shape[0]
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache, n)
+    code = _ROW_DTYPES.get(dtype)
+    if code is None or v.dtype is not dtype or v.shape != shape:
         raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
     ks = _row_stride(k, "k", cache.n_kv_heads, cache)
     vs = _row_stride(v, "v", cache.n_kv_heads, cache)
-    _check(lib.dspark_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, _ROW_DTYPES[k.dtype], row0_p,
-                                k.shape[0], start_p, table_p, max_pages, B, raw))
+    _check(lib.dspark_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, code, row0_p, n, start_p, table_p,
+                                max_pages, B, raw))
 
 
 def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, out=None, stream=None):
