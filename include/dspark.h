@@ -466,6 +466,65 @@ DSPARK_API dspark_status dspark_kv_read(
     const int32_t *block_table, int max_pages, int B, dspark_dtype dtype, void *k_out, void *v_out,
     void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  Pair i of a head of D elements, i < n_pairs, is elements
+ * i and n_pairs + i, or, with `adjacent`, 2 i and 2 i + 1; elements from
+ * 2 n_pairs on pass as they are.  At position p a pair (a, b) becomes
+ *   (a cos t - b sin t, b cos t + a sin t),   t = p * w_i,
+ * in fp32, sine and cosine within 2^-23 of those of the exact angle for every
+ * position of 31 bits: the angle is the integer product p * step[i] modulo 2^64,
+ * with step[i] = w_i / (2 pi) * 2^64 modulo 2^64 (rounded).
+ * Positions of several axes (time, height, width): pair i takes the position of
+ * axis axis[i]; axis NULL means one axis.
+ */
+typedef struct dspark_rotary {
+    const uint64_t *step;  /* [n_pairs], device */
+    const int32_t *axis;   /* [n_pairs] values in [0, n_axes), device, or NULL (then n_axes is 1) */
+    int32_t n_pairs;       /* a multiple of 4, 2 n_pairs <= head_dim */
+    int32_t n_axes;
+    int32_t adjacent;      /* 0 or 1 */
+} dspark_rotary;
+
+/*
+ * Turn rows by their positions, or back (`inverse` = 1: t = -p * w_i, which is
+ * also the gradient of the turning with respect to its rows).
+ * x, out [n_rows][n_heads][head_dim] dtype (bf16, fp16 or fp32), rows and heads
+ * apart by the strides given in elements, every one a multiple of 16 bytes, so that
+ * slices of a fused projection and heads-first layouts can be passed; the
+ * sizes that are 1 need no stride.  out may be x with the same strides, else
+ * the two must not overlap.  positions [n_axes][n_rows] int32, any sign.
+ * fp32 inside, one rounding to dtype.
+ * Limits: head_dim a multiple of 8 up to 256, n_heads at most 65536; either the heads
+ * of a row or the rows of a head lie inside one stride of the other.
+ */
+DSPARK_API dspark_status dspark_rotary_rows(
+    const dspark_rotary *rotary, const void *x, int64_t row_stride, int64_t head_stride, int n_rows, int n_heads,
+    int head_dim, dspark_dtype dtype, const int32_t *positions, int inverse, void *out, int64_t out_row_stride,
+    int64_t out_head_stride, void *stream);
+
+/*
+ * dspark_kv_append with the keys turned by their positions on the way, and the
+ * queries of the same rows turned beside them.
+ *
+ * Row i of request b goes to position start[b] + i of the request, as in
+ * dspark_kv_append, and is turned by offset + start[b] + i on every axis (offset:
+ * the length of a shared prefix, say), or by positions [n_axes][n_rows] int32
+ * when given (offset must be 0 then).  Keys are quantised from the turned fp32
+ * values: they are not rounded to dtype in between.  A key row that holds an inf
+ * or a NaN after the turning is stored as dspark_kv_append stores one.
+ * q [n_rows][n_q_heads][head_dim] of the same dtype with rows q_stride elements
+ * apart, or NULL (then n_q_heads, q_out and its stride are not used); q_out
+ * likewise, q itself with its stride or not overlapping q, k and v.  Rows that
+ * belong to no request are neither read from nor written to, in the cache or q_out;
+ * queries of a row whose place is no good are turned all the same.
+ * Limits: those of dspark_kv_append; at most 65536 heads.
+ */
+DSPARK_API dspark_status dspark_kv_append_rotary(
+    const dspark_kv_cache *cache, const dspark_rotary *rotary, const void *q, int64_t q_stride, int n_q_heads,
+    const void *k, const void *v, int64_t k_stride, int64_t v_stride, dspark_dtype dtype, const int64_t *row0,
+    int n_rows, const int32_t *start, const int32_t *block_table, int max_pages, int B, const int32_t *positions,
+    int64_t offset, void *q_out, int64_t q_out_stride, void *stream);
+
 /* Bytes of workspace of dspark_block_attention for n_rows packed rows of
  * n_q_heads heads.  Returns 0 for invalid sizes. */
 DSPARK_API size_t dspark_attention_workspace_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);

@@ -11,8 +11,10 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import os
 import threading
+from fractions import Fraction
 
 import torch
 
@@ -40,7 +42,8 @@ EXPORTS = ("dspark_version", "dspark_last_error", "dspark_workspace_bytes", "dsp
            "dspark_schedule_prefix", "dspark_schedule_policy", "dspark_verify", "dspark_read_device_flags",
            "dspark_verify_noalloc", "dspark_draft_sample_rnn", "dspark_verify_packed", "dspark_pack_target",
            "dspark_selftest_bounded_wait", "dspark_read_noalloc_flags", "dspark_selftest_philox_rate",
-           "dspark_kv_append", "dspark_kv_read", "dspark_attention_workspace_bytes", "dspark_block_attention")
+           "dspark_kv_append", "dspark_kv_read", "dspark_attention_workspace_bytes", "dspark_block_attention",
+           "dspark_rotary_rows", "dspark_kv_append_rotary")
 
 _lib = None
 _lock = threading.Lock()
@@ -50,6 +53,12 @@ class _CacheStruct(ctypes.Structure):
     """struct dspark_kv_cache"""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "flags")]
                 + [(n, ctypes.c_int32) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "format")])
+
+
+class _RotaryStruct(ctypes.Structure):
+    """struct dspark_rotary"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("step", "axis")]
+                + [(n, ctypes.c_int32) for n in ("n_pairs", "n_axes", "adjacent")])
 
 
 class DSparkError(RuntimeError):
@@ -119,6 +128,12 @@ def load(build_if_missing: bool = True):
         L.dspark_block_attention.restype = ctypes.c_int
         L.dspark_block_attention.argtypes = [cache_p, vp, i64, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32, i32,
                                              i32, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        rotary_p = ctypes.POINTER(_RotaryStruct)
+        L.dspark_rotary_rows.restype = ctypes.c_int
+        L.dspark_rotary_rows.argtypes = [rotary_p, vp, i64, i64, i32, i32, i32, i32, vp, i32, vp, i64, i64, vp]
+        L.dspark_kv_append_rotary.restype = ctypes.c_int
+        L.dspark_kv_append_rotary.argtypes = [cache_p, rotary_p, vp, i64, i32, vp, vp, i64, i64, i32, vp, i32, vp, vp, i32,
+                                              i32, vp, i64, vp, i64, vp]
         L.dspark_read_noalloc_flags.restype = ctypes.c_int
         L.dspark_read_noalloc_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         _lib = L
@@ -552,6 +567,132 @@ def kv_append(k, v, cache, block_table, start, row0, *, stream=None):
     vs = _row_stride(v, "v", cache.n_kv_heads, cache)
     _check(lib.dspark_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, code, row0_p, n, start_p, table_p,
                                 max_pages, B, raw))
+
+
+# 2 ** 64 turns' parts a radian: 2 ** 64 / (2 pi)
+_PARTS_PER_RADIAN = Fraction(2 ** 64, 2) / Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+class Rotary:
+    """Frequencies of rotary positions (struct dspark_rotary).
+
+    ``inv_freq`` (numbers or a 1-D tensor, taken as they are in 64 bits) is the
+    angle in radians that a step of one position adds to each pair.  Pair i of a
+    head of D elements is elements i and n + i of its first 2 n (n = len(inv_freq),
+    a multiple of 4, 2 n <= D), or with ``adjacent`` 2 i and 2 i + 1; the others pass
+    as they are.  ``axis`` names the axis of positions (0, 1, ..) that turns each
+    pair, for positions of several axes (time, height, width)."""
+
+    def __init__(self, inv_freq, *, axis=None, adjacent=False, device="cuda"):
+        freq = [float(w) for w in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq)]
+        if not all(math.isfinite(w) for w in freq):
+            raise ValueError("inv_freq must be finite")
+        self.n_pairs, self.n_axes, self.adjacent = len(freq), 1, bool(adjacent)
+        if self.n_pairs < 4 or self.n_pairs % 4:
+            raise ValueError("the number of frequencies must be a positive multiple of 4, got %d" % self.n_pairs)
+        steps = [round(Fraction(w) * _PARTS_PER_RADIAN) % 2 ** 64 for w in freq]
+        self.step = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in steps], dtype=torch.int64).to(device)
+        self.axis = None
+        if axis is not None:
+            axis = [int(i) for i in axis]
+            if len(axis) != self.n_pairs or min(axis) < 0 or max(axis) >= 16:
+                raise ValueError("axis must name an axis in [0, 16) for each of the %d pairs" % self.n_pairs)
+            self.n_axes = max(axis) + 1
+            self.axis = torch.tensor(axis, dtype=torch.int32).to(device)
+        self.device = self.step.device
+        self._index = self.step.get_device()
+        self.struct = _RotaryStruct(self.step.data_ptr(), None if self.axis is None else self.axis.data_ptr(), self.n_pairs,
+                                    self.n_axes, int(self.adjacent))
+        self._ref = ctypes.byref(self.struct)
+
+
+def _positions(t, rotary, n):
+    """Address of positions [n_axes, n] int32 (or [n] of one axis)."""
+    if not (t.dtype is torch.int32 and t.get_device() == rotary._index and t.is_contiguous() and t.numel() == rotary.n_axes * n
+            and (t.dim() == 2 and t.shape[0] == rotary.n_axes or t.dim() == 1 and rotary.n_axes == 1)):
+        _need(t, "positions", dtype=torch.int32, shape=(rotary.n_axes, n), device=rotary.device)
+    return t.data_ptr()
+
+
+def rotary(x, rotary, positions, *, inverse=False, out=None, stream=None):
+    """Rows ``x`` [n_rows, heads, head_dim] turned by their ``positions``
+    ([n_axes, n_rows] int32, or [n_rows] of one axis), or turned back with
+    ``inverse``, which is also the turning's gradient.  The rows and the heads of
+    ``x`` may lie apart by strides of 16-byte multiples (slices of a fused
+    projection, or a transposed heads-first tensor); ``out`` may be ``x``.
+    Returns the turned rows, in the layout of ``x`` when that has no gaps.  See
+    dspark_rotary_rows."""
+    lib = _lib or load()
+    raw = _raw_stream(stream, rotary)
+    n, heads, d = x.shape
+    code = _ROW_DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError("rows must be bf16, fp16 or fp32, got %s" % x.dtype)
+    positions_p = _positions(positions, rotary, n)
+    if out is None:
+        with _on(stream):
+            out = torch.empty_like(x)
+    elif out.dtype is not x.dtype or out.shape != x.shape:
+        raise ValueError("out must have the shape and type of x")
+    row, head, elem = x.stride()
+    out_row, out_head, out_elem = out.stride()
+    if x.get_device() != rotary._index or out.get_device() != rotary._index:
+        raise ValueError("x and out must be on %s" % rotary.device)
+    if (elem != 1 or out_elem != 1) and d > 1:
+        raise ValueError("the elements of a head of x and out must be contiguous")
+    if (n | heads | d) >> 31:
+        raise ValueError("numbers of rows and heads must be below 2^31")
+    _check(lib.dspark_rotary_rows(rotary._ref, x.data_ptr(), row, head, n, heads, d, code, positions_p, int(bool(inverse)),
+                                  out.data_ptr(), out_row, out_head, raw))
+    return out
+
+
+def kv_append_rotary(k, v, cache, block_table, start, row0, rotary, *, q=None, positions=None, offset=0, out=None,
+                     stream=None):
+    """:func:`kv_append` with the keys turned by their positions on the way, and
+    the queries ``q`` [n_rows, n_q_heads, head_dim] of the same rows turned beside
+    them, to ``out`` (made here by default; ``q`` itself turns them in place).  Row i
+    of request b is at position ``offset`` + start[b] + i on every axis, or where
+    ``positions`` ([n_axes, n_rows] int32, or [n_rows] of one axis) says.  See
+    dspark_kv_append_rotary.
+
+    Returns the turned queries, None without ``q``; rows of no request stay as
+    they were in ``out``."""
+    lib = _lib or load()
+    raw = _raw_stream(stream, cache)
+    shape, dtype = k.shape, k.dtype
+    n = shape[0]
+    B, max_pages, table_p, start_p, row0_p = _paged(block_table, start, "start", row0, cache, n)
+    code = _ROW_DTYPES.get(dtype)
+    if code is None or v.dtype is not dtype or v.shape != shape:
+        raise TypeError("k and v must have one shape and one of the types bf16, fp16 and fp32")
+    if rotary._index != cache._index:
+        raise ValueError("rotary must be on %s" % cache.device)
+    ks = _row_stride(k, "k", cache.n_kv_heads, cache)
+    vs = _row_stride(v, "v", cache.n_kv_heads, cache)
+    positions_p = None if positions is None else _positions(positions, rotary, n)
+    offset = int(offset)
+    if not -2 ** 62 <= offset <= 2 ** 62:
+        raise ValueError("offset is out of range")
+    q_p = out_p = None
+    qs = outs = heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q.dtype is not dtype or q.shape[0] != n:
+            raise TypeError("q must have the type and the rows of k")
+        qs = _row_stride(q, "q", heads, cache)
+        if out is None:
+            with _on(stream):
+                out = torch.empty(q.shape, dtype=dtype, device=cache.device)
+        elif out.dtype is not dtype or out.shape != q.shape:
+            raise ValueError("out must have the shape and type of q")
+        outs = _row_stride(out, "out", heads, cache)
+        q_p, out_p = q.data_ptr(), out.data_ptr()
+    elif out is not None:
+        raise ValueError("out is for turned queries: q is required")
+    _check(lib.dspark_kv_append_rotary(cache._ref, rotary._ref, q_p, qs, heads, k.data_ptr(), v.data_ptr(), ks, vs, code,
+                                       row0_p, n, start_p, table_p, max_pages, B, positions_p, offset, out_p, outs, raw))
+    return out
 
 
 def kv_read(cache, block_table, start, row0, n_rows, *, dtype=torch.bfloat16, out=None, stream=None):

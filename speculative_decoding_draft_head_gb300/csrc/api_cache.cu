@@ -47,6 +47,28 @@ dspark_status check_rows(const PagedRows &p, const dspark_kv_cache *c) {
     return DSPARK_OK;
 }
 
+dspark_status check_rotary(const dspark_rotary *z, int head_dim) {
+    if (!z) return fail(DSPARK_ERR_INVALID_ARG, "rotary is NULL");
+    if (!z->step || !aligned(z->step, 8) || !aligned(z->axis, 4))
+        return fail(DSPARK_ERR_INVALID_ARG, "rotary's steps are NULL or its arrays not aligned");
+    if (z->n_pairs < 4 || z->n_pairs % 4 != 0 || z->n_pairs > head_dim / 2)
+        return fail(DSPARK_ERR_INVALID_ARG, "n_pairs must be a positive multiple of 4 up to half of head_dim (got %d, %d)",
+                    z->n_pairs, head_dim);
+    if (z->n_axes < 1 || (!z->axis && z->n_axes != 1))
+        return fail(DSPARK_ERR_INVALID_ARG, "bad n_axes %d (1 without axis)", z->n_axes);
+    if (z->adjacent != 0 && z->adjacent != 1) return fail(DSPARK_ERR_INVALID_ARG, "adjacent must be 0 or 1");
+    return DSPARK_OK;
+}
+
+// bytes from the first to behind the last element of strided rows of heads
+int64_t span_bytes(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t width, size_t elem) {
+    return ((rows - 1) * row_stride + (heads - 1) * head_stride + width) * (int64_t)elem;
+}
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 bool bad_stride(int64_t stride, int64_t width, size_t elem) {
     return stride < width || (stride * (int64_t)elem) % 16 != 0;
 }
@@ -145,6 +167,94 @@ dspark_status dspark_block_attention(const dspark_kv_cache *cache, const void *q
                           out, lse, static_cast<unsigned char *>(workspace)};
     const cudaError_t e = launch_block_attention(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    return DSPARK_OK;
+}
+
+dspark_status dspark_rotary_rows(const dspark_rotary *rotary, const void *x, int64_t row_stride, int64_t head_stride,
+                                 int n_rows, int n_heads, int head_dim, dspark_dtype dtype, const int32_t *positions,
+                                 int inverse, void *out, int64_t out_row_stride, int64_t out_head_stride, void *stream) {
+    if (head_dim < 8 || head_dim % 8 != 0)
+        return fail(DSPARK_ERR_INVALID_ARG, "head_dim must be a positive multiple of 8 (got %d)", head_dim);
+    if (head_dim > kMaxRotaryDim)
+        return fail(DSPARK_ERR_UNSUPPORTED, "head_dim must be at most %d (got %d)", kMaxRotaryDim, head_dim);
+    dspark_status st = check_rotary(rotary, head_dim);
+    if (st != DSPARK_OK) return st;
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F32 && dtype != DSPARK_F16)
+        return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (n_rows < 0 || n_heads < 1) return fail(DSPARK_ERR_INVALID_ARG, "bad n_rows %d or n_heads %d", n_rows, n_heads);
+    if (n_heads > kMaxRotaryHeads) return fail(DSPARK_ERR_UNSUPPORTED, "n_heads must be at most %d", kMaxRotaryHeads);
+    if (inverse != 0 && inverse != 1) return fail(DSPARK_ERR_INVALID_ARG, "inverse must be 0 or 1");
+    if (n_rows == 0) return DSPARK_OK;
+    if (!x || !out || !positions) return fail(DSPARK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(positions, 4))
+        return fail(DSPARK_ERR_INVALID_ARG, "x and out must be 16-byte aligned, positions 4-byte");
+    const size_t elem = dtype_bytes(dtype);
+    // (a size of 1 needs no stride; the others must keep rows and heads apart)
+    int64_t *const strides[4] = {&row_stride, &head_stride, &out_row_stride, &out_head_stride};
+    for (int i = 0; i < 4; i += 2) {
+        int64_t &row = *strides[i], &head = *strides[i + 1];
+        if (n_heads == 1) head = head_dim;
+        if (n_rows == 1) row = n_heads * head > 0 ? n_heads * head : 0;
+        const bool heads_inside = head >= head_dim && (n_rows == 1 || row >= (n_heads - 1) * head + head_dim);
+        const bool rows_inside = row >= head_dim && (n_heads == 1 || head >= (n_rows - 1) * row + head_dim);
+        if (!(heads_inside || rows_inside) || (row * (int64_t)elem) % 16 != 0 || (head * (int64_t)elem) % 16 != 0)
+            return fail(DSPARK_ERR_INVALID_ARG,
+                        "strides must keep rows and heads apart, one inside the other, and 16-byte aligned");
+    }
+    const int64_t x_bytes = span_bytes(n_rows, row_stride, n_heads, head_stride, head_dim, elem);
+    const int64_t out_bytes = span_bytes(n_rows, out_row_stride, n_heads, out_head_stride, head_dim, elem);
+    const bool same = x == out && row_stride == out_row_stride && head_stride == out_head_stride;
+    if (!same && overlap(x, x_bytes, out, out_bytes))
+        return fail(DSPARK_ERR_INVALID_ARG, "out must be x with the same strides or not overlap it");
+    const RotaryRowsArgs a{*rotary, x, row_stride, head_stride, n_rows, n_heads, head_dim, dtype, positions, inverse != 0,
+                           out, out_row_stride, out_head_stride};
+    const cudaError_t e = launch_rotary_rows(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+    return DSPARK_OK;
+}
+
+dspark_status dspark_kv_append_rotary(const dspark_kv_cache *cache, const dspark_rotary *rotary, const void *q,
+                                      int64_t q_stride, int n_q_heads, const void *k, const void *v, int64_t k_stride,
+                                      int64_t v_stride, dspark_dtype dtype, const int64_t *row0, int n_rows,
+                                      const int32_t *start, const int32_t *block_table, int max_pages, int B,
+                                      const int32_t *positions, int64_t offset, void *q_out, int64_t q_out_stride,
+                                      void *stream) {
+    dspark_status st = check_cache(cache);
+    if (st != DSPARK_OK) return st;
+    const PagedRows p{row0, start, block_table, max_pages, B, n_rows};
+    if ((st = check_rows(p, cache)) != DSPARK_OK) return st;
+    if ((st = check_rotary(rotary, cache->head_dim)) != DSPARK_OK) return st;
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F32 && dtype != DSPARK_F16)
+        return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (positions && offset != 0) return fail(DSPARK_ERR_INVALID_ARG, "offset must be 0 when positions are given");
+    if (!aligned(positions, 4)) return fail(DSPARK_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    if (cache->n_kv_heads > kMaxRotaryHeads || (q && n_q_heads > kMaxRotaryHeads))
+        return fail(DSPARK_ERR_UNSUPPORTED, "at most %d heads", kMaxRotaryHeads);
+    if (n_rows == 0) return DSPARK_OK;
+    if (!k || !v) return fail(DSPARK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(DSPARK_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    const size_t elem = dtype_bytes(dtype);
+    const int64_t D = cache->head_dim, width = cache->n_kv_heads * D, q_width = n_q_heads * D;
+    if (bad_stride(k_stride, width, elem) || bad_stride(v_stride, width, elem))
+        return fail(DSPARK_ERR_INVALID_ARG, "row strides must cover a row and keep rows 16-byte aligned");
+    if (q) {
+        if (n_q_heads < 1) return fail(DSPARK_ERR_INVALID_ARG, "n_q_heads must be >= 1 (got %d)", n_q_heads);
+        if (!q_out) return fail(DSPARK_ERR_INVALID_ARG, "q_out is NULL");
+        if (!aligned(q, 16) || !aligned(q_out, 16))
+            return fail(DSPARK_ERR_INVALID_ARG, "q and q_out must be 16-byte aligned");
+        if (bad_stride(q_stride, q_width, elem) || bad_stride(q_out_stride, q_width, elem))
+            return fail(DSPARK_ERR_INVALID_ARG, "row strides must cover a row and keep rows 16-byte aligned");
+        const int64_t out_bytes = span_bytes(n_rows, q_out_stride, 1, 0, q_width, elem);
+        const bool same = q == q_out && q_stride == q_out_stride;
+        if (!same && (overlap(q, span_bytes(n_rows, q_stride, 1, 0, q_width, elem), q_out, out_bytes) ||
+                      overlap(k, span_bytes(n_rows, k_stride, 1, 0, width, elem), q_out, out_bytes) ||
+                      overlap(v, span_bytes(n_rows, v_stride, 1, 0, width, elem), q_out, out_bytes)))
+            return fail(DSPARK_ERR_INVALID_ARG, "q_out must be q with its stride or overlap none of q, k and v");
+    }
+    const AppendRotaryArgs a{*cache, p, *rotary, q, q_stride, n_q_heads, k, v, k_stride, v_stride, dtype,
+                             positions, offset, q_out, q_out_stride};
+    const cudaError_t e = launch_kv_append_rotary(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "append launch");
     return DSPARK_OK;
 }
 

@@ -255,6 +255,39 @@ struct AttentionArgs {
 size_t attention_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s);
 
+// ------------------------------------------------------- rotary positions --
+constexpr int kMaxRotaryDim = 256;
+constexpr int kMaxRotaryHeads = 1 << 16;
+struct RotaryRowsArgs {
+    dspark_rotary z;
+    const void *x;
+    int64_t row_stride, head_stride;
+    int n_rows, n_heads, head_dim;
+    dspark_dtype dt;
+    const int32_t *positions;    // [n_axes][n_rows]
+    bool inverse;
+    void *out;
+    int64_t out_row_stride, out_head_stride;
+};
+cudaError_t launch_rotary_rows(const RotaryRowsArgs &a, cudaStream_t s);
+
+struct AppendRotaryArgs {
+    dspark_kv_cache cache;
+    PagedRows rows;
+    dspark_rotary z;
+    const void *q;               // nullptr: no queries
+    int64_t q_stride;
+    int n_q_heads;
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    dspark_dtype dt;
+    const int32_t *positions;    // [n_axes][n_rows], or nullptr: offset + the row's place in its request
+    int64_t offset;
+    void *q_out;
+    int64_t q_out_stride;
+};
+cudaError_t launch_kv_append_rotary(const AppendRotaryArgs &a, cudaStream_t s);
+
 // Launch `kernel` as a programmatic dependent of the stream's previous kernel:
 // its blocks may be scheduled while that kernel drains, and every kernel
 // launched this way starts with griddepcontrol.wait (griddep_wait), which

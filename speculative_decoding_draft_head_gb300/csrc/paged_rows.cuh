@@ -108,4 +108,18 @@ __device__ __forceinline__ uint32_t float_to_pair<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// The largest of top[j] over a head row's lanes, for the head row j = sub % 4:
+// the first two exchanges halve what a lane holds, the others join the rest.
+template <int kLanes>
+__device__ __forceinline__ uint32_t top_of_row(const uint32_t (&top)[4], int sub) {
+    const bool b0 = sub & 1, b1 = sub & 2;
+    uint32_t lo = b0 ? top[1] : top[0], hi = b0 ? top[3] : top[2];
+    lo = max(lo, __shfl_xor_sync(0xffffffffu, b0 ? top[0] : top[1], 1));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, b0 ? top[2] : top[3], 1));
+    uint32_t t = max(b1 ? hi : lo, __shfl_xor_sync(0xffffffffu, b1 ? lo : hi, 2));
+#pragma unroll
+    for (int d = 4; d < kLanes; d *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
+    return t;
+}
+
 }  // namespace dspark
