@@ -570,6 +570,37 @@ DSPARK_API dspark_status dspark_block_attention(
     const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
     void *stream);
 
+/* Bytes of workspace of dspark_window_attention; 0 when it needs none (then it
+ * may be NULL) or for invalid sizes. */
+DSPARK_API size_t dspark_window_workspace_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
+
+/*
+ * dspark_block_attention through a window: a row sees the last `window` tokens
+ * up to its own and, however far back, the first `sinks` ones.
+ *
+ * Tokens are counted through the prefix and the request's own: token t of the
+ * prefix is at t, own token t at prefix_len + t.  Row i of request b, at
+ * p = prefix_len + kv_len[b] - n_b + i, sees of the tokens that
+ * dspark_block_attention shows it those at positions t > p - window and those at
+ * t < sinks.  With row_mask a row stands behind the tokens of its word (a node of a
+ * drafted tree behind its ancestors): with c of its bits set (bits from n_b on do
+ * not count) it sees those tokens, of the tokens before the block the last
+ * max(0, window - c), and those at t < sinks; window must be at least 64 then.
+ * Pages of tokens before the block that no row's window or first tokens reach are
+ * never read: their entries in the tables need not be pages, and a page may be given
+ * away as soon as the window has passed it.
+ *
+ * Everything else, scales, results, roundings, flags and limits, as
+ * dspark_block_attention; window >= 1, sinks >= 0, and prefix_len +
+ * max_pages * page_size below 2^31.
+ */
+DSPARK_API dspark_status dspark_window_attention(
+    const dspark_kv_cache *cache, const void *q, int64_t q_stride, dspark_dtype dtype, int n_q_heads,
+    const int64_t *row0, int n_rows, int B, const int32_t *block_table, int max_pages, const int32_t *kv_len,
+    const int32_t *prefix_pages, int n_prefix_pages, int prefix_len, int window, int sinks, dspark_block_mask mask,
+    const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream);
+
 /*
  * Self-test of the bounded device-side waits (the library's failure
  * detection): one block waits, with the helpers every kernel uses and a limit

@@ -5,7 +5,9 @@ this package holds the build step, the ctypes binding and the seeded workload
 generators.
 """
 from .binding import (DSparkError, KVCache, Rotary, block_attention, draft_sample, kv_append, kv_append_rotary, kv_read,
-                      load, read_device_flags, rotary, schedule_prefix, verify, version, workspace_bytes)
+                      load, read_device_flags, rotary, schedule_prefix, verify, version, window_attention,
+                      workspace_bytes)
 
 __all__ = ["DSparkError", "KVCache", "Rotary", "block_attention", "draft_sample", "kv_append", "kv_append_rotary", "kv_read",
-           "load", "read_device_flags", "rotary", "schedule_prefix", "verify", "version", "workspace_bytes"]
+           "load", "read_device_flags", "rotary", "schedule_prefix", "verify", "version", "window_attention",
+           "workspace_bytes"]

@@ -43,7 +43,7 @@ EXPORTS = ("dspark_version", "dspark_last_error", "dspark_workspace_bytes", "dsp
            "dspark_verify_noalloc", "dspark_draft_sample_rnn", "dspark_verify_packed", "dspark_pack_target",
            "dspark_selftest_bounded_wait", "dspark_read_noalloc_flags", "dspark_selftest_philox_rate",
            "dspark_kv_append", "dspark_kv_read", "dspark_attention_workspace_bytes", "dspark_block_attention",
-           "dspark_rotary_rows", "dspark_kv_append_rotary")
+           "dspark_rotary_rows", "dspark_kv_append_rotary", "dspark_window_workspace_bytes", "dspark_window_attention")
 
 _lib = None
 _lock = threading.Lock()
@@ -128,6 +128,11 @@ def load(build_if_missing: bool = True):
         L.dspark_block_attention.restype = ctypes.c_int
         L.dspark_block_attention.argtypes = [cache_p, vp, i64, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32, i32,
                                              i32, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.dspark_window_workspace_bytes.restype = sz
+        L.dspark_window_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.dspark_window_attention.restype = ctypes.c_int
+        L.dspark_window_attention.argtypes = [cache_p, vp, i64, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32, i32, i32, i32,
+                                              i32, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         rotary_p = ctypes.POINTER(_RotaryStruct)
         L.dspark_rotary_rows.restype = ctypes.c_int
         L.dspark_rotary_rows.argtypes = [rotary_p, vp, i64, i64, i32, i32, i32, i32, vp, i32, vp, i64, i64, vp]
@@ -734,6 +739,32 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     (attention_workspace_bytes, 256-byte aligned) one is kept per stream.  See dspark_block_attention.
 
     Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
+    return _attention(None, q, cache, block_table, kv_len, row0, prefix_pages, prefix_len, mask, row_mask, scale, out,
+                      workspace, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def window_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) -> int:
+    return int(load().dspark_window_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim))
+
+
+def window_attention(q, cache, block_table, kv_len, row0, *, window, sinks=0, prefix_pages=None, prefix_len=0,
+                     mask="causal", row_mask=None, scale=None, out=None, workspace=None, stream=None):
+    """:func:`block_attention` through a window: a row sees the last ``window``
+    tokens up to its own and the first ``sinks`` ones (of the prefix, then of the
+    request's own), as far as ``mask`` or ``row_mask`` shows them to it; a row with a
+    mask word stands behind the word's tokens (``window`` is at least 64 then).
+    Pages before the block that neither reaches are not read.  See
+    dspark_window_attention.
+
+    Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
+    return _attention((int(window), int(sinks)), q, cache, block_table, kv_len, row0, prefix_pages, prefix_len, mask,
+                      row_mask, scale, out, workspace, stream)
+
+
+def _attention(window, q, cache, block_table, kv_len, row0, prefix_pages, prefix_len, mask, row_mask, scale, out, workspace,
+               stream):
+    """block_attention, or with (window, sinks) window_attention"""
     lib = _lib or load()
     dev = cache.device
     raw = _raw_stream(stream, cache)
@@ -746,6 +777,9 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
     qs = _row_stride(q, "q", Hq, cache)
     pages_p = None if prefix_pages is None else _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
     words_p = None if row_mask is None else _vec(row_mask, "row_mask", torch.int64, n, cache)
+    if window is not None:
+        # (more than any cache holds is all of it)
+        window = tuple(max(-1, min(x, 0x7fffffff)) for x in window)
     if out is None:
         with _on(stream):
             out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
@@ -757,17 +791,23 @@ def block_attention(q, cache, block_table, kv_len, row0, *, prefix_pages=None, p
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
             lse_p = out["lse"].data_ptr()
+    need = 1
+    if workspace is None:
+        need = (attention_workspace_bytes if window is None else window_workspace_bytes)(B, n, Hq, cache.n_kv_heads, D)
     # (two launches that meet in the workspace: another thread's must not come in between)
-    with _default_ws.lock if workspace is None else _AS_IT_IS:
-        if workspace is None:
-            ws_p, ws_n, workspace = _default_ws.attention(attention_workspace_bytes(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
-        else:
+    with _default_ws.lock if workspace is None and (need or window is None) else _AS_IT_IS:
+        if workspace is not None:
             _need(workspace, "workspace", device=dev)
             ws_p, ws_n = workspace.data_ptr(), workspace.numel()
-        status = lib.dspark_block_attention(
-            cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
-            prefix_len, _MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(),
-            lse_p, ws_p, ws_n, raw)
+        elif need or window is None:
+            ws_p, ws_n, workspace = _default_ws.attention(need, dev, stream, raw)
+        else:
+            ws_p, ws_n = None, 0
+        head = (cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p,
+                n_pages, prefix_len)
+        tail = (_MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(), lse_p, ws_p, ws_n,
+                raw)
+        status = lib.dspark_block_attention(*head, *tail) if window is None else lib.dspark_window_attention(*head, *window, *tail)
     _check(status)
     return out
 

@@ -73,6 +73,54 @@ bool bad_stride(int64_t stride, int64_t width, size_t elem) {
     return stride < width || (stride * (int64_t)elem) % 16 != 0;
 }
 
+// The checks of an attention call, and its arguments; *nothing: there are no rows.
+dspark_status check_attention(AttentionArgs &a, const dspark_kv_cache *cache, const void *q, int64_t q_stride,
+                              dspark_dtype dtype, int n_q_heads, const int64_t *row0, int n_rows, int B,
+                              const int32_t *block_table, int max_pages, const int32_t *kv_len,
+                              const int32_t *prefix_pages, int n_prefix_pages, int prefix_len, dspark_block_mask mask,
+                              const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, size_t (*need_bytes)(int, int, int, int, int), bool *nothing) {
+    *nothing = false;
+    dspark_status st = check_cache(cache);
+    if (st != DSPARK_OK) return st;
+    const PagedRows p{row0, kv_len, block_table, max_pages, B, n_rows};
+    if ((st = check_rows(p, cache)) != DSPARK_OK) return st;
+    if (dtype == DSPARK_F32) return fail(DSPARK_ERR_UNSUPPORTED, "q must be bf16 or fp16");
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0)
+        return fail(DSPARK_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads (got %d, %d)", n_q_heads,
+                    cache->n_kv_heads);
+    if ((int64_t)n_rows * n_q_heads > 0x7fffffff / 2)
+        return fail(DSPARK_ERR_UNSUPPORTED, "n_rows * n_q_heads must be below 2^30");
+    if (prefix_len < 0 || n_prefix_pages < 0 || (int64_t)n_prefix_pages * cache->page_size < prefix_len)
+        return fail(DSPARK_ERR_INVALID_ARG, "prefix_len %d does not fit %d pages", prefix_len, n_prefix_pages);
+    if (prefix_len > 0 && !prefix_pages) return fail(DSPARK_ERR_INVALID_ARG, "prefix_pages is NULL");
+    if (mask != DSPARK_MASK_CAUSAL && mask != DSPARK_MASK_FULL)
+        return fail(DSPARK_ERR_INVALID_ARG, "unknown mask %d", (int)mask);
+    if (!std::isfinite(scale) || scale <= 0.f) return fail(DSPARK_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (n_rows == 0) {
+        *nothing = true;
+        return DSPARK_OK;
+    }
+    if (!q || !out) return fail(DSPARK_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(q, 16) || !aligned(out, 16)) return fail(DSPARK_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    if (bad_stride(q_stride, (int64_t)n_q_heads * cache->head_dim, 2))
+        return fail(DSPARK_ERR_INVALID_ARG, "q_stride must cover a row and keep rows 16-byte aligned");
+    const size_t need = need_bytes(B, n_rows, n_q_heads, cache->n_kv_heads, cache->head_dim);
+    if (need && !workspace) return fail(DSPARK_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(DSPARK_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(DSPARK_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    // (the bytes from the first to the last row of q)
+    const int64_t q_bytes = ((n_rows - 1) * q_stride + (int64_t)n_q_heads * cache->head_dim) * 2;
+    const int64_t out_bytes = (int64_t)n_rows * n_q_heads * cache->head_dim * 2;
+    const char *qb = static_cast<const char *>(q), *ob = static_cast<const char *>(out);
+    if (ob < qb + q_bytes && qb < ob + out_bytes) return fail(DSPARK_ERR_INVALID_ARG, "out must not overlap q");
+    a = AttentionArgs{*cache, p, q, q_stride, dtype, n_q_heads, prefix_pages, prefix_len, (int)mask, row_mask, scale,
+                      out, lse, static_cast<unsigned char *>(workspace)};
+    return DSPARK_OK;
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -131,42 +179,44 @@ dspark_status dspark_block_attention(const dspark_kv_cache *cache, const void *q
                                      int n_prefix_pages, int prefix_len, dspark_block_mask mask,
                                      const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace,
                                      size_t workspace_bytes, void *stream) {
-    dspark_status st = check_cache(cache);
-    if (st != DSPARK_OK) return st;
-    const PagedRows p{row0, kv_len, block_table, max_pages, B, n_rows};
-    if ((st = check_rows(p, cache)) != DSPARK_OK) return st;
-    if (dtype == DSPARK_F32) return fail(DSPARK_ERR_UNSUPPORTED, "q must be bf16 or fp16");
-    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
-    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0)
-        return fail(DSPARK_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads (got %d, %d)", n_q_heads,
-                    cache->n_kv_heads);
-    if ((int64_t)n_rows * n_q_heads > 0x7fffffff / 2)
-        return fail(DSPARK_ERR_UNSUPPORTED, "n_rows * n_q_heads must be below 2^30");
-    if (prefix_len < 0 || n_prefix_pages < 0 || (int64_t)n_prefix_pages * cache->page_size < prefix_len)
-        return fail(DSPARK_ERR_INVALID_ARG, "prefix_len %d does not fit %d pages", prefix_len, n_prefix_pages);
-    if (prefix_len > 0 && !prefix_pages) return fail(DSPARK_ERR_INVALID_ARG, "prefix_pages is NULL");
-    if (mask != DSPARK_MASK_CAUSAL && mask != DSPARK_MASK_FULL)
-        return fail(DSPARK_ERR_INVALID_ARG, "unknown mask %d", (int)mask);
-    if (!std::isfinite(scale) || scale <= 0.f) return fail(DSPARK_ERR_INVALID_ARG, "scale must be finite and > 0");
-    if (n_rows == 0) return DSPARK_OK;
-    if (!q || !out) return fail(DSPARK_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (!aligned(q, 16) || !aligned(out, 16)) return fail(DSPARK_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-    if (bad_stride(q_stride, (int64_t)n_q_heads * cache->head_dim, 2))
-        return fail(DSPARK_ERR_INVALID_ARG, "q_stride must cover a row and keep rows 16-byte aligned");
-    const size_t need = attention_ws_bytes(B, n_rows, n_q_heads, cache->n_kv_heads, cache->head_dim);
-    if (!workspace) return fail(DSPARK_ERR_INVALID_ARG, "workspace is NULL");
-    if (!aligned(workspace, 256)) return fail(DSPARK_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    if (workspace_bytes < need)
-        return fail(DSPARK_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
-    // (the bytes from the first to the last row of q)
-    const int64_t q_bytes = ((n_rows - 1) * q_stride + (int64_t)n_q_heads * cache->head_dim) * 2;
-    const int64_t out_bytes = (int64_t)n_rows * n_q_heads * cache->head_dim * 2;
-    const char *qb = static_cast<const char *>(q), *ob = static_cast<const char *>(out);
-    if (ob < qb + q_bytes && qb < ob + out_bytes) return fail(DSPARK_ERR_INVALID_ARG, "out must not overlap q");
-    const AttentionArgs a{*cache, p, q, q_stride, dtype, n_q_heads, prefix_pages, prefix_len, (int)mask, row_mask, scale,
-                          out, lse, static_cast<unsigned char *>(workspace)};
+    AttentionArgs a{};
+    bool nothing;
+    const dspark_status st = check_attention(a, cache, q, q_stride, dtype, n_q_heads, row0, n_rows, B, block_table, max_pages,
+                                             kv_len, prefix_pages, n_prefix_pages, prefix_len, mask, row_mask, scale, out,
+                                             lse, workspace, workspace_bytes, attention_ws_bytes, &nothing);
+    if (st != DSPARK_OK || nothing) return st;
     const cudaError_t e = launch_block_attention(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    return DSPARK_OK;
+}
+
+size_t dspark_window_workspace_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim) {
+    return dspark_attention_workspace_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) == 0
+               ? 0
+               : window_ws_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim);
+}
+
+dspark_status dspark_window_attention(const dspark_kv_cache *cache, const void *q, int64_t q_stride, dspark_dtype dtype,
+                                      int n_q_heads, const int64_t *row0, int n_rows, int B, const int32_t *block_table,
+                                      int max_pages, const int32_t *kv_len, const int32_t *prefix_pages,
+                                      int n_prefix_pages, int prefix_len, int window, int sinks, dspark_block_mask mask,
+                                      const uint64_t *row_mask, float scale, void *out, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream) {
+    AttentionArgs a{};
+    bool nothing;
+    const dspark_status st = check_attention(a, cache, q, q_stride, dtype, n_q_heads, row0, n_rows, B, block_table, max_pages,
+                                             kv_len, prefix_pages, n_prefix_pages, prefix_len, mask, row_mask, scale, out,
+                                             lse, workspace, workspace_bytes, window_ws_bytes, &nothing);
+    if (st != DSPARK_OK) return st;
+    if (window < 1 || sinks < 0)
+        return fail(DSPARK_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0 (got %d, %d)", window, sinks);
+    if (row_mask && window < 64)
+        return fail(DSPARK_ERR_INVALID_ARG, "window must be at least 64 with row_mask (got %d)", window);
+    if ((int64_t)max_pages * cache->page_size + prefix_len > 0x7fffffff)
+        return fail(DSPARK_ERR_INVALID_ARG, "prefix_len + max_pages * page_size passes 2^31 - 1 tokens");
+    if (nothing) return DSPARK_OK;
+    const cudaError_t e = launch_window_attention(a, window, sinks, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "window attention launch");
     return DSPARK_OK;
 }
 

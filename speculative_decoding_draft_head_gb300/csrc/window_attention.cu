@@ -1,0 +1,606 @@
+// Attention of each request's block rows through a window: the last tokens
+// before each row, and a few first ones that stay visible, of a shared prefix
+// and the request's own tokens in the quantised cache.
+//
+// Mathematics.  As in block_attention.cu: row m (a block row of a query head)
+// against tokens j, with 8-bit codes k~, v~ and scales ks, vs, has scores
+// s_j = c ks_j (q . k~_j) in log2 units, and with any reference r
+//   O = sum_j 2^(s_j - r) v_j,   l = sum_j 2^(s_j - r),   out = O / l,
+//   lse = ln 2 (r + log2 l).
+// q after a power of two per row and the codes are exact in fp16, scales and
+// all sums are fp32, and P = 2^(s_j - r) (2^12 vs_j) is rounded once to fp16 (2^-11).
+// The reference is an integer that moves only when a P passes fp16's range.
+//
+// A row sees at most window + sinks tokens, so that an item (a request's kv head
+// and up to 8 N rows of it) is short, and what bounds a call is reading the codes.
+// The products therefore put tokens on their long side: a warp takes 16 tokens
+// at a time, S^T = K Q^T and O^T = V^T P^T as 16 x 8 x 16 products whose first
+// operand is the codes, converted in registers once for all the item's rows, and
+// whose second one is N blocks of 8 rows.  (128-row tensor-core tiles would be
+// filled to a sixteenth by 8 rows, and need the codes in shared memory as fp16.)
+// Each warp walks its own tokens: every 4th chunk of 16 of the item, and of a
+// cluster's share; copies by cp.async into a ring of its own, no barrier in the
+// loop.  At the end the warps' parts meet in shared memory, and a cluster's
+// through its distributed shared memory: one launch, no workspace.
+//
+// Layouts.  Lane (g, t) = (lane / 4, lane % 4).
+//   S^T: the lane holds tokens g and g + 8 against rows 2 t and 2 t + 1.  Its part of the
+//     keys is 16 codes of either token at a time, dimensions 16 t .. 16 t + 15 of each
+//     64; the order of dimensions inside the sum is free, and q is laid out alike.
+//   P^T goes from S^T's layout to a second operand's by a transposing move of 8 x 8 fp16.
+//   O^T: the lane's part of the values is dimensions g DP/8 .. of tokens 2 t, 2 t + 1,
+//     2 t + 8 and 2 t + 9; codes of two tokens are interleaved by byte permutations
+//     before they are converted, so that it ends up with DP/8 consecutive dimensions
+//     of rows 2 t and 2 t + 1.
+// In shared memory 16-byte pieces of a chunk are permuted so that neither read
+// meets itself in a bank.
+#include <cooperative_groups.h>
+
+#include "attention_common.cuh"
+#include "tc_primitives.cuh"
+
+namespace dspark {
+namespace {
+
+namespace cg = cooperative_groups;
+using namespace tc;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kChunk = 16;          // tokens of a warp's step
+constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
+constexpr int kMaxCluster = 8;
+
+struct WindowArgs {
+    AttentionArgs a;
+    int window, sinks;
+    int slots;          // row blocks of a request that have blocks of their own; more follow in a loop
+    int cluster;        // blocks an item's tokens are split over
+};
+
+// N blocks of 8 rows a warp: blocks of 4 warps that an SM holds, and chunks of a warp under way
+template <int N>
+struct Shape {
+    static constexpr int kBlocks = N == 1 ? 4 : N == 2 ? 3 : 2;
+    static constexpr int kStages = N == 1 ? 3 : 4;
+};
+template <int DP>
+struct Slot {
+    static constexpr uint32_t kV = kChunk * DP, kScales = 2 * kChunk * DP, kBytes = kScales + 128;
+};
+template <int N, int DP>
+constexpr size_t smem_bytes() {
+    const size_t ring = (size_t)kWarps * Shape<N>::kStages * Slot<DP>::kBytes;
+    const size_t join = (size_t)(kWarps + 1) * 8 * N * (DP + 4) * 4;
+    return ring > join ? ring : join;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+// d += a b of 16 x 16 by 16 x 8 fp16
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float lds32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+
+// Where 16-byte piece `c` of token `tok` is in a chunk.  DP = 128: a token a line of 128
+// bytes; DP = 64: two.  The permutations keep apart, by banks, pieces t of tokens
+// 2 p and 2 p + 1 (keys) and pieces of tokens 2 t (or 2 t + 1) that 8 lanes read at once (values).
+template <int DP>
+__device__ __forceinline__ uint32_t piece_at(uint32_t tok, uint32_t c) {
+    if constexpr (DP == 128) return tok * 128u + ((c ^ (tok & 6u) ^ ((tok & 1u) << 2)) << 4);
+    return (tok >> 1) * 128u + ((((tok & 1u) << 2 | c) ^ (tok & 6u)) << 4);
+}
+
+// The chunks of 16 tokens that an item's rows can see: of the prefix the first
+// ones and the window's, of the request's own tokens the same.
+struct Chunks {
+    int n0, n1, n2, total;            // chunks of the prefix's first tokens, and of its window's, of the own first tokens
+    int first1, first3;               // where the windows' begin
+    __device__ __forceinline__ void find(int prefix, int sinks, int low, int end) {
+        auto up = [](int x) { return (int)(((unsigned)x + kChunk - 1) / kChunk); };
+        const int s = min(sinks, end);
+        n0 = up(min(s, prefix));
+        first1 = max(n0, low / kChunk);
+        n1 = low < prefix ? max(0, up(min(end, prefix)) - first1) : 0;
+        n2 = up(max(s - prefix, 0));
+        first3 = max(n2, max(low - prefix, 0) / kChunk);
+        total = n0 + n1 + n2 + max(0, up(max(end - prefix, 0)) - first3);
+    }
+    // chunk i: its number in its list; whether that is the own tokens'
+    __device__ __forceinline__ int at(int i, bool &own) const {
+        own = i >= n0 + n1;
+        if (!own) return i < n0 ? i : first1 + i - n0;
+        i -= n0 + n1;
+        return i < n2 ? i : first3 + i - n2;
+    }
+};
+
+// What one row sees: tokens in [low, end), and those before `sinks` (if before `end`);
+// with a mask word the block's tokens by their bits.
+struct RowRange {
+    int low, end;
+};
+
+template <typename T, int kFormat, int DP, int N>
+__global__ void __launch_bounds__(kThreads, Shape<N>::kBlocks)
+window_kernel(const __grid_constant__ WindowArgs w) {
+    using Sl = Slot<DP>;
+    constexpr int kStages = Shape<N>::kStages, kRows = 8 * N, kSteps = DP / 16, kHalves = DP / 64;
+    constexpr int kCols = DP / 8;                 // dimensions of a lane's rows
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ RowRange ranges[kRows];
+    __shared__ uint64_t words[kRows];
+    __shared__ float2 stats[kWarps + 1][kRows];   // (r, l) of the warps, and of the block
+
+    const AttentionArgs &a = w.a;
+    const dspark_kv_cache &c = a.cache;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int D = c.head_dim, Hq = a.n_q_heads, H = c.n_kv_heads, group = Hq / H;
+    const int split = blockIdx.x % w.cluster;
+    int item = blockIdx.x / w.cluster;
+    const int slot = item % w.slots;
+    item /= w.slots;
+    const int head = item % H, b = item / H;
+    const Request q = load_request(a, b);
+    if (slot == 0 && head == 0 && split == 0 && threadIdx.x == 0 && (!q.rows_ok || (q.n > 0 && !q.len_ok)))
+        atomicOr(c.flags, kFlagBadLength);
+    const int m_all = q.n * group;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages) * Sl::kBytes;
+    if (D != DP) {      // columns that no copy fills
+        for (uint32_t i = threadIdx.x; i < kWarps * kStages * Sl::kBytes / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+
+    for (int m0 = slot * kRows; m0 < m_all; m0 += w.slots * kRows) {
+        const int rows = min(kRows, m_all - m0);
+        if (!q.len_ok) {
+            if (split == 0)
+                for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
+                    const int r = i / (D / 8), m = m0 + r, blk = m / group;
+                    const int64_t place = (q.first + blk) * Hq + head * group + (m - blk * group);
+                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + place * D)[i - r * (D / 8)] =
+                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    if (i == r * (D / 8) && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+                }
+            continue;
+        }
+        // ---- what the rows see
+        const int ctx = a.prefix_len + q.len - q.n;       // tokens before the block
+        const int b0 = m0 / group, b1 = (m0 + rows - 1) / group;
+        const bool tree = a.row_mask != nullptr, causal = !tree && a.mask == DSPARK_MASK_CAUSAL;
+        int low_min = max(ctx + b0 - w.window + 1, 0), low_max = max(ctx + b1 - w.window + 1, 0);
+        const int end_min = causal ? ctx + b0 + 1 : tree ? ctx : ctx + q.n;
+        const int end_max = causal ? ctx + b1 + 1 : ctx + q.n;
+        __syncthreads();
+        if (threadIdx.x < kRows) {
+            const int m = m0 + min((int)threadIdx.x, rows - 1), blk = m / group;
+            RowRange r{max(ctx + blk - w.window + 1, 0), causal ? ctx + blk + 1 : ctx + q.n};
+            uint64_t word = 0;
+            if (tree) {
+                word = a.row_mask[q.first + blk];
+                if (q.n < 64) word &= (1ull << q.n) - 1;
+                r.low = max(ctx - max(w.window - __popcll(word), 0), 0);
+            }
+            ranges[threadIdx.x] = r;
+            words[threadIdx.x] = word;
+        }
+        __syncthreads();
+        if (tree) {
+            low_min = low_max = ranges[0].low;
+            for (int i = 1; i < kRows; ++i) low_min = min(low_min, ranges[i].low), low_max = max(low_max, ranges[i].low);
+        }
+        Chunks chunks;
+        chunks.find(a.prefix_len, w.sinks, low_min, end_max);
+
+        // ---- the warp's chunks
+        const int parts = w.cluster * kWarps, part = split * kWarps + warp;
+        const int mine = chunks.total > part ? (chunks.total - part + parts - 1) / parts : 0;
+        const int per_page = c.page_size / kChunk;
+        auto place_of = [&](int i) {          // the warp's chunk i: its number in the cache, in 16 head rows
+            if (i >= mine) return kNoChunk;
+            bool own;
+            const int chunk = chunks.at(part + i * parts, own), page_slot = chunk / per_page;
+            const int page = own ? a.rows.block_table[(int64_t)b * a.rows.max_pages + page_slot] : a.prefix_pages[page_slot];
+            if (page < 0 || page >= c.n_pages) return kBadChunk;
+            return ((uint32_t)page * (uint32_t)H + (uint32_t)head) * (uint32_t)per_page + (uint32_t)(chunk - page_slot * per_page);
+        };
+        uint32_t places = place_of(lane), places_next = kNoChunk;
+        uint32_t bad = 0;                     // of the ring's slots
+        // the tokens of a chunk that some row may see: [from, to)
+        auto bounds = [&](int i, int &pos0, int &from, int &to) {
+            bool own;
+            const int chunk = chunks.at(part + i * parts, own);
+            pos0 = chunk * kChunk + (own ? a.prefix_len : 0);
+            to = min(own ? end_max : min(a.prefix_len, end_max), pos0 + kChunk) - pos0;
+            from = pos0 < w.sinks ? 0 : max(low_min - pos0, 0);
+        };
+        auto load = [&](int i) {
+            if (i < mine) {
+                if ((i & 31) == 0) {
+                    if (i) places = places_next;
+                    places_next = place_of(i + 32 + lane);
+                }
+                const uint32_t place = __shfl_sync(0xffffffffu, places, i & 31), s = (uint32_t)i % kStages;
+                const uint32_t dst = ring + s * Sl::kBytes;
+                const bool good = place < kBadChunk;
+                bad = good ? bad & ~(1u << s) : bad | 1u << s;
+                if (!good && lane == 0) atomicOr(c.flags, kFlagBadPage);
+                int pos0, from, to;
+                bounds(i, pos0, from, to);
+                const uint64_t row = good ? (uint64_t)place * kChunk : 0;
+                constexpr int kPieces = DP / 16, kPer = 32 / kPieces;       // pieces of a token; tokens at once
+                const int col = lane % kPieces;
+                const unsigned char *k = static_cast<const unsigned char *>(c.k) + row * (uint32_t)D;
+                const unsigned char *v = static_cast<const unsigned char *>(c.v) + row * (uint32_t)D;
+#pragma unroll
+                for (int j = 0; j < kChunk / kPer; ++j) {
+                    const int tok = lane / kPieces + j * kPer;
+                    const bool there = good && tok >= from && tok < to;
+                    if (D == DP || col * 16 < D) {
+                        cp_async16(dst + piece_at<DP>((uint32_t)tok, (uint32_t)col), k + tok * D + col * 16, there);
+                        cp_async16(dst + Sl::kV + piece_at<DP>((uint32_t)tok, (uint32_t)col), v + tok * D + col * 16, there);
+                    }
+                }
+                if (lane < 8)
+                    cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, (lane < 4 ? c.k_scale : c.v_scale) + row + (lane & 3) * 4, good);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i);
+
+        // ---- the queries: block n's row g, dimensions 64 h + 16 t + 0 .. 15, in fp16 after a power of two
+        uint32_t qf[N][kSteps][2];
+        float lack[N][2];                     // what rows 2 t and 2 t + 1 of block n lack
+        const float up = a.scale * kLog2e;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int r = 8 * n + g, m = m0 + r, blk = m / group;
+            const T *src = static_cast<const T *>(a.q) + (q.first + blk) * a.q_stride + (int64_t)(head * group + (m - blk * group)) * D;
+            uint4 in[2 * kHalves];
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const int d = 64 * (i >> 1) + 16 * t + 8 * (i & 1);
+                in[i] = r < rows && d < D ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = pair_to_float<T>(u[e]);
+                    top = max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+                }
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e2 = max((int)(top >> 23) - 127, -110);
+            float mul = 1.f, f = 1.f;         // the largest element goes to [2^7, 2^8)
+            if (top >= 0x7f800000u) mul = __int_as_float(0x7fffffff);
+            else if (top != 0) {
+                mul = __uint_as_float((uint32_t)(127 + 7 - e2) << 23);
+                f = __uint_as_float((uint32_t)(127 - 7 + e2) << 23);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = pair_to_float<T>(u[e]);
+                    qf[n][2 * i + (e >> 1)][e & 1] = half_pair(x.x * mul, x.y * mul);
+                }
+            }
+            lack[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);        // rows' lanes: (2 t) * 4
+            lack[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        }
+
+        // ---- the loop over chunks
+        float o[N][DP / 16][4];
+        float ref[N][2], l[N][2];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+            ref[n][0] = ref[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            load(i + kStages - 1);            // to the place that the chunk before has left
+            const uint32_t s = (uint32_t)i % kStages, src = ring + s * Sl::kBytes;
+            int pos0, from, to;
+            bounds(i, pos0, from, to);
+            // scores
+            float x[N][4];
+#pragma unroll
+            for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                const uint4 lo = lds128(src + piece_at<DP>((uint32_t)g, (uint32_t)(4 * h + t)));
+                const uint4 hi = lds128(src + piece_at<DP>((uint32_t)g + 8u, (uint32_t)(4 * h + t)));
+                const uint32_t kl[4] = {lo.x, lo.y, lo.z, lo.w}, kh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __half2 l0, l1, h0, h1;
+                    decode4<kFormat>(kl[k], l0, l1);
+                    decode4<kFormat>(kh[k], h0, h1);
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        mma16816(x[n], as_u32(l0), as_u32(h0), as_u32(l1), as_u32(h1), qf[n][4 * h + k][0], qf[n][4 * h + k][1]);
+                }
+            }
+            // scales of tokens g and g + 8; one whose value scale (or page) is no number carries its NaN in the
+            // key's alone: where it is masked, its zero weight must not become 0 times NaN
+            float ks[2], vs[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t tok = (uint32_t)(g + 8 * e);
+                const float kv = lds32(src + Sl::kScales + tok * 4u), vv = lds32(src + Sl::kScales + 64u + tok * 4u);
+                const bool good = !(bad >> s & 1u) && vv <= 3.4028235e38f;
+                ks[e] = good ? kv * up : __int_as_float(0x7fffffff);
+                vs[e] = good && (int)tok >= from && (int)tok < to ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
+            }
+            // scores in log2 units; those that the row does not see -inf
+            const bool whole = from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= w.sinks);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = x[n][e] * ks[e >> 1] * lack[n][e & 1];
+            if (!whole) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = 8 * n + 2 * t + (e & 1), tok = g + 8 * (e >> 1), pos = pos0 + tok;
+                        const RowRange r = ranges[row];
+                        bool sees = tok >= from && tok < to && pos < r.end && (pos >= r.low || pos < w.sinks);
+                        if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
+                        if (!sees) x[n][e] = -INFINITY;
+                    }
+            }
+            // softmax terms and what they weigh the values' codes with
+            float p[N][4];
+            uint32_t pk[N][2];
+            auto terms = [&]() {
+                bool past = false;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    // (a score of -inf less a reference of -inf must not become NaN)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        p[n][e] = fast_exp2(x[n][e] - (x[n][e] == -INFINITY ? 0.f : ref[n][e & 1]));
+                    pk[n][0] = half_pair(p[n][0] * vs[0], p[n][1] * vs[0]);
+                    pk[n][1] = half_pair(p[n][2] * vs[1], p[n][3] * vs[1]);
+                    const uint32_t most = __vmaxu2(pk[n][0], pk[n][1]);
+                    past |= max(most & 0xffffu, most >> 16) >= kPast || fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])) > kSumMost;
+                }
+                return past;
+            };
+            if (__any_sync(0xffffffffu, terms())) {
+                // the references move to the chunk's largest terms, where these lie above
+                const float v0 = fmaxf(fast_log2(vs[0]), kVLeast), v1 = fmaxf(fast_log2(vs[1]), kVLeast);
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(x[n][e] + v0, x[n][e + 2] + v1);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (top == -INFINITY || !(top > ref[n][e] + kPeak)) continue;
+                        const float r = ceilf(top) - kPeak;           // P <= 2^7
+                        const float f = scale_down(1.f, ref[n][e] - r);
+                        l[n][e] = scale_down(l[n][e], ref[n][e] - r);
+                        ref[n][e] = r;
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k) o[n][k][e] *= f, o[n][k][e + 2] *= f;
+                    }
+                terms();
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                l[n][0] += p[n][0] + p[n][2];
+                l[n][1] += p[n][1] + p[n][3];
+                pk[n][0] = transpose8x8(pk[n][0]);
+                pk[n][1] = transpose8x8(pk[n][1]);
+            }
+            // outputs
+            uint32_t vw[4][DP / 32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t tok = (uint32_t)(2 * t + (j & 1) + 8 * (j >> 1));
+                if constexpr (DP == 128) {
+                    const uint4 u = lds128(src + Sl::kV + piece_at<DP>(tok, (uint32_t)g));
+                    vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = u.z, vw[j][3] = u.w;
+                } else {
+                    const uint2 u = lds64(src + Sl::kV + piece_at<DP>(tok, (uint32_t)g >> 1) + ((uint32_t)g & 1u) * 8u);
+                    vw[j][0] = u.x, vw[j][1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                const uint32_t pick = (k & 1) ? 0x7362u : 0x5140u;
+                __half2 a0, a1, a2, a3;
+                decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
+                decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
+#pragma unroll
+                for (int n = 0; n < N; ++n) mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][0], pk[n][1]);
+            }
+            __syncwarp();
+        }
+        cp_async_wait<0>();
+
+        // ---- the warps' parts join: [warp][row][dimension], the rows 4 floats apart from a power of two
+        __syncthreads();
+        float *parts_o = reinterpret_cast<float *>(smem);
+        constexpr int kPitch = DP + 4;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const int row = 8 * n + 2 * t + e;
+                if (g == 0) stats[warp][row] = make_float2(ref[n][e], sum);
+                float *to = parts_o + (warp * kRows + row) * kPitch + g * kCols;
+#pragma unroll
+                for (int k = 0; k < DP / 16; k += 2)
+                    *reinterpret_cast<float4 *>(to + 2 * k) = make_float4(o[n][k][e], o[n][k][e + 2], o[n][k + 1][e], o[n][k + 1][e + 2]);
+            }
+        __syncthreads();
+        // the join of `count` parts of row r at dimensions d .. d + 3
+        auto join = [&](int count, auto stat, auto from_part, float4 &sum, float &top, float &total) {
+            top = -INFINITY;
+            for (int i = 0; i < count; ++i) top = fmaxf(top, stat(i).x);
+            total = 0.f;
+            sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < count; ++i) {
+                const float2 st = stat(i);
+                if (st.x == -INFINITY && st.y == 0.f) continue;       // saw nothing
+                const float f = scale_down(1.f, st.x - top);
+                total += scale_down(st.y, st.x - top);
+                const float4 x = from_part(i);
+                sum.x += x.x * f, sum.y += x.y * f, sum.z += x.z * f, sum.w += x.w * f;
+            }
+        };
+        auto result = [&](int r, int d, const float4 &sum, float top, float total) {
+            const int m = m0 + r, blk = m / group;
+            const int64_t place = (q.first + blk) * Hq + head * group + (m - blk * group);
+            const float inv = total == 0.f ? 0.f : kVDown / total;
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + place * D + d) =
+                make_uint2(float_to_pair<T>(sum.x * inv, sum.y * inv), float_to_pair<T>(sum.z * inv, sum.w * inv));
+            if (d == 0 && a.lse) a.lse[place] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
+        };
+        const int quarters = D / 4;
+        float4 sum;
+        float top, total;
+        float *block_o = parts_o + kWarps * kRows * kPitch;
+        for (int i = threadIdx.x; i < rows * quarters; i += kThreads) {
+            const int r = i / quarters, d = (i - r * quarters) * 4;
+            join(kWarps, [&](int k) { return stats[k][r]; },
+                 [&](int k) { return *reinterpret_cast<const float4 *>(parts_o + (k * kRows + r) * kPitch + d); }, sum, top, total);
+            if (w.cluster == 1) {
+                result(r, d, sum, top, total);
+            } else {
+                *reinterpret_cast<float4 *>(block_o + r * kPitch + d) = sum;
+                if (d == 0) stats[kWarps][r] = make_float2(top, total);
+            }
+        }
+        if (w.cluster > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            for (int i = split * kThreads + threadIdx.x; i < rows * quarters; i += w.cluster * kThreads) {
+                const int r = i / quarters, d = (i - r * quarters) * 4;
+                join(w.cluster, [&](int k) { return *cluster.map_shared_rank(&stats[kWarps][r], k); },
+                     [&](int k) { return *reinterpret_cast<const float4 *>(cluster.map_shared_rank(block_o, k) + r * kPitch + d); },
+                     sum, top, total);
+                result(r, d, sum, top, total);
+            }
+            cluster.sync();     // before another block's memory goes, or is written again
+        }
+        __syncthreads();        // the ring is the next rows'
+        if (D != DP) {
+            for (uint32_t i = threadIdx.x; i < kWarps * kStages * Sl::kBytes / 16; i += kThreads)
+                reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+        }
+    }
+}
+
+template <typename T, int kFormat, int DP, int N>
+cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
+    static PerDeviceOnce once;
+    auto *kernel = window_kernel<T, kFormat, DP, N>;
+    constexpr size_t bytes = smem_bytes<N, DP>();
+    cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+    if (e != cudaSuccess) return e;
+    const AttentionArgs &a = w.a;
+    const int group = a.n_q_heads / a.cache.n_kv_heads;
+    // row blocks of an average request, which one block each takes at once
+    const int64_t rows = ((int64_t)a.rows.n_rows + a.rows.B - 1) / a.rows.B * group;
+    w.slots = (int)((rows + 8 * N - 1) / (8 * N));
+    // an item's tokens go to a cluster of up to 8 blocks while there are fewer blocks than SMs hold and a warp has
+    // four chunks or more
+    int64_t blocks = (int64_t)a.rows.B * a.cache.n_kv_heads * w.slots;
+    const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)w.window + w.sinks;
+    const int64_t chunks = (own < seen ? own : seen) / kChunk;
+    w.cluster = 1;
+    while (w.cluster < kMaxCluster && blocks * w.cluster < (int64_t)kNumSMs * Shape<N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
+        w.cluster *= 2;
+    blocks *= w.cluster;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)w.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, w);
+}
+
+template <typename T, int kFormat, int DP>
+cudaError_t launch_dp(WindowArgs &w, cudaStream_t s) {
+    const int group = w.a.n_q_heads / w.a.cache.n_kv_heads;
+    const int64_t rows = ((int64_t)w.a.rows.n_rows + w.a.rows.B - 1) / w.a.rows.B * group;
+    if (rows <= 8) return launch_n<T, kFormat, DP, 1>(w, s);
+    if (rows <= 16) return launch_n<T, kFormat, DP, 2>(w, s);
+    return launch_n<T, kFormat, DP, 3>(w, s);
+}
+
+template <typename T>
+cudaError_t launch_t(WindowArgs &w, cudaStream_t s) {
+    const bool e4m3 = w.a.cache.format == DSPARK_KV_E4M3;
+    if (w.a.cache.head_dim <= 64)
+        return e4m3 ? launch_dp<T, DSPARK_KV_E4M3, 64>(w, s) : launch_dp<T, DSPARK_KV_INT8, 64>(w, s);
+    return e4m3 ? launch_dp<T, DSPARK_KV_E4M3, 128>(w, s) : launch_dp<T, DSPARK_KV_INT8, 128>(w, s);
+}
+
+}  // namespace
+
+size_t window_ws_bytes(int, int, int, int, int) { return 0; }
+
+cudaError_t launch_window_attention(const AttentionArgs &a, int window, int sinks, cudaStream_t s) {
+    WindowArgs w{a, window, sinks, 1, 1};
+    return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
+}
+
+}  // namespace dspark
