@@ -117,7 +117,7 @@ dspark_status check_attention(AttentionArgs &a, const dspark_kv_cache *cache, co
     const char *qb = static_cast<const char *>(q), *ob = static_cast<const char *>(out);
     if (ob < qb + q_bytes && qb < ob + out_bytes) return fail(DSPARK_ERR_INVALID_ARG, "out must not overlap q");
     a = AttentionArgs{*cache, p, q, q_stride, dtype, n_q_heads, prefix_pages, prefix_len, (int)mask, row_mask, scale,
-                      out, lse, static_cast<unsigned char *>(workspace)};
+                      out, lse, static_cast<unsigned char *>(workspace), 0, 0};
     return DSPARK_OK;
 }
 
@@ -215,7 +215,9 @@ dspark_status dspark_window_attention(const dspark_kv_cache *cache, const void *
     if ((int64_t)max_pages * cache->page_size + prefix_len > 0x7fffffff)
         return fail(DSPARK_ERR_INVALID_ARG, "prefix_len + max_pages * page_size passes 2^31 - 1 tokens");
     if (nothing) return DSPARK_OK;
-    const cudaError_t e = launch_window_attention(a, window, sinks, static_cast<cudaStream_t>(stream));
+    a.window = window;
+    a.sinks = sinks;
+    const cudaError_t e = launch_window_attention(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "window attention launch");
     return DSPARK_OK;
 }

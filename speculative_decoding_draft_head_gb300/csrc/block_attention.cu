@@ -49,6 +49,11 @@
 // The roles' loops together nearly fill the instruction cache, so less code
 // was faster again and again: 64 scores at a time instead of 32 cost 1 to 10%, two
 // issuing warps 7%, 24 warps with the issuer apart from the converters 15%.
+//
+// Compiled twice: window_blocks.cu includes this file with kWindow true, for rows that
+// see through a window.  An item then visits fewer tiles: those of the first tokens, then those
+// that any row of its row tile's window can reach, as many for every row tile of a
+// request, so that the plan stays a division (View, own_view, prefix_view).
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -59,6 +64,12 @@ namespace dspark {
 namespace {
 
 using namespace tc;
+
+#ifdef DSPARK_WINDOW_BLOCKS
+constexpr bool kWindow = true;
+#else
+constexpr bool kWindow = false;
+#endif
 
 constexpr int kThreads = 640;
 // warps of the roles
@@ -99,6 +110,16 @@ struct Layout {
     static constexpr uint32_t kBytes = kQScale + 2048 + 1024;            // + alignment slack
 };
 
+// The tiles of a list of `total` that an item visits: `first` of its first ones, then, from a place
+// that may be the row tile's own, the rest.
+struct View {
+    int first, tiles, total;
+    // how far the others lie behind the first when the window of a row tile begins at token `low`
+    __device__ __forceinline__ int skip(int low) const {
+        return max(first, min(low / plan::kTile, total - (tiles - first))) - first;
+    }
+};
+
 // Consecutive tiles of one item
 struct Piece {
     int tiles, first;   // how many, and the first one's number in the item
@@ -110,13 +131,16 @@ struct Piece {
     int n;              // block rows (own tokens)
     int request;        // -1: the prefix
     int out;            // kDirect, kFirst, kContinued
-    int pad;
+    // through a window: tiles of the list before a gap, its width, and the first token that a row may see behind it
+    int first_tiles, skip, low;
+    // the list's tile that is the item's tile i
+    __device__ __forceinline__ int tile(int i) const { return i < first_tiles ? i : i + skip; }
 };
 // Up to four tiles of each group, taken in turns: 0 of the first, 0 of the
 // second, 1 of the first ..; pairs as tiles of the first.
 struct Round {
     int flags;                    // kRoundPair, kRoundEnd; bits 2 s, 2 s + 1: the first / last tile of stream s's piece is here
-    int n[2], token[2], piece[2]; // of the streams: tiles, first token, place of the piece
+    int n[2], token[2], piece[2]; // of the streams: tiles, first token (through a window: first tile of the item), place of the piece
     uint32_t chunks[2][32];       // where the tokens are, 16 a chunk, 8 chunks a tile
 };
 enum { kRoundPair = 16, kRoundEnd = 32 };
@@ -141,7 +165,38 @@ struct Partials {
     int64_t *unit0[2];  // [B] first own unit of each request in the class's part of the line, after the prefix's
     float2 *stats;      // (r, l): [R Hq] prefix, [R Hq] own, [kCtas][256] continued pairs, [2 kCtas][128] continued singles
     float *o;           // the same rows of D unnormalised outputs
+    int *prefix_low;    // through a window: the first token of the prefix behind its first ones that any row sees
 };
+
+// The own tiles that a request's row tiles visit.  A row tile's window is window + rows - 1 tokens long,
+// whichever the rows; L tokens touch (L + 126) / 128 + 1 tiles at most.
+__device__ __forceinline__ View own_view(const AttentionArgs &a, int n, int len, int group) {
+    const int total = plan::token_tiles(len);
+    if constexpr (!kWindow) return {0, total, total};
+    const int first = plan::token_tiles(min(max(a.sinks - a.prefix_len, 0), len));
+    // (a word's row may see one token further back than its place says)
+    const int rows = a.row_mask ? n + 1 : a.mask == DSPARK_MASK_CAUSAL ? min(n, (plan::kTileRows + group - 2) / group + 1) : n;
+    const int64_t tiles = first + ((int64_t)a.window + rows - 1 + 126) / plan::kTile + 1;
+    return {first, (int)(tiles < total ? tiles : total), total};
+}
+// The prefix's, with `low` as in Partials.
+__device__ __forceinline__ View prefix_view(const AttentionArgs &a, int low) {
+    const int total = plan::token_tiles(a.prefix_len);
+    if constexpr (!kWindow) return {0, total, total};
+    const int first = plan::token_tiles(min(a.sinks, a.prefix_len));
+    const int tiles = first + (low < a.prefix_len ? max(total - max(first, low / plan::kTile), 0) : 0);
+    return {first, tiles, total};
+}
+// The first token of the window of block row `i` behind ctx tokens (in any list that these are counted in), at
+// least 0; with a mask word, of which c bits count, that of its tokens before the block.
+__device__ __forceinline__ int window_low(const AttentionArgs &a, int ctx, int i) { return max(ctx + i - a.window + 1, 0); }
+__device__ __forceinline__ int window_low_of_word(const AttentionArgs &a, int ctx, int c) {
+    return max(ctx - max(a.window - c, 0), 0);
+}
+__device__ __forceinline__ uint64_t word_of(const AttentionArgs &a, int64_t row, int n) {
+    const uint64_t word = a.row_mask[row];
+    return n < 64 ? word & ((1ull << n) - 1) : word;
+}
 
 __device__ __forceinline__ int prefix_rows(const AttentionArgs &a) {
     const int64_t r = a.rows.row0[a.rows.B];
@@ -187,7 +242,7 @@ __device__ __forceinline__ void store8(float *to, const uint32_t *x, float f) {
 // ------------------------------------------------------------------ the plan --
 // The line as a CTA sees it.
 struct Line {
-    int group, prefix_m, prefix_tiles;
+    int group, prefix_m, prefix_tiles, prefix_low;
     int64_t prefix[2], pairs, total;   // units of the prefix's items by class, of all pairs, of all
 };
 
@@ -226,7 +281,7 @@ struct Walk {
                 __syncwarp();
                 b = at;
                 m = w_n[at - wb] * group;
-                tiles = plan::token_tiles(w_len[at - wb]);
+                tiles = own_view(a, w_n[at - wb], w_len[at - wb], group).tiles;
                 __syncwarp();
                 return true;
             }
@@ -293,7 +348,20 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
         p.n = b < 0 ? 0 : k.w_n[b - k.wb];
         p.ctx = p.len - p.n;
         p.out = t0 > 0 ? kContinued : (b >= 0 && z.prefix_tiles == 0 && t1 == tiles) ? kDirect : kFirst;
-        p.pad = 0;
+        p.first_tiles = p.skip = p.low = 0;
+        if constexpr (kWindow) {
+            const View view = b < 0 ? prefix_view(a, z.prefix_low) : own_view(a, p.n, p.len, z.group);
+            p.first_tiles = view.first;
+            p.low = b >= 0 ? window_low(a, p.ctx, p.m0 / z.group) : z.prefix_low < p.len ? z.prefix_low : 0x7fffffff;
+            if (b >= 0 && a.row_mask) {
+                int least = 64;
+                for (int i = lane; i < p.n; i += 32) least = min(least, __popcll(word_of(a, p.row_base + i, p.n)));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+                p.low = window_low_of_word(a, p.ctx, least);
+            }
+            p.skip = view.skip(p.low);
+        }
         __syncwarp();
         // the cursor moves to the next item
         k.start = k.u = start + plan::item_total(cls, tiles);
@@ -324,6 +392,8 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
 // kept by chunk of 16 tokens (a chunk lies inside one page), as the chunk's
 // number in the cache, in units of 16 head rows: 32 chunks (4 tiles) at a time,
 // one a lane, their pages loaded four tiles before they are needed.
+// tokens of a run: a power of two of them share a page
+__device__ __forceinline__ int run_tokens(int page_size) { return min(page_size & -page_size, plan::kTile); }
 constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 // Pieces a stream's tiles refer to: a slot is written again only after every
 // tile of its piece has left the rings (the next piece is planned while the last
@@ -338,9 +408,16 @@ struct Stream {
     Piece slots[kPieces];
 
     __device__ __forceinline__ void load_pages(const AttentionArgs &a, const Piece &p, int t, int lane) {
-        const int per_page = a.cache.page_size / 16, chunk = (p.first + t) * 8 + lane;
+        const int per_page = a.cache.page_size / 16;
+        const int chunk = kWindow ? p.tile(p.first + t + (lane >> 3)) * 8 + (lane & 7) : (p.first + t) * 8 + lane;
         int place = -1, pg = 0;
-        if ((int64_t)chunk * 16 < p.len) {
+        bool some = (int64_t)chunk * 16 < p.len;
+        if constexpr (kWindow) {    // pages that no row sees are not looked at; a page's tokens are loaded a run at a time
+            const int sinks = p.request < 0 ? a.sinks : max(a.sinks - a.prefix_len, 0);
+            const int run = run_tokens(a.cache.page_size), at = chunk * 16 & -run;
+            some = some && (at < sinks || at + run > p.low);
+        }
+        if (some) {
             const int slot = chunk / per_page;
             place = p.head * per_page + (chunk - slot * per_page);
             pg = p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
@@ -374,7 +451,7 @@ __device__ __noinline__ int stream_round(const AttentionArgs &a, const Line &z, 
     const Piece *p = s.slots + count % kPieces;
     if (lane == 0) {
         r.n[id] = n;
-        r.token[id] = (p->first + j) * plan::kTile;
+        r.token[id] = kWindow ? p->first + j : (p->first + j) * plan::kTile;
         r.piece[id] = id * kPieces + (int)(count % kPieces);
     }
     __syncwarp();
@@ -522,7 +599,32 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     }
 
     // ---- the line of units, and the requests this CTA's workers start in
-    const int prefix_m = prefix_rows(a) * group, prefix_tiles = plan::token_tiles(a.prefix_len);
+    const int prefix_m = prefix_rows(a) * group;
+    int prefix_low = 0;
+    if constexpr (kWindow) {
+        // (a request's first row, or a row whose word has no bits, reaches furthest back)
+        prefix_low = a.prefix_len;
+        for (int b = tid; b < a.rows.B; b += kThreads) {
+            const Request q = load_request(a, b);
+            if (!q.len_ok || q.n == 0) continue;
+            const int ctx = a.prefix_len + q.len - q.n;
+            int low = window_low(a, ctx, 0);
+            if (a.row_mask) {
+                int least = 64;
+                for (int i = 0; i < q.n; ++i) least = min(least, __popcll(word_of(a, q.first + i, q.n)));
+                low = window_low_of_word(a, ctx, least);
+            }
+            prefix_low = min(prefix_low, low);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) prefix_low = min(prefix_low, __shfl_xor_sync(0xffffffffu, prefix_low, d));
+        if (lane == 0) scan[0][warp] = prefix_low;
+        __syncthreads();
+        for (int i = 0; i < kThreads / 32; ++i) prefix_low = min(prefix_low, (int)scan[0][i]);
+        __syncthreads();
+        if (blockIdx.x == 0 && tid == 0) *parts.prefix_low = prefix_low;
+    }
+    const int prefix_tiles = prefix_view(a, prefix_low).tiles;
     int64_t prefix[2];
     for (int k = 0; k < 2; ++k) prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
     auto request_units = [&](int b, int64_t (&x)[2]) {
@@ -531,7 +633,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const Request q = load_request(a, b);
         if (blockIdx.x == 0 && (!q.rows_ok || (q.n > 0 && !q.len_ok))) atomicOr(c.flags, kFlagBadLength);
         if (!q.len_ok || q.n == 0) return;
-        const int tiles = plan::token_tiles(q.len);
+        const int tiles = own_view(a, q.n, q.len, group).tiles;
         for (int k = 0; k < 2; ++k) x[k] = plan::head_units(k, q.n * group, tiles) * c.n_kv_heads;
     };
     int64_t mine[2];
@@ -561,6 +663,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         line.group = group;
         line.prefix_m = prefix_m;
         line.prefix_tiles = prefix_tiles;
+        line.prefix_low = prefix_low;
         line.prefix[0] = prefix[0];
         line.prefix[1] = prefix[1];
         line.pairs = pairs;
@@ -642,18 +745,20 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     // on), to place `position` of the order of operands, in runs of tokens that share a page: their
     // codes or (another warp) with the keys the scales of both.  (Copies by the warp's own cp.async,
     // 512 bytes at a time, held it up: 2300 clocks a tile.)
-    const int run = min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
+    const int run = run_tokens(c.page_size), runs = plan::kTile / run;
     auto load = [&](uint32_t mine, bool is_v, uint32_t position, bool codes) {
         const int i = lane & 7;
         const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
         const bool good = i < runs && id < kBadChunk;
         const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
+        // of the tile's chunks those that nothing comes from: with a window also such as no row sees
+        const unsigned gone = kWindow ? __ballot_sync(0xffffffffu, mine >= kBadChunk) & 0xffu : bad;
         const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
         const uint32_t slot = position % kRaw;
         if (!warp_wait(raw_empty(slot), ((position / kRaw) & 1) ^ 1, abort)) return false;
         const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
         if (lane == 0) {
-            if (codes) raw_bad[slot] = (int)bad;
+            if (codes) raw_bad[slot] = (int)gone;
             mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (codes ? D : is_v ? 0 : 8)));
         }
         __syncwarp();
@@ -694,7 +799,8 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             order.step(flags);
             if (!end) {
                 const Piece &p = piece_at(uniform(r.piece[id]));
-                valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
+                if constexpr (kWindow) valid = uniform(p.len) - uniform(p.tile(r.token[id] + i)) * plan::kTile;
+                else valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
                 if (flags & kTileFirst) {
                     // the piece's queries, by both teams
 #pragma unroll 1
@@ -997,6 +1103,29 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             const int ctx = uniform(p.ctx), tiles = uniform(p.tiles);
             int sees = ctx, token = uniform(p.first) * plan::kTile;
             uint64_t word = 0;
+            int low = 0, sinks = 0;     // through a window: from `low` on, and tokens before `sinks`
+            if constexpr (kWindow) {
+                sinks = p.request < 0 ? a.sinks : max(a.sinks - a.prefix_len, 0);
+                // the row's block and its place in it, for the prefix where any row's window reaches that
+                int64_t first_row = p.row_base;
+                int n_block = p.n, behind = ctx, i = blk;
+                if (p.request < 0 && uniform(line.prefix_low) < p.len) {
+                    int lo = 0, hi = a.rows.B;
+                    while (hi - lo > 1) {       // the last request that begins at or before the row
+                        const int mid = (lo + hi) >> 1;
+                        if (a.rows.row0[mid] <= blk) lo = mid;
+                        else hi = mid;
+                    }
+                    const Request q = load_request(a, lo);
+                    first_row = q.first;
+                    n_block = q.n;
+                    i = blk - (int)q.first;
+                    behind = a.prefix_len + (q.len_ok ? q.len - q.n : 0);
+                }
+                if (n_block == 0) low = 0x7fffffff;
+                else if (!a.row_mask) low = window_low(a, behind, i);
+                else if (live) low = window_low_of_word(a, behind, __popcll(word_of(a, first_row + i, n_block)));
+            }
             if (p.request >= 0) {
                 if (a.row_mask) {
                     if (live) word = a.row_mask[p.row_base + blk];
@@ -1010,6 +1139,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++n, token += plan::kTile) {
                 const bool first = j == 0;
+                if constexpr (kWindow) token = uniform(p.tile(p.first + j)) * plan::kTile;
                 if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
                 tc_fence_after();
                 if (first) {
@@ -1019,7 +1149,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (warp_live) {
                     const uint32_t ss = n % kScaleSlots;
                     const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 256, *vs = ks + 128;
-                    const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
+                    // some row does not see some token of this tile
+                    bool masked = token > ctx - plan::kTile;
+                    if constexpr (kWindow)
+                        masked = masked || __any_sync(0xffffffffu, live && low > token && sinks - plan::kTile < token);
                     float ref = r == -INFINITY ? 0.f : r;
                     __syncwarp();
                     // the row's scores 32 columns at a time: more would spill, and with this much shared
@@ -1031,6 +1164,10 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                         if (masked) {
                             const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
                             bits = full == 32 ? ~0u : (1u << full) - 1;
+                            if constexpr (kWindow) {
+                                const int hid = min(max(low - from_t, 0), 32), sink = min(max(sinks - from_t, 0), 32);
+                                bits &= (hid == 32 ? 0u : ~0u << hid) | (sink == 32 ? ~0u : (1u << sink) - 1);
+                            }
                             const int sh = from_t - ctx;   // block token of the first column
                             if (sh > -32 && sh < 64) bits |= (uint32_t)(sh >= 0 ? word >> sh : word << -sh);
                             some_hidden = __any_sync(0xffffffffu, bits != ~0u);
@@ -1235,7 +1372,8 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
     const Request q = load_request(a, b);
     if (q.n == 0) return;
     // the line: units of the prefix by class, of all pairs, of all (the last request's end)
-    const int prefix_m = prefix_rows(a) * group, prefix_tiles = plan::token_tiles(a.prefix_len);
+    const int prefix_m = prefix_rows(a) * group;
+    const int prefix_tiles = prefix_view(a, kWindow ? *parts.prefix_low : 0).tiles;
     int64_t prefix[2], pairs, total;
     {
         const int last = a.rows.B - 1;
@@ -1245,7 +1383,9 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         for (int k = 0; k < 2; ++k) {
             prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
             end[k] = prefix[k] + parts.unit0[k][last] +
-                     (z.len_ok && z.n > 0 ? plan::head_units(k, z.n * group, plan::token_tiles(z.len)) * c.n_kv_heads : 0);
+                     (z.len_ok && z.n > 0
+                          ? plan::head_units(k, z.n * group, own_view(a, z.n, z.len, group).tiles) * c.n_kv_heads
+                          : 0);
         }
         pairs = end[0];
         total = end[0] + end[1];
@@ -1256,7 +1396,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
     // this lane's item (0 the prefix's, 1 the request's own) and its place among the item's workers
     const int side = lane >> 4, at = lane & 15;
     const int m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
-    const int tiles = side ? plan::token_tiles(q.len) : prefix_tiles;
+    const int tiles = side ? own_view(a, q.n, q.len, group).tiles : prefix_tiles;
     for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < c.n_kv_heads * chunks; i += gridDim.y * kJoinWarps) {
         const int h = i / chunks, m0 = (i - h * chunks) * per, m1 = min(m0 + per, own_m);
         int item = -1;             // the row tile that is looked at
@@ -1355,7 +1495,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
 }
 
 struct Regions {
-    size_t unit1, stats, o, bytes;
+    size_t unit1, stats, o, low, bytes;
 };
 Regions regions(int B, int n_rows, int n_q_heads, int D) {
     const size_t parts = 2 * (size_t)n_rows * n_q_heads + 2 * (size_t)kCtas * plan::kTileRows;
@@ -1363,7 +1503,8 @@ Regions regions(int B, int n_rows, int n_q_heads, int D) {
     g.unit1 = align_up((size_t)B * sizeof(int64_t), 256);
     g.stats = 2 * g.unit1;
     g.o = align_up(g.stats + parts * sizeof(float2), 256);
-    g.bytes = align_up(g.o + parts * D * sizeof(float), 256);
+    g.low = align_up(g.o + parts * D * sizeof(float), 256);
+    g.bytes = g.low + (kWindow ? 256 : 0);
     return g;
 }
 
@@ -1400,17 +1541,28 @@ cudaError_t launch_format(const AttentionArgs &a, const Partials &p, cudaStream_
     return e4m3 ? launch_t<T, DSPARK_KV_E4M3, 128>(a, p, s) : launch_t<T, DSPARK_KV_INT8, 128>(a, p, s);
 }
 
+cudaError_t launch_blocks(const AttentionArgs &a, cudaStream_t s) {
+    const Regions g = regions(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.head_dim);
+    const Partials p{{reinterpret_cast<int64_t *>(a.ws), reinterpret_cast<int64_t *>(a.ws + g.unit1)},
+                     reinterpret_cast<float2 *>(a.ws + g.stats), reinterpret_cast<float *>(a.ws + g.o),
+                     reinterpret_cast<int *>(a.ws + g.low)};
+    return a.dt == DSPARK_BF16 ? launch_format<__nv_bfloat16>(a, p, s) : launch_format<__half>(a, p, s);
+}
+
 }  // namespace
 
+#ifdef DSPARK_WINDOW_BLOCKS
+size_t window_blocks_ws_bytes(int B, int n_rows, int n_q_heads, int, int head_dim) {
+    return regions(B, n_rows, n_q_heads, head_dim).bytes;
+}
+
+cudaError_t launch_window_blocks(const AttentionArgs &a, cudaStream_t s) { return launch_blocks(a, s); }
+#else
 size_t attention_ws_bytes(int B, int n_rows, int n_q_heads, int, int head_dim) {
     return regions(B, n_rows, n_q_heads, head_dim).bytes;
 }
 
-cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s) {
-    const Regions g = regions(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.head_dim);
-    const Partials p{{reinterpret_cast<int64_t *>(a.ws), reinterpret_cast<int64_t *>(a.ws + g.unit1)},
-                     reinterpret_cast<float2 *>(a.ws + g.stats), reinterpret_cast<float *>(a.ws + g.o)};
-    return a.dt == DSPARK_BF16 ? launch_format<__nv_bfloat16>(a, p, s) : launch_format<__half>(a, p, s);
-}
+cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s) { return launch_blocks(a, s); }
+#endif
 
 }  // namespace dspark

@@ -251,11 +251,15 @@ struct AttentionArgs {
     void *out;
     float *lse;
     unsigned char *ws;
+    int window, sinks;           // dspark_window_attention only
 };
 size_t attention_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s);
 size_t window_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
-cudaError_t launch_window_attention(const AttentionArgs &a, int window, int sinks, cudaStream_t s);
+cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s);
+// its blocks with many rows
+size_t window_blocks_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_window_blocks(const AttentionArgs &a, cudaStream_t s);
 
 // ------------------------------------------------------- rotary positions --
 constexpr int kMaxRotaryDim = 256;

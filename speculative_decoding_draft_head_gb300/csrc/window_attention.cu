@@ -52,7 +52,6 @@ constexpr int kMaxCluster = 8;
 
 struct WindowArgs {
     AttentionArgs a;
-    int window, sinks;
     int slots;          // row blocks of a request that have blocks of their own; more follow in a loop
     int cluster;        // blocks an item's tokens are split over
 };
@@ -199,18 +198,18 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         const int ctx = a.prefix_len + q.len - q.n;       // tokens before the block
         const int b0 = m0 / group, b1 = (m0 + rows - 1) / group;
         const bool tree = a.row_mask != nullptr, causal = !tree && a.mask == DSPARK_MASK_CAUSAL;
-        int low_min = max(ctx + b0 - w.window + 1, 0), low_max = max(ctx + b1 - w.window + 1, 0);
+        int low_min = max(ctx + b0 - a.window + 1, 0), low_max = max(ctx + b1 - a.window + 1, 0);
         const int end_min = causal ? ctx + b0 + 1 : tree ? ctx : ctx + q.n;
         const int end_max = causal ? ctx + b1 + 1 : ctx + q.n;
         __syncthreads();
         if (threadIdx.x < kRows) {
             const int m = m0 + min((int)threadIdx.x, rows - 1), blk = m / group;
-            RowRange r{max(ctx + blk - w.window + 1, 0), causal ? ctx + blk + 1 : ctx + q.n};
+            RowRange r{max(ctx + blk - a.window + 1, 0), causal ? ctx + blk + 1 : ctx + q.n};
             uint64_t word = 0;
             if (tree) {
                 word = a.row_mask[q.first + blk];
                 if (q.n < 64) word &= (1ull << q.n) - 1;
-                r.low = max(ctx - max(w.window - __popcll(word), 0), 0);
+                r.low = max(ctx - max(a.window - __popcll(word), 0), 0);
             }
             ranges[threadIdx.x] = r;
             words[threadIdx.x] = word;
@@ -221,7 +220,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             for (int i = 1; i < kRows; ++i) low_min = min(low_min, ranges[i].low), low_max = max(low_max, ranges[i].low);
         }
         Chunks chunks;
-        chunks.find(a.prefix_len, w.sinks, low_min, end_max);
+        chunks.find(a.prefix_len, a.sinks, low_min, end_max);
 
         // ---- the warp's chunks
         const int parts = w.cluster * kWarps, part = split * kWarps + warp;
@@ -243,7 +242,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             const int chunk = chunks.at(part + i * parts, own);
             pos0 = chunk * kChunk + (own ? a.prefix_len : 0);
             to = min(own ? end_max : min(a.prefix_len, end_max), pos0 + kChunk) - pos0;
-            from = pos0 < w.sinks ? 0 : max(low_min - pos0, 0);
+            from = pos0 < a.sinks ? 0 : max(low_min - pos0, 0);
         };
         auto load = [&](int i) {
             if (i < mine) {
@@ -375,7 +374,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 vs[e] = good && (int)tok >= from && (int)tok < to ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
             }
             // scores in log2 units; those that the row does not see -inf
-            const bool whole = from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= w.sinks);
+            const bool whole = from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= a.sinks);
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -387,7 +386,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                     for (int e = 0; e < 4; ++e) {
                         const int row = 8 * n + 2 * t + (e & 1), tok = g + 8 * (e >> 1), pos = pos0 + tok;
                         const RowRange r = ranges[row];
-                        bool sees = tok >= from && tok < to && pos < r.end && (pos >= r.low || pos < w.sinks);
+                        bool sees = tok >= from && tok < to && pos < r.end && (pos >= r.low || pos < a.sinks);
                         if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
                         if (!sees) x[n][e] = -INFINITY;
                     }
@@ -556,7 +555,7 @@ cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     // an item's tokens go to a cluster of up to 8 blocks while there are fewer blocks than SMs hold and a warp has
     // four chunks or more
     int64_t blocks = (int64_t)a.rows.B * a.cache.n_kv_heads * w.slots;
-    const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)w.window + w.sinks;
+    const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)a.window + a.sinks;
     const int64_t chunks = (own < seen ? own : seen) / kChunk;
     w.cluster = 1;
     while (w.cluster < kMaxCluster && blocks * w.cluster < (int64_t)kNumSMs * Shape<N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
@@ -596,10 +595,18 @@ cudaError_t launch_t(WindowArgs &w, cudaStream_t s) {
 
 }  // namespace
 
-size_t window_ws_bytes(int, int, int, int, int) { return 0; }
+// Blocks with many rows go to the 128-row tiles of the tensor cores.
+static bool many_rows(int B, int n_rows, int n_q_heads, int n_kv_heads) {
+    return ((int64_t)n_rows + B - 1) / B * (n_q_heads / n_kv_heads) >= 128;
+}
 
-cudaError_t launch_window_attention(const AttentionArgs &a, int window, int sinks, cudaStream_t s) {
-    WindowArgs w{a, window, sinks, 1, 1};
+size_t window_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim) {
+    return many_rows(B, n_rows, n_q_heads, n_kv_heads) ? window_blocks_ws_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) : 0;
+}
+
+cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s) {
+    if (many_rows(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.n_kv_heads)) return launch_window_blocks(a, s);
+    WindowArgs w{a, 1, 1};
     return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
 }
 

@@ -86,6 +86,9 @@ SHAPES = {
     "long context, window as long": ([1], [20011], 0, 4, 1, 64, 64, 19999, 4),
     "long prefix": ([2, 5], [3, 70], 20011, 4, 1, 64, 64, 900, 133),
     "prompt": ([700], [10], 5, 4, 2, 128, 16, 200, 4),
+    "prompts": ([700, 1, 90, 260], [10, 500, 300, 0], 205, 8, 2, 128, 64, 150, 30),
+    "prompts longer than the window": ([1300, 900], [700, 2000], 0, 6, 2, 64, 48, 129, 1),
+    "prompt of wide heads, no first tokens": ([300, 280], [1000, 140], 90, 64, 1, 96, 16, 333, 0),
     "many short requests": ([1, 2, 3] * 60, [5, 40, 130] * 60, 20, 4, 2, 64, 16, 33, 4),
 }
 
@@ -97,7 +100,7 @@ def test_shapes(name, fmt, dtype):
 
 
 @pytest.mark.parametrize("name", ["verify blocks", "window into the prefix", "block longer than the window",
-                                  "blocks of many row blocks", "sinks past everything", "prompt"])
+                                  "blocks of many row blocks", "sinks past everything", "prompt", "prompts"])
 def test_full_block(name):
     _run(*SHAPES[name], mask="full")
 
@@ -113,6 +116,16 @@ def test_tree_masks_and_rows_that_see_nothing(n, ctx, prefix, window, sinks):
     got, *_ = _run([n, n], [ctx, ctx], prefix, 4, 2, 64, 16, window, sinks, mask="full", words=words)
     if ctx == 0 and prefix == 0:
         assert bool((got["out"][0] == 0).all()) and bool((got["lse"][0] == -math.inf).all())
+
+
+@pytest.mark.parametrize("ctx,prefix,window,sinks", [(0, 0, 64, 0), (5, 20, 64, 9), (700, 130, 100, 150), (300, 0, 64, 0),
+                                                     (90, 300, 200, 40)])
+def test_trees_of_many_query_heads(ctx, prefix, window, sinks):
+    gen = torch.Generator().manual_seed(ctx)
+    n = 50
+    words = torch.randint(-2 ** 63, 2 ** 63 - 1, (2 * n + 9,), generator=gen)
+    words[0], words[2 * n - 1] = 0, -1
+    _run([n, 9, n], [ctx, 3, ctx + 77], prefix, 20, 2, 64, 16, window, sinks, mask="full", words=words)
 
 
 @pytest.mark.parametrize("mask,tree", [("causal", False), ("full", False), ("full", True)])
@@ -223,8 +236,9 @@ def test_rows_of_no_request_and_strided_queries():
     _check({k: t[:5] for k, t in out.items()}, plain_window.attention(wide[:5, 2:6], pool, row0, [20, 30], 25, 3))
 
 
-def test_the_same_call_gives_the_same_bits_on_a_stream_and_replayed():
-    shape = ([3, 1, 6], [700, 20, 90], 50, 8, 2, 128, 64, 300, 4)
+@pytest.mark.parametrize("rows", [[3, 1, 6], [130, 70, 90]])
+def test_the_same_call_gives_the_same_bits_on_a_stream_and_replayed(rows):
+    shape = (rows, [700, 20, 90], 50, 8, 2, 128, 64, 300, 4)
     got, q, pool, row0, lens = _run(*shape)
     cache, args = pool.cache(binding), (pool.table.cuda(), torch.tensor(lens).int().cuda(), row0.cuda())
     kw = dict(window=300, sinks=4, prefix_pages=pool.prefix_pages.cuda(), prefix_len=50)
