@@ -34,6 +34,8 @@
 //     of rows 2 t and 2 t + 1.
 // In shared memory 16-byte pieces of a chunk are permuted so that neither read
 // meets itself in a bank.
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "attention_common.cuh"
@@ -160,6 +162,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     __shared__ RowRange ranges[kRows];
     __shared__ uint64_t words[kRows];
     __shared__ float2 stats[kWarps + 1][kRows];   // (r, l) of the warps, and of the block
+    __shared__ float weights[kWarps][kRows];      // of the warps' parts in the block's
 
     const AttentionArgs &a = w.a;
     const dspark_kv_cache &c = a.cache;
@@ -222,21 +225,12 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         Chunks chunks;
         chunks.find(a.prefix_len, a.sinks, low_min, end_max);
 
-        // ---- the warp's chunks
+        // ---- the warp's chunks: their numbers in the cache, in 16 head rows, a lane each for 32 of them, and the
+        // next 32; bits of those that some row sees only in part (or not at all)
         const int parts = w.cluster * kWarps, part = split * kWarps + warp;
         const int mine = chunks.total > part ? (chunks.total - part + parts - 1) / parts : 0;
         const int per_page = c.page_size / kChunk;
-        auto place_of = [&](int i) {          // the warp's chunk i: its number in the cache, in 16 head rows
-            if (i >= mine) return kNoChunk;
-            bool own;
-            const int chunk = chunks.at(part + i * parts, own), page_slot = chunk / per_page;
-            const int page = own ? a.rows.block_table[(int64_t)b * a.rows.max_pages + page_slot] : a.prefix_pages[page_slot];
-            if (page < 0 || page >= c.n_pages) return kBadChunk;
-            return ((uint32_t)page * (uint32_t)H + (uint32_t)head) * (uint32_t)per_page + (uint32_t)(chunk - page_slot * per_page);
-        };
-        uint32_t places = place_of(lane), places_next = kNoChunk;
-        uint32_t bad = 0;                     // of the ring's slots
-        // the tokens of a chunk that some row may see: [from, to)
+        // the tokens of a chunk that some row may see: [from, to), and where it begins
         auto bounds = [&](int i, int &pos0, int &from, int &to) {
             bool own;
             const int chunk = chunks.at(part + i * parts, own);
@@ -244,40 +238,73 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             to = min(own ? end_max : min(a.prefix_len, end_max), pos0 + kChunk) - pos0;
             from = pos0 < a.sinks ? 0 : max(low_min - pos0, 0);
         };
-        auto load = [&](int i) {
+        auto look = [&](int i, uint32_t &place, uint32_t &edges) {
+            place = kNoChunk;
+            bool edge = false;
             if (i < mine) {
-                if ((i & 31) == 0) {
-                    if (i) places = places_next;
-                    places_next = place_of(i + 32 + lane);
-                }
-                const uint32_t place = __shfl_sync(0xffffffffu, places, i & 31), s = (uint32_t)i % kStages;
-                const uint32_t dst = ring + s * Sl::kBytes;
-                const bool good = place < kBadChunk;
-                bad = good ? bad & ~(1u << s) : bad | 1u << s;
-                if (!good && lane == 0) atomicOr(c.flags, kFlagBadPage);
+                bool own;
+                const int chunk = chunks.at(part + i * parts, own), page_slot = chunk / per_page;
+                const int page = own ? a.rows.block_table[(int64_t)b * a.rows.max_pages + page_slot] : a.prefix_pages[page_slot];
+                place = page < 0 || page >= c.n_pages ? kBadChunk
+                                                      : ((uint32_t)page * (uint32_t)H + (uint32_t)head) * (uint32_t)per_page +
+                                                            (uint32_t)(chunk - page_slot * per_page);
                 int pos0, from, to;
                 bounds(i, pos0, from, to);
-                const uint64_t row = good ? (uint64_t)place * kChunk : 0;
-                constexpr int kPieces = DP / 16, kPer = 32 / kPieces;       // pieces of a token; tokens at once
-                const int col = lane % kPieces;
-                const unsigned char *k = static_cast<const unsigned char *>(c.k) + row * (uint32_t)D;
-                const unsigned char *v = static_cast<const unsigned char *>(c.v) + row * (uint32_t)D;
+                edge = !(from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= a.sinks));
+            }
+            edges = __ballot_sync(0xffffffffu, edge);
+        };
+        uint32_t places, edges, places_next = kNoChunk, edges_next = 0;
+        look(lane, places, edges);
+        // Chunk i to the ring's place `to`; bits of the ring's places that hold an edge, and no page.
+        uint32_t slot_edge = 0, slot_bad = 0;
+        constexpr int kPieces = DP / 16, kPer = 32 / kPieces;       // pieces of a token; tokens at once
+        const int col = lane % kPieces, tok0 = lane / kPieces;
+        // (the permutation repeats every 8 tokens: tokens tok0 + 4 j at DP = 128 have two, tok0 + 8 j at 64 one)
+        const uint32_t put0 = piece_at<DP>((uint32_t)tok0, (uint32_t)col), put1 = piece_at<DP>((uint32_t)(tok0 + kPer), (uint32_t)col);
+        const bool in_row = D == DP || col * 16 < D;
+        const float *const scales = (lane < 4 ? c.k_scale : c.v_scale) + (lane & 3) * 4;
+        auto copy = [&](uint32_t dst, uint64_t place, auto width, auto there) {
+            const uint64_t at = place * (uint64_t)(kChunk * width) + (uint32_t)(tok0 * width + col * 16);
+            const unsigned char *k = static_cast<const unsigned char *>(c.k) + at, *v = static_cast<const unsigned char *>(c.v) + at;
+            if (in_row) {
 #pragma unroll
                 for (int j = 0; j < kChunk / kPer; ++j) {
-                    const int tok = lane / kPieces + j * kPer;
-                    const bool there = good && tok >= from && tok < to;
-                    if (D == DP || col * 16 < D) {
-                        cp_async16(dst + piece_at<DP>((uint32_t)tok, (uint32_t)col), k + tok * D + col * 16, there);
-                        cp_async16(dst + Sl::kV + piece_at<DP>((uint32_t)tok, (uint32_t)col), v + tok * D + col * 16, there);
-                    }
+                    const uint32_t to = dst + ((j & 1) ? put1 : put0) + (uint32_t)((j >> 1) * 2 * kPer * DP);
+                    cp_async16(to, k + j * kPer * width, there(tok0 + j * kPer));
+                    cp_async16(to + Sl::kV, v + j * kPer * width, there(tok0 + j * kPer));
                 }
-                if (lane < 8)
-                    cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, (lane < 4 ? c.k_scale : c.v_scale) + row + (lane & 3) * 4, good);
+            }
+            if (lane < 8) cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, scales + place * kChunk, true);
+        };
+        auto load = [&](int i, uint32_t s) {
+            if (i < mine) {
+                if ((i & 31) == 0) {
+                    if (i) places = places_next, edges = edges_next;
+                    if (i + 32 < mine) look(i + 32 + lane, places_next, edges_next);
+                }
+                const uint32_t place = __shfl_sync(0xffffffffu, places, i & 31), dst = ring + s * Sl::kBytes, bit = 1u << s;
+                slot_edge &= ~bit, slot_bad &= ~bit;
+                if (place < kBadChunk && !(edges >> (i & 31) & 1u)) {
+                    auto all = [](int) { return true; };
+                    if (D == DP) copy(dst, place, std::integral_constant<int, DP>{}, all);
+                    else copy(dst, place, D, all);
+                } else {
+                    const bool good = place < kBadChunk;
+                    slot_edge |= bit;
+                    if (!good) {
+                        slot_bad |= bit;
+                        if (lane == 0) atomicOr(c.flags, kFlagBadPage);
+                    }
+                    int pos0, from, to;
+                    bounds(i, pos0, from, to);
+                    copy(dst, good ? place : 0, D, [&](int tok) { return good && tok >= from && tok < to; });
+                }
             }
             cp_async_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i);
+        for (int i = 0; i < kStages - 1; ++i) load(i, (uint32_t)i);
 
         // ---- the queries: block n's row g, dimensions 64 h + 16 t + 0 .. 15, in fp16 after a power of two
         uint32_t qf[N][kSteps][2];
@@ -335,22 +362,32 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             ref[n][0] = ref[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
         }
+        // places in a chunk of what the lane reads: keys of tokens g and g + 8 (8 lines on), its pieces 64 dimensions
+        // apart; values of tokens 2 t, 2 t + 1 and of those 8 on
+        uint32_t get_k[kHalves], get_v[2];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) get_k[h] = piece_at<DP>((uint32_t)g, (uint32_t)(4 * h + t));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            get_v[j] = Sl::kV + (DP == 128 ? piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g)
+                                           : piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g >> 1) + ((uint32_t)g & 1u) * 8u);
+        uint32_t s = 0, s_load = kStages - 1;
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            load(i + kStages - 1);            // to the place that the chunk before has left
-            const uint32_t s = (uint32_t)i % kStages, src = ring + s * Sl::kBytes;
-            int pos0, from, to;
-            bounds(i, pos0, from, to);
+            load(i + kStages - 1, s_load);    // to the place that the chunk before has left
+            const uint32_t src = ring + s * Sl::kBytes;
+            const bool edge = slot_edge >> s & 1u, bad = slot_bad >> s & 1u;
+            s = s + 1 == kStages ? 0 : s + 1;
+            s_load = s_load + 1 == kStages ? 0 : s_load + 1;
             // scores
             float x[N][4];
 #pragma unroll
             for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-                const uint4 lo = lds128(src + piece_at<DP>((uint32_t)g, (uint32_t)(4 * h + t)));
-                const uint4 hi = lds128(src + piece_at<DP>((uint32_t)g + 8u, (uint32_t)(4 * h + t)));
+                const uint4 lo = lds128(src + get_k[h]), hi = lds128(src + get_k[h] + 8u * DP);
                 const uint32_t kl[4] = {lo.x, lo.y, lo.z, lo.w}, kh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -367,19 +404,24 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             float ks[2], vs[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t tok = (uint32_t)(g + 8 * e);
-                const float kv = lds32(src + Sl::kScales + tok * 4u), vv = lds32(src + Sl::kScales + 64u + tok * 4u);
-                const bool good = !(bad >> s & 1u) && vv <= 3.4028235e38f;
+                const float kv = lds32(src + Sl::kScales + (uint32_t)(g + 8 * e) * 4u);
+                const float vv = lds32(src + Sl::kScales + 64u + (uint32_t)(g + 8 * e) * 4u);
+                const bool good = vv <= 3.4028235e38f;
                 ks[e] = good ? kv * up : __int_as_float(0x7fffffff);
-                vs[e] = good && (int)tok >= from && (int)tok < to ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
+                vs[e] = good ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
             }
-            // scores in log2 units; those that the row does not see -inf
-            const bool whole = from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= a.sinks);
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] = x[n][e] * ks[e >> 1] * lack[n][e & 1];
-            if (!whole) {
+                for (int e = 0; e < 4; ++e) x[n][e] *= ks[e >> 1];
+            if (edge) {     // scores that the row does not see: -inf
+                int pos0, from, to;
+                bounds(i, pos0, from, to);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = g + 8 * e;
+                    if (tok < from || tok >= to || bad) vs[e] = 0.f;
+                }
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -388,35 +430,42 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                         const RowRange r = ranges[row];
                         bool sees = tok >= from && tok < to && pos < r.end && (pos >= r.low || pos < a.sinks);
                         if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
-                        if (!sees) x[n][e] = -INFINITY;
+                        x[n][e] = !sees ? -INFINITY : bad ? __int_as_float(0x7fffffff) : x[n][e];
                     }
             }
-            // softmax terms and what they weigh the values' codes with
+            // softmax terms and what they weigh the values' codes with; whether one of these, or a sum, passes its bound
             float p[N][4];
             uint32_t pk[N][2];
-            auto terms = [&]() {
-                bool past = false;
+            auto terms = [&](auto masked) {
+                uint32_t past = 0;
+                float most = 0.f;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    // (a score of -inf less a reference of -inf must not become NaN)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[n][e] = fast_exp2(x[n][e] - (x[n][e] == -INFINITY ? 0.f : ref[n][e & 1]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = fmaf(x[n][e], lack[n][e & 1], -ref[n][e & 1]);
+                        // (-inf less a reference of -inf must not become NaN)
+                        p[n][e] = fast_exp2(decltype(masked)::value && x[n][e] == -INFINITY ? -INFINITY : y);
+                    }
                     pk[n][0] = half_pair(p[n][0] * vs[0], p[n][1] * vs[0]);
                     pk[n][1] = half_pair(p[n][2] * vs[1], p[n][3] * vs[1]);
-                    const uint32_t most = __vmaxu2(pk[n][0], pk[n][1]);
-                    past |= max(most & 0xffffu, most >> 16) >= kPast || fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])) > kSumMost;
+                    past |= __vmaxu2(pk[n][0], pk[n][1]) + 0x04000400u;       // kPast and more: a half's top bit
+                    p[n][0] += p[n][2];
+                    p[n][1] += p[n][3];
+                    most = max3(most, p[n][0], p[n][1]);
                 }
-                return past;
+                static_assert(kPast + 0x0400u == 0x8000u, "");
+                return (past & 0x80008000u) || most > kSumMost;
             };
-            if (__any_sync(0xffffffffu, terms())) {
+            const bool past = edge ? terms(std::true_type{}) : terms(std::false_type{});
+            if (__any_sync(0xffffffffu, past)) {
                 // the references move to the chunk's largest terms, where these lie above
                 const float v0 = fmaxf(fast_log2(vs[0]), kVLeast), v1 = fmaxf(fast_log2(vs[1]), kVLeast);
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(x[n][e] + v0, x[n][e + 2] + v1);
+                        float top = fmaxf(x[n][e] * lack[n][e] + v0, x[n][e + 2] * lack[n][e] + v1);
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         if (top == -INFINITY || !(top > ref[n][e] + kPeak)) continue;
@@ -427,12 +476,12 @@ window_kernel(const __grid_constant__ WindowArgs w) {
 #pragma unroll
                         for (int k = 0; k < DP / 16; ++k) o[n][k][e] *= f, o[n][k][e + 2] *= f;
                     }
-                terms();
+                terms(std::true_type{});
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                l[n][0] += p[n][0] + p[n][2];
-                l[n][1] += p[n][1] + p[n][3];
+                l[n][0] += p[n][0];
+                l[n][1] += p[n][1];
                 pk[n][0] = transpose8x8(pk[n][0]);
                 pk[n][1] = transpose8x8(pk[n][1]);
             }
@@ -440,12 +489,12 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             uint32_t vw[4][DP / 32];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t tok = (uint32_t)(2 * t + (j & 1) + 8 * (j >> 1));
+                const uint32_t at = src + get_v[j & 1] + (uint32_t)(j >> 1) * 8u * DP;
                 if constexpr (DP == 128) {
-                    const uint4 u = lds128(src + Sl::kV + piece_at<DP>(tok, (uint32_t)g));
+                    const uint4 u = lds128(at);
                     vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = u.z, vw[j][3] = u.w;
                 } else {
-                    const uint2 u = lds64(src + Sl::kV + piece_at<DP>(tok, (uint32_t)g >> 1) + ((uint32_t)g & 1u) * 8u);
+                    const uint2 u = lds64(at);
                     vw[j][0] = u.x, vw[j][1] = u.y;
                 }
             }
@@ -458,7 +507,6 @@ window_kernel(const __grid_constant__ WindowArgs w) {
 #pragma unroll
                 for (int n = 0; n < N; ++n) mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][0], pk[n][1]);
             }
-            __syncwarp();
         }
         cp_async_wait<0>();
 
@@ -481,21 +529,25 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                     *reinterpret_cast<float4 *>(to + 2 * k) = make_float4(o[n][k][e], o[n][k][e + 2], o[n][k + 1][e], o[n][k + 1][e + 2]);
             }
         __syncthreads();
-        // the join of `count` parts of row r at dimensions d .. d + 3
-        auto join = [&](int count, auto stat, auto from_part, float4 &sum, float &top, float &total) {
+        // what a part's row counts in the join of `count` parts, whose references and sums `stat` gives
+        auto weigh = [&](int count, auto stat, float &top, float &total, auto put) {
             top = -INFINITY;
             for (int i = 0; i < count; ++i) top = fmaxf(top, stat(i).x);
             total = 0.f;
-            sum = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int i = 0; i < count; ++i) {
                 const float2 st = stat(i);
-                if (st.x == -INFINITY && st.y == 0.f) continue;       // saw nothing
-                const float f = scale_down(1.f, st.x - top);
-                total += scale_down(st.y, st.x - top);
-                const float4 x = from_part(i);
-                sum.x += x.x * f, sum.y += x.y * f, sum.z += x.z * f, sum.w += x.w * f;
+                const bool saw = !(st.x == -INFINITY && st.y == 0.f);
+                put(i, saw ? scale_down(1.f, st.x - top) : 0.f);
+                if (saw) total += scale_down(st.y, st.x - top);
             }
         };
+        if (threadIdx.x < kRows) {
+            const int r = threadIdx.x;
+            float top, total;
+            weigh(kWarps, [&](int k) { return stats[k][r]; }, top, total, [&](int k, float f) { weights[k][r] = f; });
+            stats[kWarps][r] = make_float2(top, total);
+        }
+        __syncthreads();
         auto result = [&](int r, int d, const float4 &sum, float top, float total) {
             const int m = m0 + r, blk = m / group;
             const int64_t place = (q.first + blk) * Hq + head * group + (m - blk * group);
@@ -504,29 +556,28 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 make_uint2(float_to_pair<T>(sum.x * inv, sum.y * inv), float_to_pair<T>(sum.z * inv, sum.w * inv));
             if (d == 0 && a.lse) a.lse[place] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
         };
+        auto add = [](float4 &sum, const float4 &x, float f) { sum.x += x.x * f, sum.y += x.y * f, sum.z += x.z * f, sum.w += x.w * f; };
         const int quarters = D / 4;
-        float4 sum;
-        float top, total;
         float *block_o = parts_o + kWarps * kRows * kPitch;
         for (int i = threadIdx.x; i < rows * quarters; i += kThreads) {
             const int r = i / quarters, d = (i - r * quarters) * 4;
-            join(kWarps, [&](int k) { return stats[k][r]; },
-                 [&](int k) { return *reinterpret_cast<const float4 *>(parts_o + (k * kRows + r) * kPitch + d); }, sum, top, total);
-            if (w.cluster == 1) {
-                result(r, d, sum, top, total);
-            } else {
-                *reinterpret_cast<float4 *>(block_o + r * kPitch + d) = sum;
-                if (d == 0) stats[kWarps][r] = make_float2(top, total);
-            }
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) add(sum, *reinterpret_cast<const float4 *>(parts_o + (k * kRows + r) * kPitch + d), weights[k][r]);
+            if (w.cluster == 1) result(r, d, sum, stats[kWarps][r].x, stats[kWarps][r].y);
+            else *reinterpret_cast<float4 *>(block_o + r * kPitch + d) = sum;
         }
         if (w.cluster > 1) {
             cg::cluster_group cluster = cg::this_cluster();
             cluster.sync();
             for (int i = split * kThreads + threadIdx.x; i < rows * quarters; i += w.cluster * kThreads) {
                 const int r = i / quarters, d = (i - r * quarters) * 4;
-                join(w.cluster, [&](int k) { return *cluster.map_shared_rank(&stats[kWarps][r], k); },
-                     [&](int k) { return *reinterpret_cast<const float4 *>(cluster.map_shared_rank(block_o, k) + r * kPitch + d); },
-                     sum, top, total);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                float top, total;
+                weigh(w.cluster, [&](int k) { return *cluster.map_shared_rank(&stats[kWarps][r], k); }, top, total,
+                      [&](int k, float f) {
+                          add(sum, *reinterpret_cast<const float4 *>(cluster.map_shared_rank(block_o, k) + r * kPitch + d), f);
+                      });
                 result(r, d, sum, top, total);
             }
             cluster.sync();     // before another block's memory goes, or is written again
@@ -581,7 +632,7 @@ cudaError_t launch_dp(WindowArgs &w, cudaStream_t s) {
     const int group = w.a.n_q_heads / w.a.cache.n_kv_heads;
     const int64_t rows = ((int64_t)w.a.rows.n_rows + w.a.rows.B - 1) / w.a.rows.B * group;
     if (rows <= 8) return launch_n<T, kFormat, DP, 1>(w, s);
-    if (rows <= 16) return launch_n<T, kFormat, DP, 2>(w, s);
+    if (rows <= 10) return launch_n<T, kFormat, DP, 2>(w, s);
     return launch_n<T, kFormat, DP, 3>(w, s);
 }
 
