@@ -48,9 +48,11 @@ namespace cg = cooperative_groups;
 using namespace tc;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kChunk = 16;          // tokens of a warp's step
+constexpr int kChunk = 16;          // tokens of a product
+constexpr int kPair = 1;            // chunks of a warp's step
 constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 constexpr int kMaxCluster = 8;
+constexpr float kUnset = -1e30f;    // the reference before the first token: below all that count
 
 struct WindowArgs {
     AttentionArgs a;
@@ -59,24 +61,28 @@ struct WindowArgs {
 };
 
 // N blocks of 8 rows a warp: blocks of 4 warps that an SM holds, and chunks of a warp under way
-template <int N>
+template <int DP, int N>
 struct Shape {
-    static constexpr int kBlocks = N == 1 ? 4 : N == 2 ? 3 : 2;
-    static constexpr int kStages = N == 1 ? 3 : 4;
+    static constexpr int kAcc = DP / 64 * N;       // sixteens of a lane's sums
+    static constexpr int kBlocks = kAcc <= 2 ? 4 : kAcc <= 4 ? 3 : 2;
+    static constexpr int kStages = 3;
 };
 template <int DP>
 struct Slot {
     static constexpr uint32_t kV = kChunk * DP, kScales = 2 * kChunk * DP, kBytes = kScales + 128;
+    static constexpr uint32_t kStep = kPair * kBytes;
 };
-template <int N, int DP>
-constexpr size_t smem_bytes() {
-    const size_t ring = (size_t)kWarps * Shape<N>::kStages * Slot<DP>::kBytes;
-    const size_t join = (size_t)(kWarps + 1) * 8 * N * (DP + 4) * 4;
-    return ring > join ? ring : join;
-}
+// Shared memory: the ring, in whose place the parts meet at the end; the queries
+template <int DP, int N>
+struct Smem {
+    static constexpr uint32_t kRing = kWarps * Shape<DP, N>::kStages * Slot<DP>::kStep;
+    static constexpr uint32_t kJoin = (kWarps + 1) * 8 * N * (DP + 4) * 4;
+    static constexpr uint32_t kQ = kRing > kJoin ? kRing : kJoin;
+    static constexpr uint32_t kBytes = kQ + N * (DP / 32) * 512;
+};
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -153,16 +159,17 @@ struct RowRange {
 };
 
 template <typename T, int kFormat, int DP, int N>
-__global__ void __launch_bounds__(kThreads, Shape<N>::kBlocks)
+__global__ void __launch_bounds__(kThreads, Shape<DP, N>::kBlocks)
 window_kernel(const __grid_constant__ WindowArgs w) {
     using Sl = Slot<DP>;
-    constexpr int kStages = Shape<N>::kStages, kRows = 8 * N, kSteps = DP / 16, kHalves = DP / 64;
+    constexpr int kStages = Shape<DP, N>::kStages, kRows = 8 * N, kHalves = DP / 64;
     constexpr int kCols = DP / 8;                 // dimensions of a lane's rows
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ RowRange ranges[kRows];
     __shared__ uint64_t words[kRows];
     __shared__ float2 stats[kWarps + 1][kRows];   // (r, l) of the warps, and of the block
     __shared__ float weights[kWarps][kRows];      // of the warps' parts in the block's
+    __shared__ float lacks[kRows];                // what the rows' queries lack
 
     const AttentionArgs &a = w.a;
     const dspark_kv_cache &c = a.cache;
@@ -177,9 +184,9 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     if (slot == 0 && head == 0 && split == 0 && threadIdx.x == 0 && (!q.rows_ok || (q.n > 0 && !q.len_ok)))
         atomicOr(c.flags, kFlagBadLength);
     const int m_all = q.n * group;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages) * Sl::kBytes;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages) * Sl::kStep;
     if (D != DP) {      // columns that no copy fills
-        for (uint32_t i = threadIdx.x; i < kWarps * kStages * Sl::kBytes / 16; i += kThreads)
+        for (uint32_t i = threadIdx.x; i < Smem<DP, N>::kRing / 16; i += kThreads)
             reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
@@ -217,6 +224,47 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             ranges[threadIdx.x] = r;
             words[threadIdx.x] = word;
         }
+        // ---- the queries, a block of 8 rows a warp: row g, dimensions 64 h + 16 t + 0 .. 15, in fp16 after a power of
+        // two; what lane (g, t) needs of them for two products lies together
+        for (int n = warp; n < N; n += kWarps) {
+            const int r = 8 * n + g, m = m0 + r, blk = m / group;
+            const T *src = static_cast<const T *>(a.q) + (q.first + blk) * a.q_stride + (int64_t)(head * group + (m - blk * group)) * D;
+            uint4 in[2 * kHalves];
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const int d = 64 * (i >> 1) + 16 * t + 8 * (i & 1);
+                in[i] = r < rows && d < D ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                // (two values a word: the 16-bit types' bits order like their values)
+                const uint32_t m2 = 0x7fff7fffu, u = __vmaxu2(__vmaxu2(in[i].x & m2, in[i].y & m2), __vmaxu2(in[i].z & m2, in[i].w & m2));
+                const float2 x = pair_to_float<T>(u);
+                top = max(top, max(__float_as_uint(x.x), __float_as_uint(x.y)));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e2 = max((int)(top >> 23) - 127, -110);
+            float mul = 1.f, f = 1.f;         // the largest element goes to [2^7, 2^8)
+            if (top >= 0x7f800000u) mul = __int_as_float(0x7fffffff);
+            else if (top != 0) {
+                mul = __uint_as_float((uint32_t)(127 + 7 - e2) << 23);
+                f = __uint_as_float((uint32_t)(127 - 7 + e2) << 23);
+            }
+            if (t == 0) lacks[r] = f;
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = pair_to_float<T>(u[e]);
+                    h[e] = half_pair(x.x * mul, x.y * mul);
+                }
+                reinterpret_cast<uint4 *>(smem + Smem<DP, N>::kQ)[(n * 2 * kHalves + i) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
         __syncthreads();
         if (tree) {
             low_min = low_max = ranges[0].low;
@@ -232,6 +280,10 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         const int per_page = c.page_size / kChunk;
         // the tokens of a chunk that some row may see: [from, to), and where it begins
         auto bounds = [&](int i, int &pos0, int &from, int &to) {
+            if (i >= mine) {
+                pos0 = from = to = 0;
+                return;
+            }
             bool own;
             const int chunk = chunks.at(part + i * parts, own);
             pos0 = chunk * kChunk + (own ? a.prefix_len : 0);
@@ -256,7 +308,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         };
         uint32_t places, edges, places_next = kNoChunk, edges_next = 0;
         look(lane, places, edges);
-        // Chunk i to the ring's place `to`; bits of the ring's places that hold an edge, and no page.
+        // bits of the ring's chunks that are an edge, and of those that have no page
         uint32_t slot_edge = 0, slot_bad = 0;
         constexpr int kPieces = DP / 16, kPer = 32 / kPieces;       // pieces of a token; tokens at once
         const int col = lane % kPieces, tok0 = lane / kPieces;
@@ -264,93 +316,47 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         const uint32_t put0 = piece_at<DP>((uint32_t)tok0, (uint32_t)col), put1 = piece_at<DP>((uint32_t)(tok0 + kPer), (uint32_t)col);
         const bool in_row = D == DP || col * 16 < D;
         const float *const scales = (lane < 4 ? c.k_scale : c.v_scale) + (lane & 3) * 4;
-        auto copy = [&](uint32_t dst, uint64_t place, auto width, auto there) {
+        auto copy = [&](uint32_t dst, uint64_t place, auto width) {
             const uint64_t at = place * (uint64_t)(kChunk * width) + (uint32_t)(tok0 * width + col * 16);
             const unsigned char *k = static_cast<const unsigned char *>(c.k) + at, *v = static_cast<const unsigned char *>(c.v) + at;
             if (in_row) {
 #pragma unroll
                 for (int j = 0; j < kChunk / kPer; ++j) {
                     const uint32_t to = dst + ((j & 1) ? put1 : put0) + (uint32_t)((j >> 1) * 2 * kPer * DP);
-                    cp_async16(to, k + j * kPer * width, there(tok0 + j * kPer));
-                    cp_async16(to + Sl::kV, v + j * kPer * width, there(tok0 + j * kPer));
+                    cp_async16(to, k + j * kPer * width);
+                    cp_async16(to + Sl::kV, v + j * kPer * width);
                 }
             }
-            if (lane < 8) cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, scales + place * kChunk, true);
+            if (lane < 8) cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, scales + place * kChunk);
         };
+        // step i: chunks 2 i and 2 i + 1; one behind the last is an edge of which nothing is there
+        const int steps = (mine + kPair - 1) / kPair;
         auto load = [&](int i, uint32_t s) {
-            if (i < mine) {
-                if ((i & 31) == 0) {
+            if (i < steps) {
+                if (i % (32 / kPair) == 0) {
                     if (i) places = places_next, edges = edges_next;
-                    if (i + 32 < mine) look(i + 32 + lane, places_next, edges_next);
+                    if (kPair * i + 32 < mine) look(kPair * i + 32 + lane, places_next, edges_next);
                 }
-                const uint32_t place = __shfl_sync(0xffffffffu, places, i & 31), dst = ring + s * Sl::kBytes, bit = 1u << s;
-                slot_edge &= ~bit, slot_bad &= ~bit;
-                if (place < kBadChunk && !(edges >> (i & 31) & 1u)) {
-                    auto all = [](int) { return true; };
-                    if (D == DP) copy(dst, place, std::integral_constant<int, DP>{}, all);
-                    else copy(dst, place, D, all);
-                } else {
-                    const bool good = place < kBadChunk;
-                    slot_edge |= bit;
-                    if (!good) {
+                slot_edge &= ~(3u << (2 * s)), slot_bad &= ~(3u << (2 * s));
+#pragma unroll
+                for (int u = 0; u < kPair; ++u) {
+                    const int at = kPair * i + u;
+                    const uint32_t place = __shfl_sync(0xffffffffu, places, at & 31), bit = 1u << (2 * s + u);
+                    const uint32_t dst = ring + s * Sl::kStep + (uint32_t)u * Sl::kBytes;
+                    if (edges >> (at & 31) & 1u || place >= kBadChunk) slot_edge |= bit;
+                    if (place < kBadChunk) {
+                        if (D == DP) copy(dst, place, std::integral_constant<int, DP>{});
+                        else copy(dst, place, D);
+                    } else if (place == kBadChunk) {
                         slot_bad |= bit;
                         if (lane == 0) atomicOr(c.flags, kFlagBadPage);
                     }
-                    int pos0, from, to;
-                    bounds(i, pos0, from, to);
-                    copy(dst, good ? place : 0, D, [&](int tok) { return good && tok >= from && tok < to; });
                 }
             }
             cp_async_commit();
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i, (uint32_t)i);
-
-        // ---- the queries: block n's row g, dimensions 64 h + 16 t + 0 .. 15, in fp16 after a power of two
-        uint32_t qf[N][kSteps][2];
-        float lack[N][2];                     // what rows 2 t and 2 t + 1 of block n lack
-        const float up = a.scale * kLog2e;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int r = 8 * n + g, m = m0 + r, blk = m / group;
-            const T *src = static_cast<const T *>(a.q) + (q.first + blk) * a.q_stride + (int64_t)(head * group + (m - blk * group)) * D;
-            uint4 in[2 * kHalves];
-#pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const int d = 64 * (i >> 1) + 16 * t + 8 * (i & 1);
-                in[i] = r < rows && d < D ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
-            }
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 x = pair_to_float<T>(u[e]);
-                    top = max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
-                }
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e2 = max((int)(top >> 23) - 127, -110);
-            float mul = 1.f, f = 1.f;         // the largest element goes to [2^7, 2^8)
-            if (top >= 0x7f800000u) mul = __int_as_float(0x7fffffff);
-            else if (top != 0) {
-                mul = __uint_as_float((uint32_t)(127 + 7 - e2) << 23);
-                f = __uint_as_float((uint32_t)(127 - 7 + e2) << 23);
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 x = pair_to_float<T>(u[e]);
-                    qf[n][2 * i + (e >> 1)][e & 1] = half_pair(x.x * mul, x.y * mul);
-                }
-            }
-            lack[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);        // rows' lanes: (2 t) * 4
-            lack[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-        }
 
         // ---- the loop over chunks
         float o[N][DP / 16][4];
@@ -359,7 +365,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-            ref[n][0] = ref[n][1] = -INFINITY;
+            ref[n][0] = ref[n][1] = kUnset;
             l[n][0] = l[n][1] = 0.f;
         }
         // places in a chunk of what the lane reads: keys of tokens g and g + 8 (8 lines on), its pieces 64 dimensions
@@ -371,143 +377,209 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         for (int j = 0; j < 2; ++j)
             get_v[j] = Sl::kV + (DP == 128 ? piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g)
                                            : piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g >> 1) + ((uint32_t)g & 1u) * 8u);
-        uint32_t s = 0, s_load = kStages - 1;
+        const float up = a.scale * kLog2e;
+        const uint32_t q_at = smem_u32(smem) + Smem<DP, N>::kQ + (uint32_t)lane * 16u;
+        float lack[N][2];                     // of rows 2 t and 2 t + 1 of each block
+#pragma unroll
+        for (int n = 0; n < N; ++n) lack[n][0] = lacks[8 * n + 2 * t], lack[n][1] = lacks[8 * n + 2 * t + 1];
+        // (of the N blocks of rows the first M exist)
+        auto walk = [&](auto blocks) {
+            constexpr int M = decltype(blocks)::value;
+            uint32_t s = 0, s_load = kStages - 1;
 #pragma unroll 1
-        for (int i = 0; i < mine; ++i) {
-            cp_async_wait<kStages - 2>();
-            __syncwarp();
-            load(i + kStages - 1, s_load);    // to the place that the chunk before has left
-            const uint32_t src = ring + s * Sl::kBytes;
-            const bool edge = slot_edge >> s & 1u, bad = slot_bad >> s & 1u;
-            s = s + 1 == kStages ? 0 : s + 1;
-            s_load = s_load + 1 == kStages ? 0 : s_load + 1;
-            // scores
-            float x[N][4];
+            for (int i = 0; i < steps; ++i) {
+                cp_async_wait<kStages - 2>();
+                __syncwarp();
+                load(i + kStages - 1, s_load);    // to the place that the step before has left
+                const uint32_t src = ring + s * Sl::kStep;
+                const uint32_t edge = slot_edge >> (2 * s) & 3u, bad = slot_bad >> (2 * s) & 3u;
+                s = s + 1 == kStages ? 0 : s + 1;
+                s_load = s_load + 1 == kStages ? 0 : s_load + 1;
+                // scores
+                float x[M][kPair][4];
 #pragma unroll
-            for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+                for (int n = 0; n < M; ++n)
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                const uint4 lo = lds128(src + get_k[h]), hi = lds128(src + get_k[h] + 8u * DP);
-                const uint32_t kl[4] = {lo.x, lo.y, lo.z, lo.w}, kh[4] = {hi.x, hi.y, hi.z, hi.w};
+                    for (int u = 0; u < kPair; ++u) x[n][u][0] = x[n][u][1] = x[n][u][2] = x[n][u][3] = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    __half2 l0, l1, h0, h1;
-                    decode4<kFormat>(kl[k], l0, l1);
-                    decode4<kFormat>(kh[k], h0, h1);
+                for (int h = 0; h < kHalves; ++h) {
+                    uint32_t kw[kPair][2][4];
 #pragma unroll
-                    for (int n = 0; n < N; ++n)
-                        mma16816(x[n], as_u32(l0), as_u32(h0), as_u32(l1), as_u32(h1), qf[n][4 * h + k][0], qf[n][4 * h + k][1]);
-                }
-            }
-            // scales of tokens g and g + 8; one whose value scale (or page) is no number carries its NaN in the
-            // key's alone: where it is masked, its zero weight must not become 0 times NaN
-            float ks[2], vs[2];
+                    for (int u = 0; u < kPair; ++u)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float kv = lds32(src + Sl::kScales + (uint32_t)(g + 8 * e) * 4u);
-                const float vv = lds32(src + Sl::kScales + 64u + (uint32_t)(g + 8 * e) * 4u);
-                const bool good = vv <= 3.4028235e38f;
-                ks[e] = good ? kv * up : __int_as_float(0x7fffffff);
-                vs[e] = good ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
-            }
+                        for (int e = 0; e < 2; ++e) {
+                            const uint4 v = lds128(src + get_k[h] + (uint32_t)u * Sl::kBytes + (uint32_t)e * 8u * DP);
+                            kw[u][e][0] = v.x, kw[u][e][1] = v.y, kw[u][e][2] = v.z, kw[u][e][3] = v.w;
+                        }
 #pragma unroll
-            for (int n = 0; n < N; ++n)
+                    for (int k = 0; k < 4; k += 2) {
+                        __half2 f[kPair][2][2][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] *= ks[e >> 1];
-            if (edge) {     // scores that the row does not see: -inf
-                int pos0, from, to;
-                bounds(i, pos0, from, to);
+                        for (int u = 0; u < kPair; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = g + 8 * e;
-                    if (tok < from || tok >= to || bad) vs[e] = 0.f;
-                }
+                            for (int e = 0; e < 2; ++e) {
+                                decode4<kFormat>(kw[u][e][k], f[u][0][e][0], f[u][0][e][1]);
+                                decode4<kFormat>(kw[u][e][k + 1], f[u][1][e][0], f[u][1][e][1]);
+                            }
 #pragma unroll
-                for (int n = 0; n < N; ++n)
+                        for (int n = 0; n < M; ++n) {
+                            const uint4 v = lds128(q_at + (uint32_t)((n * 2 * kHalves + 2 * h + (k >> 1)) * 512));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 8 * n + 2 * t + (e & 1), tok = g + 8 * (e >> 1), pos = pos0 + tok;
-                        const RowRange r = ranges[row];
-                        bool sees = tok >= from && tok < to && pos < r.end && (pos >= r.low || pos < a.sinks);
-                        if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
-                        x[n][e] = !sees ? -INFINITY : bad ? __int_as_float(0x7fffffff) : x[n][e];
+                            for (int u = 0; u < kPair; ++u)
+                                mma16816(x[n][u], as_u32(f[u][0][0][0]), as_u32(f[u][0][1][0]), as_u32(f[u][0][0][1]),
+                                         as_u32(f[u][0][1][1]), v.x, v.y);
+#pragma unroll
+                            for (int u = 0; u < kPair; ++u)
+                                mma16816(x[n][u], as_u32(f[u][1][0][0]), as_u32(f[u][1][1][0]), as_u32(f[u][1][0][1]),
+                                         as_u32(f[u][1][1][1]), v.z, v.w);
+                        }
                     }
-            }
-            // softmax terms and what they weigh the values' codes with; whether one of these, or a sum, passes its bound
-            float p[N][4];
-            uint32_t pk[N][2];
-            auto terms = [&](auto masked) {
-                uint32_t past = 0;
-                float most = 0.f;
-#pragma unroll
-                for (int n = 0; n < N; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = fmaf(x[n][e], lack[n][e & 1], -ref[n][e & 1]);
-                        // (-inf less a reference of -inf must not become NaN)
-                        p[n][e] = fast_exp2(decltype(masked)::value && x[n][e] == -INFINITY ? -INFINITY : y);
-                    }
-                    pk[n][0] = half_pair(p[n][0] * vs[0], p[n][1] * vs[0]);
-                    pk[n][1] = half_pair(p[n][2] * vs[1], p[n][3] * vs[1]);
-                    past |= __vmaxu2(pk[n][0], pk[n][1]) + 0x04000400u;       // kPast and more: a half's top bit
-                    p[n][0] += p[n][2];
-                    p[n][1] += p[n][3];
-                    most = max3(most, p[n][0], p[n][1]);
                 }
-                static_assert(kPast + 0x0400u == 0x8000u, "");
-                return (past & 0x80008000u) || most > kSumMost;
-            };
-            const bool past = edge ? terms(std::true_type{}) : terms(std::false_type{});
-            if (__any_sync(0xffffffffu, past)) {
-                // the references move to the chunk's largest terms, where these lie above
-                const float v0 = fmaxf(fast_log2(vs[0]), kVLeast), v1 = fmaxf(fast_log2(vs[1]), kVLeast);
+                // scales of tokens g and g + 8; one whose value scale (or page) is no number carries its NaN in the
+                // key's alone: where it is masked, its zero weight must not become 0 times NaN
+                float vs[kPair][2];
 #pragma unroll
-                for (int n = 0; n < N; ++n)
+                for (int u = 0; u < kPair; ++u)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(x[n][e] * lack[n][e] + v0, x[n][e + 2] * lack[n][e] + v1);
+                        const uint32_t at = src + (uint32_t)u * Sl::kBytes + Sl::kScales + (uint32_t)(g + 8 * e) * 4u;
+                        const float kv = lds32(at), vv = lds32(at + 64u);
+                        const bool good = vv <= 3.4028235e38f;
+                        const float ks = good ? kv * up : __int_as_float(0x7fffffff);
+                        vs[u][e] = good ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
 #pragma unroll
-                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        if (top == -INFINITY || !(top > ref[n][e] + kPeak)) continue;
-                        const float r = ceilf(top) - kPeak;           // P <= 2^7
-                        const float f = scale_down(1.f, ref[n][e] - r);
-                        l[n][e] = scale_down(l[n][e], ref[n][e] - r);
-                        ref[n][e] = r;
-#pragma unroll
-                        for (int k = 0; k < DP / 16; ++k) o[n][k][e] *= f, o[n][k][e + 2] *= f;
+                        for (int n = 0; n < M; ++n) x[n][u][2 * e] *= ks, x[n][u][2 * e + 1] *= ks;
                     }
-                terms(std::true_type{});
-            }
+                if (edge) {     // scores that the row does not see: -inf
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                l[n][0] += p[n][0];
-                l[n][1] += p[n][1];
-                pk[n][0] = transpose8x8(pk[n][0]);
-                pk[n][1] = transpose8x8(pk[n][1]);
-            }
-            // outputs
-            uint32_t vw[4][DP / 32];
+                    for (int u = 0; u < kPair; ++u) {
+                        int pos0, from, to;
+                        bounds(kPair * i + u, pos0, from, to);
+                        if (bad >> u & 1u) to = 0;
+                        // what lies where no token is must not meet a weight of 0
+#pragma unroll 1
+                        for (int j = 0; j < kChunk; j += kPer) {
+                            if (tok0 + j < from || tok0 + j >= to)
+                                st_shared_v4(src + (uint32_t)u * Sl::kBytes + Sl::kV + piece_at<DP>((uint32_t)(tok0 + j), (uint32_t)col),
+                                             make_uint4(0, 0, 0, 0));
+                        }
+                        __syncwarp();
+                        if (bad >> u & 1u) bounds(kPair * i + u, pos0, from, to);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = src + get_v[j & 1] + (uint32_t)(j >> 1) * 8u * DP;
-                if constexpr (DP == 128) {
-                    const uint4 u = lds128(at);
-                    vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = u.z, vw[j][3] = u.w;
-                } else {
-                    const uint2 u = lds64(at);
-                    vw[j][0] = u.x, vw[j][1] = u.y;
+                        for (int e = 0; e < 2; ++e) {
+                            const int tok = g + 8 * e, pos = pos0 + tok;
+                            const bool there = tok >= from && tok < to;
+                            if (!there || (bad >> u & 1u)) vs[u][e] = 0.f;
+#pragma unroll
+                            for (int n = 0; n < M; ++n)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f) {
+                                    const int row = 8 * n + 2 * t + f;
+                                    const RowRange r = ranges[row];
+                                    bool sees = there && pos < r.end && (pos >= r.low || pos < a.sinks);
+                                    if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
+                                    float &y = x[n][u][2 * e + f];
+                                    y = !sees ? -INFINITY : (bad >> u & 1u) ? __int_as_float(0x7fffffff) : y;
+                                }
+                        }
+                    }
+                }
+                // softmax terms and what they weigh the values' codes with; whether one of these, or a sum, passes its
+                // bound
+                uint32_t pk[M][kPair][2];
+                float sum[M][2];
+                auto terms = [&]() {
+                    uint32_t past = 0;
+                    float most = 0.f;
+#pragma unroll
+                    for (int n = 0; n < M; ++n) {
+                        sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+                        for (int u = 0; u < kPair; ++u) {
+                            float p[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(x[n][u][e], lack[n][e & 1], -ref[n][e & 1]));
+                            pk[n][u][0] = half_pair(p[0] * vs[u][0], p[1] * vs[u][0]);
+                            pk[n][u][1] = half_pair(p[2] * vs[u][1], p[3] * vs[u][1]);
+                            past |= __vmaxu2(pk[n][u][0], pk[n][u][1]) + 0x04000400u;       // kPast and more: a half's top bit
+                            sum[n][0] += p[0] + p[2];
+                            sum[n][1] += p[1] + p[3];
+                        }
+                        most = max3(most, sum[n][0], sum[n][1]);
+                    }
+                    static_assert(kPast + 0x0400u == 0x8000u, "");
+                    return (past & 0x80008000u) || most > kSumMost;
+                };
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    const bool past = terms();
+                    if (again || !__any_sync(0xffffffffu, past)) break;
+                    // the references move to the step's largest terms, where these lie above
+                    float lv[kPair][2];
+#pragma unroll
+                    for (int u = 0; u < kPair; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) lv[u][e] = fmaxf(fast_log2(vs[u][e]), kVLeast);
+#pragma unroll
+                    for (int n = 0; n < M; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int u = 0; u < kPair; ++u)
+                                top = max3(top, x[n][u][e] * lack[n][e] + lv[u][0], x[n][u][e + 2] * lack[n][e] + lv[u][1]);
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            if (top == -INFINITY || !(top > ref[n][e] + kPeak)) continue;
+                            const float r = ceilf(top) - kPeak;           // P <= 2^7
+                            const float f = scale_down(1.f, ref[n][e] - r);
+                            l[n][e] = scale_down(l[n][e], ref[n][e] - r);
+                            ref[n][e] = r;
+#pragma unroll
+                            for (int k = 0; k < DP / 16; ++k) o[n][k][e] *= f, o[n][k][e + 2] *= f;
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < M; ++n) {
+                    l[n][0] += sum[n][0];
+                    l[n][1] += sum[n][1];
+#pragma unroll
+                    for (int u = 0; u < kPair; ++u) {
+                        pk[n][u][0] = transpose8x8(pk[n][u][0]);
+                        pk[n][u][1] = transpose8x8(pk[n][u][1]);
+                    }
+                }
+                // outputs
+#pragma unroll
+                for (int u = 0; u < kPair; ++u) {
+                    uint32_t vw[4][DP / 32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t at = src + get_v[j & 1] + (uint32_t)u * Sl::kBytes + (uint32_t)(j >> 1) * 8u * DP;
+                        if constexpr (DP == 128) {
+                            const uint4 v = lds128(at);
+                            vw[j][0] = v.x, vw[j][1] = v.y, vw[j][2] = v.z, vw[j][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(at);
+                            vw[j][0] = v.x, vw[j][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t pick = (k & 1) ? 0x7362u : 0x5140u;
+                        __half2 a0, a1, a2, a3;
+                        decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
+                        decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
+#pragma unroll
+                        for (int n = 0; n < M; ++n)
+                            mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][u][0], pk[n][u][1]);
+                    }
                 }
             }
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                const uint32_t pick = (k & 1) ? 0x7362u : 0x5140u;
-                __half2 a0, a1, a2, a3;
-                decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
-                decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
-#pragma unroll
-                for (int n = 0; n < N; ++n) mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][0], pk[n][1]);
-            }
-        }
+        };
+        if (N >= 3 && rows <= kRows / 3) walk(std::integral_constant<int, (N + 2) / 3>{});
+        else if (N >= 2 && rows <= (N == 2 ? 8 : kRows / 3 * 2)) walk(std::integral_constant<int, N == 2 ? 1 : (2 * N + 2) / 3>{});
+        else walk(std::integral_constant<int, N>{});
         cp_async_wait<0>();
 
         // ---- the warps' parts join: [warp][row][dimension], the rows 4 floats apart from a power of two
@@ -531,14 +603,13 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         __syncthreads();
         // what a part's row counts in the join of `count` parts, whose references and sums `stat` gives
         auto weigh = [&](int count, auto stat, float &top, float &total, auto put) {
-            top = -INFINITY;
+            top = kUnset;
             for (int i = 0; i < count; ++i) top = fmaxf(top, stat(i).x);
             total = 0.f;
             for (int i = 0; i < count; ++i) {
                 const float2 st = stat(i);
-                const bool saw = !(st.x == -INFINITY && st.y == 0.f);
-                put(i, saw ? scale_down(1.f, st.x - top) : 0.f);
-                if (saw) total += scale_down(st.y, st.x - top);
+                put(i, scale_down(1.f, st.x - top));
+                total += scale_down(st.y, st.x - top);
             }
         };
         if (threadIdx.x < kRows) {
@@ -584,7 +655,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         }
         __syncthreads();        // the ring is the next rows'
         if (D != DP) {
-            for (uint32_t i = threadIdx.x; i < kWarps * kStages * Sl::kBytes / 16; i += kThreads)
+            for (uint32_t i = threadIdx.x; i < Smem<DP, N>::kRing / 16; i += kThreads)
                 reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
@@ -595,7 +666,7 @@ template <typename T, int kFormat, int DP, int N>
 cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     static PerDeviceOnce once;
     auto *kernel = window_kernel<T, kFormat, DP, N>;
-    constexpr size_t bytes = smem_bytes<N, DP>();
+    constexpr size_t bytes = Smem<DP, N>::kBytes;
     cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
     if (e != cudaSuccess) return e;
     const AttentionArgs &a = w.a;
@@ -609,7 +680,7 @@ cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)a.window + a.sinks;
     const int64_t chunks = (own < seen ? own : seen) / kChunk;
     w.cluster = 1;
-    while (w.cluster < kMaxCluster && blocks * w.cluster < (int64_t)kNumSMs * Shape<N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
+    while (w.cluster < kMaxCluster && blocks * w.cluster < (int64_t)kNumSMs * Shape<DP, N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
         w.cluster *= 2;
     blocks *= w.cluster;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
