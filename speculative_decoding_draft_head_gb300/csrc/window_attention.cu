@@ -48,14 +48,30 @@ namespace cg = cooperative_groups;
 using namespace tc;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kChunk = 16;          // tokens of a product
-constexpr int kPair = 1;            // chunks of a warp's step
+constexpr int kChunk = 16;          // tokens of a warp's step
 constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 constexpr int kMaxCluster = 8;
 constexpr float kUnset = -1e30f;    // the reference before the first token: below all that count
 
+// Division of numbers below 2^31 by a fixed one: x / d = (2 x m / 2^32) / 2^s with s = ceil(log2 d),
+// m = ceil(2^(31 + s) / d).
+struct Divider {
+    uint32_t d, m, s;
+    explicit Divider(int by = 1) : d((uint32_t)by), s(0) {
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int div(int x) const { return (int)(__umulhi(2u * (uint32_t)x, m) >> s); }
+    __device__ __forceinline__ int div(int x, int &rest) const {
+        const int y = div(x);
+        rest = x - y * (int)d;
+        return y;
+    }
+};
+
 struct WindowArgs {
     AttentionArgs a;
+    Divider by_cluster, by_slots, by_heads, by_group, by_page;      // the last: chunks a page
     int slots;          // row blocks of a request that have blocks of their own; more follow in a loop
     int cluster;        // blocks an item's tokens are split over
 };
@@ -64,25 +80,26 @@ struct WindowArgs {
 template <int DP, int N>
 struct Shape {
     static constexpr int kAcc = DP / 64 * N;       // sixteens of a lane's sums
-    static constexpr int kBlocks = kAcc <= 2 ? 4 : kAcc <= 4 ? 3 : 2;
+    static constexpr int kBlocks = kAcc <= 2 ? 4 : kAcc <= 4 ? 4 : 3;
     static constexpr int kStages = 3;
 };
 template <int DP>
 struct Slot {
     static constexpr uint32_t kV = kChunk * DP, kScales = 2 * kChunk * DP, kBytes = kScales + 128;
-    static constexpr uint32_t kStep = kPair * kBytes;
 };
 // Shared memory: the ring, in whose place the parts meet at the end; the queries
 template <int DP, int N>
 struct Smem {
-    static constexpr uint32_t kRing = kWarps * Shape<DP, N>::kStages * Slot<DP>::kStep;
+    static constexpr uint32_t kRing = kWarps * Shape<DP, N>::kStages * Slot<DP>::kBytes;
     static constexpr uint32_t kJoin = (kWarps + 1) * 8 * N * (DP + 4) * 4;
     static constexpr uint32_t kQ = kRing > kJoin ? kRing : kJoin;
     static constexpr uint32_t kBytes = kQ + N * (DP / 32) * 512;
 };
 
+// (offsets that are known go into the instruction)
+template <uint32_t kDst, uint32_t kSrc>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -103,20 +120,32 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+template <uint32_t kAt = 0>
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(kAt));
     return v;
 }
+template <uint32_t kAt = 0>
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
     uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(v.x), "=r"(v.y) : "r"(at), "n"(kAt));
     return v;
 }
+template <uint32_t kAt = 0>
 __device__ __forceinline__ float lds32(uint32_t at) {
     float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    asm volatile("ld.shared.f32 %0, [%1 + %2];" : "=f"(v) : "r"(at), "n"(kAt));
     return v;
+}
+
+// Calls f with the numbers 0 .. n - 1 as constants.
+template <int n, int i = 0, typename F>
+__device__ __forceinline__ void each(F &&f) {
+    if constexpr (i < n) {
+        f(std::integral_constant<int, i>{});
+        each<n, i + 1>(f);
+    }
 }
 
 // Where 16-byte piece `c` of token `tok` is in a chunk.  DP = 128: a token a line of 128
@@ -157,6 +186,15 @@ struct Chunks {
 struct RowRange {
     int low, end;
 };
+// An item as a warp sees it.  In shared memory, as the loop over chunks needs every register.
+struct View {
+    Chunks chunks;
+    int low_min, low_max, end_min, end_max;     // of the rows' ranges
+    int ctx;                                    // tokens before the block
+    int m0, rows;                               // the item's rows: their first of the request's head's, how many
+    int n, b, head;
+    int64_t first;                              // packed row of the request's first
+};
 
 template <typename T, int kFormat, int DP, int N>
 __global__ void __launch_bounds__(kThreads, Shape<DP, N>::kBlocks)
@@ -164,76 +202,168 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     using Sl = Slot<DP>;
     constexpr int kStages = Shape<DP, N>::kStages, kRows = 8 * N, kHalves = DP / 64;
     constexpr int kCols = DP / 8;                 // dimensions of a lane's rows
+    constexpr int kPieces = DP / 16, kPer = 32 / kPieces;   // pieces of a token; tokens a copy takes at once
     extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ View views[kWarps];
     __shared__ RowRange ranges[kRows];
     __shared__ uint64_t words[kRows];
     __shared__ float2 stats[kWarps + 1][kRows];   // (r, l) of the warps, and of the block
     __shared__ float weights[kWarps][kRows];      // of the warps' parts in the block's
     __shared__ float lacks[kRows];                // what the rows' queries lack
+    __shared__ int64_t row_place[kRows];             // of the rows' results, in heads
 
     const AttentionArgs &a = w.a;
     const dspark_kv_cache &c = a.cache;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int D = c.head_dim, Hq = a.n_q_heads, H = c.n_kv_heads, group = Hq / H;
-    const int split = blockIdx.x % w.cluster;
-    int item = blockIdx.x / w.cluster;
-    const int slot = item % w.slots;
-    item /= w.slots;
-    const int head = item % H, b = item / H;
-    const Request q = load_request(a, b);
-    if (slot == 0 && head == 0 && split == 0 && threadIdx.x == 0 && (!q.rows_ok || (q.n > 0 && !q.len_ok)))
-        atomicOr(c.flags, kFlagBadLength);
-    const int m_all = q.n * group;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages) * Sl::kStep;
+    const int D = c.head_dim, H = c.n_kv_heads, group = a.n_q_heads / H;
+    int split;
+    int item = w.by_cluster.div((int)blockIdx.x, split);
+    const int parts = w.cluster * kWarps, part = split * kWarps + warp;     // the warp takes every parts-th chunk
+    const bool tree = a.row_mask != nullptr, causal = !tree && a.mask == DSPARK_MASK_CAUSAL;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages) * Sl::kBytes;
+    View &view = views[warp];
+    int m0;
+    {
+        int slot, head;
+        item = w.by_slots.div(item, slot);
+        const int b = w.by_heads.div(item, head);
+        const Request q = load_request(a, b);
+        if (lane == 0) view.b = b, view.head = head, view.first = q.first, view.n = q.n;
+        m0 = slot * kRows;
+        if (!q.rows_ok || (q.n > 0 && !q.len_ok)) {     // no rows, or rows of NaN
+            if (slot == 0 && head == 0 && split == 0 && threadIdx.x == 0) atomicOr(c.flags, kFlagBadLength);
+            if (slot == 0 && split == 0)
+                for (int i = threadIdx.x; i < q.n * group * (D / 8); i += kThreads) {
+                    const int m = i / (D / 8), blk = m / group;
+                    const int64_t place = (q.first + blk) * a.n_q_heads + head * group + (m - blk * group);
+                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + place * D)[i - m * (D / 8)] =
+                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    if (i == m * (D / 8) && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+                }
+            return;
+        }
+        if (lane == 0) view.ctx = a.prefix_len + q.len - q.n;
+    }
     if (D != DP) {      // columns that no copy fills
         for (uint32_t i = threadIdx.x; i < Smem<DP, N>::kRing / 16; i += kThreads)
             reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
+    __syncwarp();
 
-    for (int m0 = slot * kRows; m0 < m_all; m0 += w.slots * kRows) {
-        const int rows = min(kRows, m_all - m0);
-        if (!q.len_ok) {
-            if (split == 0)
-                for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
-                    const int r = i / (D / 8), m = m0 + r, blk = m / group;
-                    const int64_t place = (q.first + blk) * Hq + head * group + (m - blk * group);
-                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + place * D)[i - r * (D / 8)] =
-                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    if (i == r * (D / 8) && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
-                }
-            continue;
-        }
-        // ---- what the rows see
-        const int ctx = a.prefix_len + q.len - q.n;       // tokens before the block
-        const int b0 = m0 / group, b1 = (m0 + rows - 1) / group;
-        const bool tree = a.row_mask != nullptr, causal = !tree && a.mask == DSPARK_MASK_CAUSAL;
-        int low_min = max(ctx + b0 - a.window + 1, 0), low_max = max(ctx + b1 - a.window + 1, 0);
-        const int end_min = causal ? ctx + b0 + 1 : tree ? ctx : ctx + q.n;
-        const int end_max = causal ? ctx + b1 + 1 : ctx + q.n;
-        __syncthreads();
-        if (threadIdx.x < kRows) {
-            const int m = m0 + min((int)threadIdx.x, rows - 1), blk = m / group;
-            RowRange r{max(ctx + blk - a.window + 1, 0), causal ? ctx + blk + 1 : ctx + q.n};
+#pragma unroll 1
+    while (m0 < view.n * group) {
+        // ---- what the rows see, a lane each
+        int mine;
+        {
+            const int n = view.n, ctx = view.ctx, rows = min(kRows, n * group - m0);
+            const int blk = w.by_group.div(m0 + min(lane, rows - 1));
+            RowRange r{max(ctx + blk - a.window + 1, 0), causal ? ctx + blk + 1 : ctx + n};
             uint64_t word = 0;
             if (tree) {
-                word = a.row_mask[q.first + blk];
-                if (q.n < 64) word &= (1ull << q.n) - 1;
+                word = a.row_mask[view.first + blk];
+                if (n < 64) word &= (1ull << n) - 1;
                 r.low = max(ctx - max(a.window - __popcll(word), 0), 0);
             }
-            ranges[threadIdx.x] = r;
-            words[threadIdx.x] = word;
+            if (warp == 0 && lane < kRows) ranges[lane] = r, words[lane] = word;
+            const int low_min = __reduce_min_sync(0xffffffffu, r.low), low_max = __reduce_max_sync(0xffffffffu, r.low);
+            const int end_min = tree ? ctx : __reduce_min_sync(0xffffffffu, r.end), end_max = __reduce_max_sync(0xffffffffu, r.end);
+            Chunks chunks;
+            chunks.find(a.prefix_len, a.sinks, low_min, end_max);
+            mine = chunks.total > part ? (chunks.total - part + parts - 1) / parts : 0;
+            if (lane == 0) {
+                view.chunks = chunks;
+                view.low_min = low_min, view.low_max = low_max, view.end_min = end_min, view.end_max = end_max;
+                view.m0 = m0, view.rows = rows;
+            }
+            __syncwarp();
         }
+        // ---- the warp's chunks: the tokens of chunk i that some row may see, [from, to), and where it begins
+        auto bounds = [&](int i, int &pos0, int &from, int &to) {
+            bool own;
+            const int chunk = view.chunks.at(part + i * parts, own);
+            pos0 = chunk * kChunk + (own ? a.prefix_len : 0);
+            to = min(own ? view.end_max : min(a.prefix_len, view.end_max), pos0 + kChunk) - pos0;
+            from = pos0 < a.sinks ? 0 : max(view.low_min - pos0, 0);
+        };
+        // Chunk i's number in the cache, in 16 head rows; bits (of the lanes' chunks) of those that some row sees only
+        // in part or not at all.
+        auto look = [&](int i, uint32_t &place, uint32_t &edges) {
+            place = kNoChunk;
+            bool edge = false;
+            if (i < mine) {
+                bool own;
+                int in_page;
+                const int chunk = view.chunks.at(part + i * parts, own), page_slot = w.by_page.div(chunk, in_page);
+                const int page = own ? a.rows.block_table[(int64_t)view.b * a.rows.max_pages + page_slot] : a.prefix_pages[page_slot];
+                place = page < 0 || page >= c.n_pages ? kBadChunk
+                                                      : ((uint32_t)page * (uint32_t)H + (uint32_t)view.head) * w.by_page.d + (uint32_t)in_page;
+                int pos0, from, to;
+                bounds(i, pos0, from, to);
+                edge = !(from == 0 && to == kChunk && pos0 + kChunk <= view.end_min &&
+                         (pos0 >= view.low_max || pos0 + kChunk <= a.sinks));
+            }
+            edges = __ballot_sync(0xffffffffu, edge);
+        };
+        uint32_t places, edges, places_next = kNoChunk, edges_next = 0;    // of 32 chunks, a lane each, and of the next 32
+        look(lane, places, edges);
+        uint32_t slot_edge = 0, slot_bad = 0;   // bits of the ring's chunks that are an edge, and of those that have no page
+        const int col = lane % kPieces, tok0 = lane / kPieces;
+        // (the permutation repeats every 8 tokens: tokens tok0 + 4 j at DP = 128 have two, tok0 + 8 j at 64 one)
+        const uint32_t put0 = piece_at<DP>((uint32_t)tok0, (uint32_t)col), put1 = piece_at<DP>((uint32_t)(tok0 + kPer), (uint32_t)col);
+        const float *const scales = (lane < 4 ? c.k_scale : c.v_scale) + (lane & 3) * 4;
+        auto copy = [&](uint32_t dst, uint64_t place, auto width) {
+            const uint64_t at = place * (uint64_t)(kChunk * width) + (uint32_t)(tok0 * width + col * 16);
+            const unsigned char *k = static_cast<const unsigned char *>(c.k) + at, *v = static_cast<const unsigned char *>(c.v) + at;
+            if (lane < 8) cp_async16<Sl::kScales, 0>(dst + (uint32_t)lane * 16u, scales + place * kChunk);
+            if (D != DP && col * 16 >= D) return;
+            const uint32_t to0 = dst + put0, to1 = dst + put1;
+            each<kChunk / kPer>([&](auto j) {
+                constexpr uint32_t kTo = (decltype(j)::value >> 1) * 2 * kPer * DP;
+                const uint32_t to = decltype(j)::value & 1 ? to1 : to0;
+                if constexpr (std::is_same_v<decltype(width), int>) {
+                    cp_async16<kTo, 0>(to, k + j * kPer * width);
+                    cp_async16<kTo + Sl::kV, 0>(to, v + j * kPer * width);
+                } else {
+                    cp_async16<kTo, decltype(j)::value * kPer * DP>(to, k);
+                    cp_async16<kTo + Sl::kV, decltype(j)::value * kPer * DP>(to, v);
+                }
+            });
+        };
+        auto load = [&](int i, uint32_t s) {
+            if (i < mine) {
+                if ((i & 31) == 0) {
+                    if (i) places = places_next, edges = edges_next;
+                    if (i + 32 < mine) look(i + 32 + lane, places_next, edges_next);
+                }
+                const uint32_t place = __shfl_sync(0xffffffffu, places, i & 31), bit = 1u << s;
+                slot_edge = (edges >> (i & 31) & 1u) || place >= kBadChunk ? slot_edge | bit : slot_edge & ~bit;
+                if (place < kBadChunk) {
+                    slot_bad &= ~bit;
+                    if (D == DP) copy(ring + s * Sl::kBytes, place, std::integral_constant<int, DP>{});
+                    else copy(ring + s * Sl::kBytes, place, D);
+                } else {
+                    slot_bad |= bit;
+                    if (lane == 0) atomicOr(c.flags, kFlagBadPage);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) load(i, (uint32_t)i);
+
         // ---- the queries, a block of 8 rows a warp: row g, dimensions 64 h + 16 t + 0 .. 15, in fp16 after a power of
         // two; what lane (g, t) needs of them for two products lies together
         for (int n = warp; n < N; n += kWarps) {
-            const int r = 8 * n + g, m = m0 + r, blk = m / group;
-            const T *src = static_cast<const T *>(a.q) + (q.first + blk) * a.q_stride + (int64_t)(head * group + (m - blk * group)) * D;
+            const int r = 8 * n + g;
+            int of;
+            const int blk = w.by_group.div(m0 + r, of);
+            const T *src = static_cast<const T *>(a.q) + (view.first + blk) * a.q_stride + (int64_t)(view.head * group + of) * D;
             uint4 in[2 * kHalves];
 #pragma unroll
             for (int i = 0; i < 2 * kHalves; ++i) {
                 const int d = 64 * (i >> 1) + 16 * t + 8 * (i & 1);
-                in[i] = r < rows && d < D ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
+                in[i] = r < view.rows && d < D ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
             }
             uint32_t top = 0;
 #pragma unroll
@@ -266,108 +396,20 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             }
         }
         __syncthreads();
-        if (tree) {
-            low_min = low_max = ranges[0].low;
-            for (int i = 1; i < kRows; ++i) low_min = min(low_min, ranges[i].low), low_max = max(low_max, ranges[i].low);
-        }
-        Chunks chunks;
-        chunks.find(a.prefix_len, a.sinks, low_min, end_max);
-
-        // ---- the warp's chunks: their numbers in the cache, in 16 head rows, a lane each for 32 of them, and the
-        // next 32; bits of those that some row sees only in part (or not at all)
-        const int parts = w.cluster * kWarps, part = split * kWarps + warp;
-        const int mine = chunks.total > part ? (chunks.total - part + parts - 1) / parts : 0;
-        const int per_page = c.page_size / kChunk;
-        // the tokens of a chunk that some row may see: [from, to), and where it begins
-        auto bounds = [&](int i, int &pos0, int &from, int &to) {
-            if (i >= mine) {
-                pos0 = from = to = 0;
-                return;
-            }
-            bool own;
-            const int chunk = chunks.at(part + i * parts, own);
-            pos0 = chunk * kChunk + (own ? a.prefix_len : 0);
-            to = min(own ? end_max : min(a.prefix_len, end_max), pos0 + kChunk) - pos0;
-            from = pos0 < a.sinks ? 0 : max(low_min - pos0, 0);
-        };
-        auto look = [&](int i, uint32_t &place, uint32_t &edges) {
-            place = kNoChunk;
-            bool edge = false;
-            if (i < mine) {
-                bool own;
-                const int chunk = chunks.at(part + i * parts, own), page_slot = chunk / per_page;
-                const int page = own ? a.rows.block_table[(int64_t)b * a.rows.max_pages + page_slot] : a.prefix_pages[page_slot];
-                place = page < 0 || page >= c.n_pages ? kBadChunk
-                                                      : ((uint32_t)page * (uint32_t)H + (uint32_t)head) * (uint32_t)per_page +
-                                                            (uint32_t)(chunk - page_slot * per_page);
-                int pos0, from, to;
-                bounds(i, pos0, from, to);
-                edge = !(from == 0 && to == kChunk && pos0 + kChunk <= end_min && (pos0 >= low_max || pos0 + kChunk <= a.sinks));
-            }
-            edges = __ballot_sync(0xffffffffu, edge);
-        };
-        uint32_t places, edges, places_next = kNoChunk, edges_next = 0;
-        look(lane, places, edges);
-        // bits of the ring's chunks that are an edge, and of those that have no page
-        uint32_t slot_edge = 0, slot_bad = 0;
-        constexpr int kPieces = DP / 16, kPer = 32 / kPieces;       // pieces of a token; tokens at once
-        const int col = lane % kPieces, tok0 = lane / kPieces;
-        // (the permutation repeats every 8 tokens: tokens tok0 + 4 j at DP = 128 have two, tok0 + 8 j at 64 one)
-        const uint32_t put0 = piece_at<DP>((uint32_t)tok0, (uint32_t)col), put1 = piece_at<DP>((uint32_t)(tok0 + kPer), (uint32_t)col);
-        const bool in_row = D == DP || col * 16 < D;
-        const float *const scales = (lane < 4 ? c.k_scale : c.v_scale) + (lane & 3) * 4;
-        auto copy = [&](uint32_t dst, uint64_t place, auto width) {
-            const uint64_t at = place * (uint64_t)(kChunk * width) + (uint32_t)(tok0 * width + col * 16);
-            const unsigned char *k = static_cast<const unsigned char *>(c.k) + at, *v = static_cast<const unsigned char *>(c.v) + at;
-            if (in_row) {
-#pragma unroll
-                for (int j = 0; j < kChunk / kPer; ++j) {
-                    const uint32_t to = dst + ((j & 1) ? put1 : put0) + (uint32_t)((j >> 1) * 2 * kPer * DP);
-                    cp_async16(to, k + j * kPer * width);
-                    cp_async16(to + Sl::kV, v + j * kPer * width);
-                }
-            }
-            if (lane < 8) cp_async16(dst + Sl::kScales + (uint32_t)lane * 16u, scales + place * kChunk);
-        };
-        // step i: chunks 2 i and 2 i + 1; one behind the last is an edge of which nothing is there
-        const int steps = (mine + kPair - 1) / kPair;
-        auto load = [&](int i, uint32_t s) {
-            if (i < steps) {
-                if (i % (32 / kPair) == 0) {
-                    if (i) places = places_next, edges = edges_next;
-                    if (kPair * i + 32 < mine) look(kPair * i + 32 + lane, places_next, edges_next);
-                }
-                slot_edge &= ~(3u << (2 * s)), slot_bad &= ~(3u << (2 * s));
-#pragma unroll
-                for (int u = 0; u < kPair; ++u) {
-                    const int at = kPair * i + u;
-                    const uint32_t place = __shfl_sync(0xffffffffu, places, at & 31), bit = 1u << (2 * s + u);
-                    const uint32_t dst = ring + s * Sl::kStep + (uint32_t)u * Sl::kBytes;
-                    if (edges >> (at & 31) & 1u || place >= kBadChunk) slot_edge |= bit;
-                    if (place < kBadChunk) {
-                        if (D == DP) copy(dst, place, std::integral_constant<int, DP>{});
-                        else copy(dst, place, D);
-                    } else if (place == kBadChunk) {
-                        slot_bad |= bit;
-                        if (lane == 0) atomicOr(c.flags, kFlagBadPage);
-                    }
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i, (uint32_t)i);
 
         // ---- the loop over chunks
         float o[N][DP / 16][4];
-        float ref[N][2], l[N][2];
+        float ref[N][2], l[N][2], lack[N][2];  // of rows 2 t and 2 t + 1 of each block
 #pragma unroll
         for (int n = 0; n < N; ++n) {
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
             ref[n][0] = ref[n][1] = kUnset;
             l[n][0] = l[n][1] = 0.f;
+            lack[n][0] = lacks[8 * n + 2 * t], lack[n][1] = lacks[8 * n + 2 * t + 1];
         }
+        const float up = a.scale * kLog2e;
+        const uint32_t q_at = smem_u32(smem) + Smem<DP, N>::kQ + (uint32_t)lane * 16u;
         // places in a chunk of what the lane reads: keys of tokens g and g + 8 (8 lines on), its pieces 64 dimensions
         // apart; values of tokens 2 t, 2 t + 1 and of those 8 on
         uint32_t get_k[kHalves], get_v[2];
@@ -377,157 +419,110 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         for (int j = 0; j < 2; ++j)
             get_v[j] = Sl::kV + (DP == 128 ? piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g)
                                            : piece_at<DP>((uint32_t)(2 * t + j), (uint32_t)g >> 1) + ((uint32_t)g & 1u) * 8u);
-        const float up = a.scale * kLog2e;
-        const uint32_t q_at = smem_u32(smem) + Smem<DP, N>::kQ + (uint32_t)lane * 16u;
-        float lack[N][2];                     // of rows 2 t and 2 t + 1 of each block
-#pragma unroll
-        for (int n = 0; n < N; ++n) lack[n][0] = lacks[8 * n + 2 * t], lack[n][1] = lacks[8 * n + 2 * t + 1];
         // (of the N blocks of rows the first M exist)
         auto walk = [&](auto blocks) {
             constexpr int M = decltype(blocks)::value;
-            uint32_t s = 0, s_load = kStages - 1;
+            uint32_t s = 0;
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i) {
+            for (int i = 0; i < mine; ++i) {
                 cp_async_wait<kStages - 2>();
                 __syncwarp();
-                load(i + kStages - 1, s_load);    // to the place that the step before has left
-                const uint32_t src = ring + s * Sl::kStep;
-                const uint32_t edge = slot_edge >> (2 * s) & 3u, bad = slot_bad >> (2 * s) & 3u;
-                s = s + 1 == kStages ? 0 : s + 1;
-                s_load = s_load + 1 == kStages ? 0 : s_load + 1;
+                load(i + kStages - 1, s == 0 ? kStages - 1 : s - 1);    // to the place that the chunk before has left
+                const uint32_t src = ring + s * Sl::kBytes;
+                const bool edge = slot_edge >> s & 1u;
                 // scores
-                float x[M][kPair][4];
+                float x[M][4];
 #pragma unroll
-                for (int n = 0; n < M; ++n)
-#pragma unroll
-                    for (int u = 0; u < kPair; ++u) x[n][u][0] = x[n][u][1] = x[n][u][2] = x[n][u][3] = 0.f;
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    uint32_t kw[kPair][2][4];
-#pragma unroll
-                    for (int u = 0; u < kPair; ++u)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint4 v = lds128(src + get_k[h] + (uint32_t)u * Sl::kBytes + (uint32_t)e * 8u * DP);
-                            kw[u][e][0] = v.x, kw[u][e][1] = v.y, kw[u][e][2] = v.z, kw[u][e][3] = v.w;
-                        }
-#pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        __half2 f[kPair][2][2][2];
-#pragma unroll
-                        for (int u = 0; u < kPair; ++u)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                decode4<kFormat>(kw[u][e][k], f[u][0][e][0], f[u][0][e][1]);
-                                decode4<kFormat>(kw[u][e][k + 1], f[u][1][e][0], f[u][1][e][1]);
-                            }
-#pragma unroll
-                        for (int n = 0; n < M; ++n) {
-                            const uint4 v = lds128(q_at + (uint32_t)((n * 2 * kHalves + 2 * h + (k >> 1)) * 512));
-#pragma unroll
-                            for (int u = 0; u < kPair; ++u)
-                                mma16816(x[n][u], as_u32(f[u][0][0][0]), as_u32(f[u][0][1][0]), as_u32(f[u][0][0][1]),
-                                         as_u32(f[u][0][1][1]), v.x, v.y);
-#pragma unroll
-                            for (int u = 0; u < kPair; ++u)
-                                mma16816(x[n][u], as_u32(f[u][1][0][0]), as_u32(f[u][1][1][0]), as_u32(f[u][1][0][1]),
-                                         as_u32(f[u][1][1][1]), v.z, v.w);
-                        }
-                    }
-                }
+                for (int n = 0; n < M; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+                each<kHalves>([&](auto hc) {
+                    constexpr int h = decltype(hc)::value;
+                    const uint4 lo = lds128(src + get_k[h]), hi = lds128<8 * DP>(src + get_k[h]);
+                    const uint32_t kl[4] = {lo.x, lo.y, lo.z, lo.w}, kh[4] = {hi.x, hi.y, hi.z, hi.w};
+                    each<2>([&](auto kc) {
+                        constexpr int k = 2 * decltype(kc)::value;
+                        __half2 f[4], e[4];
+                        decode4<kFormat>(kl[k], f[0], f[1]);
+                        decode4<kFormat>(kh[k], e[0], e[1]);
+                        decode4<kFormat>(kl[k + 1], f[2], f[3]);
+                        decode4<kFormat>(kh[k + 1], e[2], e[3]);
+                        each<M>([&](auto nc) {
+                            constexpr int n = decltype(nc)::value;
+                            const uint4 u = lds128<(n * 2 * kHalves + 2 * h + (k >> 1)) * 512>(q_at);
+                            mma16816(x[n], as_u32(f[0]), as_u32(e[0]), as_u32(f[1]), as_u32(e[1]), u.x, u.y);
+                            mma16816(x[n], as_u32(f[2]), as_u32(e[2]), as_u32(f[3]), as_u32(e[3]), u.z, u.w);
+                        });
+                    });
+                });
                 // scales of tokens g and g + 8; one whose value scale (or page) is no number carries its NaN in the
                 // key's alone: where it is masked, its zero weight must not become 0 times NaN
-                float vs[kPair][2];
+                float vs[2];
+                const uint32_t scale_at = src + (uint32_t)g * 4u;
+                each<2>([&](auto ec) {
+                    constexpr int e = decltype(ec)::value;
+                    const float kv = lds32<Sl::kScales + e * 32>(scale_at), vv = lds32<Sl::kScales + 64 + e * 32>(scale_at);
+                    const bool good = vv <= 3.4028235e38f;
+                    const float ks = good ? kv * up : __int_as_float(0x7fffffff);
+                    vs[e] = good ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
 #pragma unroll
-                for (int u = 0; u < kPair; ++u)
+                    for (int n = 0; n < M; ++n) x[n][2 * e] *= ks, x[n][2 * e + 1] *= ks;
+                });
+                if (edge) {     // scores that the row does not see: -inf
+                    const bool bad = slot_bad >> s & 1u;
+                    const int ctx = view.ctx;
+                    int pos0, from, to;
+                    bounds(i, pos0, from, to);
+                    // what lies where no token is must not meet a weight of 0
+#pragma unroll 1
+                    for (int j = tok0; j < kChunk; j += kPer)
+                        if (bad || j < from || j >= to)
+                            st_shared_v4(src + Sl::kV + piece_at<DP>((uint32_t)j, (uint32_t)col), make_uint4(0, 0, 0, 0));
+                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t at = src + (uint32_t)u * Sl::kBytes + Sl::kScales + (uint32_t)(g + 8 * e) * 4u;
-                        const float kv = lds32(at), vv = lds32(at + 64u);
-                        const bool good = vv <= 3.4028235e38f;
-                        const float ks = good ? kv * up : __int_as_float(0x7fffffff);
-                        vs[u][e] = good ? fminf(vv * kVUp, 3.4028235e38f) : 0.f;
+                        const int tok = g + 8 * e, pos = pos0 + tok;
+                        const bool there = tok >= from && tok < to;
+                        if (!there || bad) vs[e] = 0.f;
 #pragma unroll
-                        for (int n = 0; n < M; ++n) x[n][u][2 * e] *= ks, x[n][u][2 * e + 1] *= ks;
-                    }
-                if (edge) {     // scores that the row does not see: -inf
+                        for (int n = 0; n < M; ++n)
 #pragma unroll
-                    for (int u = 0; u < kPair; ++u) {
-                        int pos0, from, to;
-                        bounds(kPair * i + u, pos0, from, to);
-                        if (bad >> u & 1u) to = 0;
-                        // what lies where no token is must not meet a weight of 0
-#pragma unroll 1
-                        for (int j = 0; j < kChunk; j += kPer) {
-                            if (tok0 + j < from || tok0 + j >= to)
-                                st_shared_v4(src + (uint32_t)u * Sl::kBytes + Sl::kV + piece_at<DP>((uint32_t)(tok0 + j), (uint32_t)col),
-                                             make_uint4(0, 0, 0, 0));
-                        }
-                        __syncwarp();
-                        if (bad >> u & 1u) bounds(kPair * i + u, pos0, from, to);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int tok = g + 8 * e, pos = pos0 + tok;
-                            const bool there = tok >= from && tok < to;
-                            if (!there || (bad >> u & 1u)) vs[u][e] = 0.f;
-#pragma unroll
-                            for (int n = 0; n < M; ++n)
-#pragma unroll
-                                for (int f = 0; f < 2; ++f) {
-                                    const int row = 8 * n + 2 * t + f;
-                                    const RowRange r = ranges[row];
-                                    bool sees = there && pos < r.end && (pos >= r.low || pos < a.sinks);
-                                    if (tree && pos >= ctx) sees = tok < to && (words[row] >> (pos - ctx) & 1);
-                                    float &y = x[n][u][2 * e + f];
-                                    y = !sees ? -INFINITY : (bad >> u & 1u) ? __int_as_float(0x7fffffff) : y;
-                                }
-                        }
+                            for (int f = 0; f < 2; ++f) {
+                                const RowRange r = ranges[8 * n + 2 * t + f];
+                                bool sees = there && pos < r.end && (pos >= r.low || pos < a.sinks);
+                                if (tree && pos >= ctx) sees = tok < to && (words[8 * n + 2 * t + f] >> (pos - ctx) & 1);
+                                float &y = x[n][2 * e + f];
+                                y = !sees ? -INFINITY : bad ? __int_as_float(0x7fffffff) : y;
+                            }
                     }
                 }
                 // softmax terms and what they weigh the values' codes with; whether one of these, or a sum, passes its
                 // bound
-                uint32_t pk[M][kPair][2];
+                uint32_t pk[M][2];
                 float sum[M][2];
-                auto terms = [&]() {
+#pragma unroll 1
+                for (bool again = false;; again = true) {
                     uint32_t past = 0;
                     float most = 0.f;
 #pragma unroll
                     for (int n = 0; n < M; ++n) {
-                        sum[n][0] = sum[n][1] = 0.f;
+                        float p[4];
 #pragma unroll
-                        for (int u = 0; u < kPair; ++u) {
-                            float p[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(x[n][u][e], lack[n][e & 1], -ref[n][e & 1]));
-                            pk[n][u][0] = half_pair(p[0] * vs[u][0], p[1] * vs[u][0]);
-                            pk[n][u][1] = half_pair(p[2] * vs[u][1], p[3] * vs[u][1]);
-                            past |= __vmaxu2(pk[n][u][0], pk[n][u][1]) + 0x04000400u;       // kPast and more: a half's top bit
-                            sum[n][0] += p[0] + p[2];
-                            sum[n][1] += p[1] + p[3];
-                        }
+                        for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(x[n][e], lack[n][e & 1], -ref[n][e & 1]));
+                        pk[n][0] = half_pair(p[0] * vs[0], p[1] * vs[0]);
+                        pk[n][1] = half_pair(p[2] * vs[1], p[3] * vs[1]);
+                        static_assert(kPast + 0x0400u == 0x8000u, "");
+                        past |= __vmaxu2(pk[n][0], pk[n][1]) + 0x04000400u;       // kPast and more: a half's top bit
+                        sum[n][0] = p[0] + p[2];
+                        sum[n][1] = p[1] + p[3];
                         most = max3(most, sum[n][0], sum[n][1]);
                     }
-                    static_assert(kPast + 0x0400u == 0x8000u, "");
-                    return (past & 0x80008000u) || most > kSumMost;
-                };
-#pragma unroll 1
-                for (bool again = false;; again = true) {
-                    const bool past = terms();
-                    if (again || !__any_sync(0xffffffffu, past)) break;
-                    // the references move to the step's largest terms, where these lie above
-                    float lv[kPair][2];
-#pragma unroll
-                    for (int u = 0; u < kPair; ++u)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) lv[u][e] = fmaxf(fast_log2(vs[u][e]), kVLeast);
+                    if (again || !__any_sync(0xffffffffu, (past & 0x80008000u) || most > kSumMost)) break;
+                    // the references move to the chunk's largest terms, where these lie above
+                    const float v0 = fmaxf(fast_log2(vs[0]), kVLeast), v1 = fmaxf(fast_log2(vs[1]), kVLeast);
 #pragma unroll
                     for (int n = 0; n < M; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float top = -INFINITY;
-#pragma unroll
-                            for (int u = 0; u < kPair; ++u)
-                                top = max3(top, x[n][u][e] * lack[n][e] + lv[u][0], x[n][u][e + 2] * lack[n][e] + lv[u][1]);
+                            float top = fmaxf(x[n][e] * lack[n][e] + v0, x[n][e + 2] * lack[n][e] + v1);
 #pragma unroll
                             for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                             if (top == -INFINITY || !(top > ref[n][e] + kPeak)) continue;
@@ -543,42 +538,36 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 for (int n = 0; n < M; ++n) {
                     l[n][0] += sum[n][0];
                     l[n][1] += sum[n][1];
-#pragma unroll
-                    for (int u = 0; u < kPair; ++u) {
-                        pk[n][u][0] = transpose8x8(pk[n][u][0]);
-                        pk[n][u][1] = transpose8x8(pk[n][u][1]);
-                    }
+                    pk[n][0] = transpose8x8(pk[n][0]);
+                    pk[n][1] = transpose8x8(pk[n][1]);
                 }
                 // outputs
-#pragma unroll
-                for (int u = 0; u < kPair; ++u) {
-                    uint32_t vw[4][DP / 32];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t at = src + get_v[j & 1] + (uint32_t)u * Sl::kBytes + (uint32_t)(j >> 1) * 8u * DP;
-                        if constexpr (DP == 128) {
-                            const uint4 v = lds128(at);
-                            vw[j][0] = v.x, vw[j][1] = v.y, vw[j][2] = v.z, vw[j][3] = v.w;
-                        } else {
-                            const uint2 v = lds64(at);
-                            vw[j][0] = v.x, vw[j][1] = v.y;
-                        }
+                uint32_t vw[4][DP / 32];
+                each<4>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    const uint32_t at = src + get_v[j & 1];
+                    if constexpr (DP == 128) {
+                        const uint4 v = lds128<(j >> 1) * 8 * DP>(at);
+                        vw[j][0] = v.x, vw[j][1] = v.y, vw[j][2] = v.z, vw[j][3] = v.w;
+                    } else {
+                        const uint2 v = lds64<(j >> 1) * 8 * DP>(at);
+                        vw[j][0] = v.x, vw[j][1] = v.y;
                     }
+                });
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t pick = (k & 1) ? 0x7362u : 0x5140u;
-                        __half2 a0, a1, a2, a3;
-                        decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
-                        decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t pick = (k & 1) ? 0x7362u : 0x5140u;
+                    __half2 a0, a1, a2, a3;
+                    decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
+                    decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
 #pragma unroll
-                        for (int n = 0; n < M; ++n)
-                            mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][u][0], pk[n][u][1]);
-                    }
+                    for (int n = 0; n < M; ++n) mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][0], pk[n][1]);
                 }
+                s = s + 1 == kStages ? 0 : s + 1;
             }
         };
-        if (N >= 3 && rows <= kRows / 3) walk(std::integral_constant<int, (N + 2) / 3>{});
-        else if (N >= 2 && rows <= (N == 2 ? 8 : kRows / 3 * 2)) walk(std::integral_constant<int, N == 2 ? 1 : (2 * N + 2) / 3>{});
+        if (N == 3 && view.rows <= 8) walk(std::integral_constant<int, 1>{});
+        else if (N > 1 && view.rows <= 8 * (N - 1)) walk(std::integral_constant<int, N == 1 ? 1 : N - 1>{});
         else walk(std::integral_constant<int, N>{});
         cp_async_wait<0>();
 
@@ -587,7 +576,8 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         float *parts_o = reinterpret_cast<float *>(smem);
         constexpr int kPitch = DP + 4;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+        for (int n = 0; n < N; ++n) {
+            if (8 * n >= view.rows) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float sum = l[n][e];
@@ -600,8 +590,10 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 for (int k = 0; k < DP / 16; k += 2)
                     *reinterpret_cast<float4 *>(to + 2 * k) = make_float4(o[n][k][e], o[n][k][e + 2], o[n][k + 1][e], o[n][k + 1][e + 2]);
             }
+        }
         __syncthreads();
-        // what a part's row counts in the join of `count` parts, whose references and sums `stat` gives
+        // what a part's row counts in the join of `count` parts, whose references and sums `stat` gives (a part that
+        // saw nothing: kUnset and 0, and its output is 0)
         auto weigh = [&](int count, auto stat, float &top, float &total, auto put) {
             top = kUnset;
             for (int i = 0; i < count; ++i) top = fmaxf(top, stat(i).x);
@@ -612,48 +604,59 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 total += scale_down(st.y, st.x - top);
             }
         };
-        if (threadIdx.x < kRows) {
+        auto finish = [&](int r, float top, float total) {     // what a row's sums are multiplied by
+            if (a.lse) a.lse[row_place[r]] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
+            return total == 0.f ? 0.f : kVDown / total;
+        };
+        const int rows = view.rows;
+        if (threadIdx.x < rows) {
             const int r = threadIdx.x;
-            float top, total;
-            weigh(kWarps, [&](int k) { return stats[k][r]; }, top, total, [&](int k, float f) { weights[k][r] = f; });
+            int of;
+            const int blk = w.by_group.div(view.m0 + r, of);
+            row_place[r] = (view.first + blk) * a.n_q_heads + view.head * group + of;
+            float top, total, f[kWarps];
+            weigh(kWarps, [&](int k) { return stats[k][r]; }, top, total, [&](int k, float x) { f[k] = x; });
             stats[kWarps][r] = make_float2(top, total);
+            const float by = w.cluster == 1 ? finish(r, top, total) : 1.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) weights[k][r] = f[k] * by;
         }
         __syncthreads();
-        auto result = [&](int r, int d, const float4 &sum, float top, float total) {
-            const int m = m0 + r, blk = m / group;
-            const int64_t place = (q.first + blk) * Hq + head * group + (m - blk * group);
-            const float inv = total == 0.f ? 0.f : kVDown / total;
-            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + place * D + d) =
-                make_uint2(float_to_pair<T>(sum.x * inv, sum.y * inv), float_to_pair<T>(sum.z * inv, sum.w * inv));
-            if (d == 0 && a.lse) a.lse[place] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
-        };
         auto add = [](float4 &sum, const float4 &x, float f) { sum.x += x.x * f, sum.y += x.y * f, sum.z += x.z * f, sum.w += x.w * f; };
-        const int quarters = D / 4;
+        auto store = [&](int r, int d, const float4 &x) {
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row_place[r] * D + d) =
+                make_uint2(float_to_pair<T>(x.x, x.y), float_to_pair<T>(x.z, x.w));
+        };
+        // a thread takes four dimensions of every kAtOnce-th row
+        constexpr int kAtOnce = kThreads / (DP / 4);
+        const int d = (int)threadIdx.x % (DP / 4) * 4;
         float *block_o = parts_o + kWarps * kRows * kPitch;
-        for (int i = threadIdx.x; i < rows * quarters; i += kThreads) {
-            const int r = i / quarters, d = (i - r * quarters) * 4;
+        for (int r = (int)threadIdx.x / (DP / 4); r < rows; r += kAtOnce) {
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) add(sum, *reinterpret_cast<const float4 *>(parts_o + (k * kRows + r) * kPitch + d), weights[k][r]);
-            if (w.cluster == 1) result(r, d, sum, stats[kWarps][r].x, stats[kWarps][r].y);
-            else *reinterpret_cast<float4 *>(block_o + r * kPitch + d) = sum;
+            if (w.cluster > 1) *reinterpret_cast<float4 *>(block_o + r * kPitch + d) = sum;
+            else if (d < D) store(r, d, sum);
         }
         if (w.cluster > 1) {
             cg::cluster_group cluster = cg::this_cluster();
             cluster.sync();
-            for (int i = split * kThreads + threadIdx.x; i < rows * quarters; i += w.cluster * kThreads) {
-                const int r = i / quarters, d = (i - r * quarters) * 4;
+            for (int r = split * kAtOnce + (int)threadIdx.x / (DP / 4); r < rows; r += w.cluster * kAtOnce) {
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                 float top, total;
                 weigh(w.cluster, [&](int k) { return *cluster.map_shared_rank(&stats[kWarps][r], k); }, top, total,
                       [&](int k, float f) {
                           add(sum, *reinterpret_cast<const float4 *>(cluster.map_shared_rank(block_o, k) + r * kPitch + d), f);
                       });
-                result(r, d, sum, top, total);
+                const float by = d == 0 ? finish(r, top, total) : total == 0.f ? 0.f : kVDown / total;
+                sum.x *= by, sum.y *= by, sum.z *= by, sum.w *= by;
+                if (d < D) store(r, d, sum);
             }
             cluster.sync();     // before another block's memory goes, or is written again
         }
-        __syncthreads();        // the ring is the next rows'
+        m0 = view.m0 + w.slots * kRows;
+        if (m0 >= view.n * group) break;
+        __syncthreads();        // the ring, the ranges and the queries are the next rows'
         if (D != DP) {
             for (uint32_t i = threadIdx.x; i < Smem<DP, N>::kRing / 16; i += kThreads)
                 reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
@@ -673,16 +676,18 @@ cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     const int group = a.n_q_heads / a.cache.n_kv_heads;
     // row blocks of an average request, which one block each takes at once
     const int64_t rows = ((int64_t)a.rows.n_rows + a.rows.B - 1) / a.rows.B * group;
-    w.slots = (int)((rows + 8 * N - 1) / (8 * N));
+    w.slots = (int)(((a.rows.n_rows > a.rows.B ? rows * 3 / 2 : rows) + 8 * N - 1) / (8 * N));
     // an item's tokens go to a cluster of up to 8 blocks while there are fewer blocks than SMs hold and a warp has
     // four chunks or more
     int64_t blocks = (int64_t)a.rows.B * a.cache.n_kv_heads * w.slots;
     const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)a.window + a.sinks;
     const int64_t chunks = (own < seen ? own : seen) / kChunk;
     w.cluster = 1;
-    while (w.cluster < kMaxCluster && blocks * w.cluster < (int64_t)kNumSMs * Shape<DP, N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
+    while (w.cluster < kMaxCluster && blocks * w.cluster * 2 <= (int64_t)kNumSMs * Shape<DP, N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
         w.cluster *= 2;
     blocks *= w.cluster;
+    w.by_cluster = Divider(w.cluster);
+    w.by_slots = Divider(w.slots);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -703,7 +708,7 @@ cudaError_t launch_dp(WindowArgs &w, cudaStream_t s) {
     const int group = w.a.n_q_heads / w.a.cache.n_kv_heads;
     const int64_t rows = ((int64_t)w.a.rows.n_rows + w.a.rows.B - 1) / w.a.rows.B * group;
     if (rows <= 8) return launch_n<T, kFormat, DP, 1>(w, s);
-    if (rows <= 10) return launch_n<T, kFormat, DP, 2>(w, s);
+    if (rows <= 16) return launch_n<T, kFormat, DP, 2>(w, s);
     return launch_n<T, kFormat, DP, 3>(w, s);
 }
 
@@ -728,7 +733,8 @@ size_t window_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int hea
 
 cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s) {
     if (many_rows(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.n_kv_heads)) return launch_window_blocks(a, s);
-    WindowArgs w{a, 1, 1};
+    WindowArgs w{a, Divider(), Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
+                 Divider(a.cache.page_size / kChunk), 1, 1};
     return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
 }
 
