@@ -51,9 +51,10 @@
 // issuing warps 7%, 24 warps with the issuer apart from the converters 15%.
 //
 // Compiled twice: window_blocks.cu includes this file with kWindow true, for rows that
-// see through a window.  An item then visits fewer tiles: those of the first tokens, then those
-// that any row of its row tile's window can reach, as many for every row tile of a
-// request, so that the plan stays a division (View, own_view, prefix_view).
+// see through a window.  An item's list of tokens then has a gap: behind the first tokens it
+// goes on where its row tile's window begins, both to a chunk of 16.  Lengths, contexts and places
+// are counted without the gap, so that only the look-up of pages knows of it, and as many
+// tiles are planned for every row tile of a request, so that the plan stays a division.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -110,16 +111,6 @@ struct Layout {
     static constexpr uint32_t kBytes = kQScale + 2048 + 1024;            // + alignment slack
 };
 
-// The tiles of a list of `total` that an item visits: `first` of its first ones, then, from a place
-// that may be the row tile's own, the rest.
-struct View {
-    int first, tiles, total;
-    // how far the others lie behind the first when the window of a row tile begins at token `low`
-    __device__ __forceinline__ int skip(int low) const {
-        return max(first, min(low / plan::kTile, total - (tiles - first))) - first;
-    }
-};
-
 // Consecutive tiles of one item
 struct Piece {
     int tiles, first;   // how many, and the first one's number in the item
@@ -131,16 +122,14 @@ struct Piece {
     int n;              // block rows (own tokens)
     int request;        // -1: the prefix
     int out;            // kDirect, kFirst, kContinued
-    // through a window: tiles of the list before a gap, its width, and the first token that a row may see behind it
-    int first_tiles, skip, low;
-    // the list's tile that is the item's tile i
-    __device__ __forceinline__ int tile(int i) const { return i < first_tiles ? i : i + skip; }
+    // through a window: chunks of the list before the gap, and the gap's (len and ctx are without it)
+    int first_chunks, gap;
 };
 // Up to four tiles of each group, taken in turns: 0 of the first, 0 of the
 // second, 1 of the first ..; pairs as tiles of the first.
 struct Round {
     int flags;                    // kRoundPair, kRoundEnd; bits 2 s, 2 s + 1: the first / last tile of stream s's piece is here
-    int n[2], token[2], piece[2]; // of the streams: tiles, first token (through a window: first tile of the item), place of the piece
+    int n[2], token[2], piece[2]; // of the streams: tiles, first token, place of the piece
     uint32_t chunks[2][32];       // where the tokens are, 16 a chunk, 8 chunks a tile
 };
 enum { kRoundPair = 16, kRoundEnd = 32 };
@@ -168,24 +157,29 @@ struct Partials {
     int *prefix_low;    // through a window: the first token of the prefix behind its first ones that any row sees
 };
 
-// The own tiles that a request's row tiles visit.  A row tile's window is window + rows - 1 tokens long,
-// whichever the rows; L tokens touch (L + 126) / 128 + 1 tiles at most.
-__device__ __forceinline__ View own_view(const AttentionArgs &a, int n, int len, int group) {
+__device__ __forceinline__ int up16(int x) { return (int)((unsigned)x + 15u & ~15u); }
+// Own tiles of a request's row tiles.  A row tile's window is window + rows - 1 tokens long, whichever the rows.
+__device__ __forceinline__ int own_tiles(const AttentionArgs &a, int n, int len, int group) {
     const int total = plan::token_tiles(len);
-    if constexpr (!kWindow) return {0, total, total};
-    const int first = plan::token_tiles(min(max(a.sinks - a.prefix_len, 0), len));
+    if constexpr (!kWindow) return total;
     // (a word's row may see one token further back than its place says)
     const int rows = a.row_mask ? n + 1 : a.mask == DSPARK_MASK_CAUSAL ? min(n, (plan::kTileRows + group - 2) / group + 1) : n;
-    const int64_t tiles = first + ((int64_t)a.window + rows - 1 + 126) / plan::kTile + 1;
-    return {first, (int)(tiles < total ? tiles : total), total};
+    const int64_t seen = (int64_t)up16(min(max(a.sinks - a.prefix_len, 0), len)) + a.window + rows - 1 + 15;
+    return seen < len ? plan::token_tiles((int)seen) : total;
 }
-// The prefix's, with `low` as in Partials.
-__device__ __forceinline__ View prefix_view(const AttentionArgs &a, int low) {
-    const int total = plan::token_tiles(a.prefix_len);
-    if constexpr (!kWindow) return {0, total, total};
-    const int first = plan::token_tiles(min(a.sinks, a.prefix_len));
-    const int tiles = first + (low < a.prefix_len ? max(total - max(first, low / plan::kTile), 0) : 0);
-    return {first, tiles, total};
+// The prefix's tokens that some row sees, first ones and those from `low` (as in Partials) on, with the gap between them.
+__device__ __forceinline__ int prefix_seen(const AttentionArgs &a, int low, int &first, int &gap) {
+    first = gap = 0;
+    if constexpr (!kWindow) return a.prefix_len;
+    const int sinks = min(a.sinks, a.prefix_len);
+    if (low >= a.prefix_len) return sinks;
+    first = up16(sinks);
+    gap = max((low & ~15) - first, 0);
+    return a.prefix_len - gap;
+}
+__device__ __forceinline__ int prefix_tiles_of(const AttentionArgs &a, int low) {
+    int first, gap;
+    return plan::token_tiles(prefix_seen(a, low, first, gap));
 }
 // The first token of the window of block row `i` behind ctx tokens (in any list that these are counted in), at
 // least 0; with a mask word, of which c bits count, that of its tokens before the block.
@@ -281,7 +275,7 @@ struct Walk {
                 __syncwarp();
                 b = at;
                 m = w_n[at - wb] * group;
-                tiles = own_view(a, w_n[at - wb], w_len[at - wb], group).tiles;
+                tiles = own_tiles(a, w_n[at - wb], w_len[at - wb], group);
                 __syncwarp();
                 return true;
             }
@@ -348,19 +342,27 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
         p.n = b < 0 ? 0 : k.w_n[b - k.wb];
         p.ctx = p.len - p.n;
         p.out = t0 > 0 ? kContinued : (b >= 0 && z.prefix_tiles == 0 && t1 == tiles) ? kDirect : kFirst;
-        p.first_tiles = p.skip = p.low = 0;
+        p.first_chunks = p.gap = 0;
         if constexpr (kWindow) {
-            const View view = b < 0 ? prefix_view(a, z.prefix_low) : own_view(a, p.n, p.len, z.group);
-            p.first_tiles = view.first;
-            p.low = b >= 0 ? window_low(a, p.ctx, p.m0 / z.group) : z.prefix_low < p.len ? z.prefix_low : 0x7fffffff;
-            if (b >= 0 && a.row_mask) {
-                int least = 64;
-                for (int i = lane; i < p.n; i += 32) least = min(least, __popcll(word_of(a, p.row_base + i, p.n)));
+            int first, gap;
+            if (b < 0) {
+                p.len = p.ctx = prefix_seen(a, z.prefix_low, first, gap);
+            } else {
+                int low = window_low(a, p.ctx, p.m0 / z.group);
+                if (a.row_mask) {
+                    int least = 64;
+                    for (int i = lane; i < p.n; i += 32) least = min(least, __popcll(word_of(a, p.row_base + i, p.n)));
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
-                p.low = window_low_of_word(a, p.ctx, least);
+                    for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+                    low = window_low_of_word(a, p.ctx, least);
+                }
+                first = up16(min(max(a.sinks - a.prefix_len, 0), p.len));
+                gap = max((low & ~15) - first, 0);
+                p.len -= gap;
+                p.ctx -= gap;
             }
-            p.skip = view.skip(p.low);
+            p.first_chunks = first >> 4;
+            p.gap = gap >> 4;
         }
         __syncwarp();
         // the cursor moves to the next item
@@ -392,8 +394,6 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
 // kept by chunk of 16 tokens (a chunk lies inside one page), as the chunk's
 // number in the cache, in units of 16 head rows: 32 chunks (4 tiles) at a time,
 // one a lane, their pages loaded four tiles before they are needed.
-// tokens of a run: a power of two of them share a page
-__device__ __forceinline__ int run_tokens(int page_size) { return min(page_size & -page_size, plan::kTile); }
 constexpr uint32_t kNoChunk = 0xffffffffu, kBadChunk = 0xfffffffeu;
 // Pieces a stream's tiles refer to: a slot is written again only after every
 // tile of its piece has left the rings (the next piece is planned while the last
@@ -409,15 +409,10 @@ struct Stream {
 
     __device__ __forceinline__ void load_pages(const AttentionArgs &a, const Piece &p, int t, int lane) {
         const int per_page = a.cache.page_size / 16;
-        const int chunk = kWindow ? p.tile(p.first + t + (lane >> 3)) * 8 + (lane & 7) : (p.first + t) * 8 + lane;
+        int chunk = (p.first + t) * 8 + lane;
         int place = -1, pg = 0;
-        bool some = (int64_t)chunk * 16 < p.len;
-        if constexpr (kWindow) {    // pages that no row sees are not looked at; a page's tokens are loaded a run at a time
-            const int sinks = p.request < 0 ? a.sinks : max(a.sinks - a.prefix_len, 0);
-            const int run = run_tokens(a.cache.page_size), at = chunk * 16 & -run;
-            some = some && (at < sinks || at + run > p.low);
-        }
-        if (some) {
+        if ((int64_t)chunk * 16 < p.len) {
+            if (kWindow && chunk >= p.first_chunks) chunk += p.gap;
             const int slot = chunk / per_page;
             place = p.head * per_page + (chunk - slot * per_page);
             pg = p.request < 0 ? a.prefix_pages[slot] : a.rows.block_table[(int64_t)p.request * a.rows.max_pages + slot];
@@ -451,7 +446,7 @@ __device__ __noinline__ int stream_round(const AttentionArgs &a, const Line &z, 
     const Piece *p = s.slots + count % kPieces;
     if (lane == 0) {
         r.n[id] = n;
-        r.token[id] = kWindow ? p->first + j : (p->first + j) * plan::kTile;
+        r.token[id] = (p->first + j) * plan::kTile;
         r.piece[id] = id * kPieces + (int)(count % kPieces);
     }
     __syncwarp();
@@ -624,7 +619,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         __syncthreads();
         if (blockIdx.x == 0 && tid == 0) *parts.prefix_low = prefix_low;
     }
-    const int prefix_tiles = prefix_view(a, prefix_low).tiles;
+    const int prefix_tiles = prefix_tiles_of(a, prefix_low);
     int64_t prefix[2];
     for (int k = 0; k < 2; ++k) prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
     auto request_units = [&](int b, int64_t (&x)[2]) {
@@ -633,7 +628,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         const Request q = load_request(a, b);
         if (blockIdx.x == 0 && (!q.rows_ok || (q.n > 0 && !q.len_ok))) atomicOr(c.flags, kFlagBadLength);
         if (!q.len_ok || q.n == 0) return;
-        const int tiles = own_view(a, q.n, q.len, group).tiles;
+        const int tiles = own_tiles(a, q.n, q.len, group);
         for (int k = 0; k < 2; ++k) x[k] = plan::head_units(k, q.n * group, tiles) * c.n_kv_heads;
     };
     int64_t mine[2];
@@ -745,20 +740,18 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
     // on), to place `position` of the order of operands, in runs of tokens that share a page: their
     // codes or (another warp) with the keys the scales of both.  (Copies by the warp's own cp.async,
     // 512 bytes at a time, held it up: 2300 clocks a tile.)
-    const int run = run_tokens(c.page_size), runs = plan::kTile / run;
+    const int run = kWindow ? 16 : min(c.page_size & -c.page_size, plan::kTile), runs = plan::kTile / run;
     auto load = [&](uint32_t mine, bool is_v, uint32_t position, bool codes) {
         const int i = lane & 7;
         const uint32_t id = __shfl_sync(0xffffffffu, mine, (i * (run / 16)) & 7);
         const bool good = i < runs && id < kBadChunk;
         const unsigned bad = __ballot_sync(0xffffffffu, mine == kBadChunk) & 0xffu;
-        // of the tile's chunks those that nothing comes from: with a window also such as no row sees
-        const unsigned gone = kWindow ? __ballot_sync(0xffffffffu, mine >= kBadChunk) & 0xffu : bad;
         const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, good) & 0xffu);
         const uint32_t slot = position % kRaw;
         if (!warp_wait(raw_empty(slot), ((position / kRaw) & 1) ^ 1, abort)) return false;
         const uint32_t at = base + L::kRawAt + slot * L::kRawBytes;
         if (lane == 0) {
-            if (codes) raw_bad[slot] = (int)gone;
+            if (codes) raw_bad[slot] = (int)bad;
             mbar_arrive_expect_tx(raw_full(slot), n * (uint32_t)(run * (codes ? D : is_v ? 0 : 8)));
         }
         __syncwarp();
@@ -799,8 +792,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             order.step(flags);
             if (!end) {
                 const Piece &p = piece_at(uniform(r.piece[id]));
-                if constexpr (kWindow) valid = uniform(p.len) - uniform(p.tile(r.token[id] + i)) * plan::kTile;
-                else valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
+                valid = uniform(p.len) - uniform(r.token[id]) - i * plan::kTile;
                 if (flags & kTileFirst) {
                     // the piece's queries, by both teams
 #pragma unroll 1
@@ -1109,7 +1101,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 // the row's block and its place in it, for the prefix where any row's window reaches that
                 int64_t first_row = p.row_base;
                 int n_block = p.n, behind = ctx, i = blk;
-                if (p.request < 0 && uniform(line.prefix_low) < p.len) {
+                if (p.request < 0 && uniform(line.prefix_low) < a.prefix_len) {
                     int lo = 0, hi = a.rows.B;
                     while (hi - lo > 1) {       // the last request that begins at or before the row
                         const int mid = (lo + hi) >> 1;
@@ -1120,7 +1112,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     first_row = q.first;
                     n_block = q.n;
                     i = blk - (int)q.first;
-                    behind = a.prefix_len + (q.len_ok ? q.len - q.n : 0);
+                    behind = ctx + (q.len_ok ? q.len - q.n : 0);      // (without the prefix's gap)
                 }
                 if (n_block == 0) low = 0x7fffffff;
                 else if (!a.row_mask) low = window_low(a, behind, i);
@@ -1139,7 +1131,6 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++n, token += plan::kTile) {
                 const bool first = j == 0;
-                if constexpr (kWindow) token = uniform(p.tile(p.first + j)) * plan::kTile;
                 if (!warp_wait(s_full(w), n & 1, abort)) { ok = false; break; }
                 tc_fence_after();
                 if (first) {
@@ -1373,7 +1364,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
     if (q.n == 0) return;
     // the line: units of the prefix by class, of all pairs, of all (the last request's end)
     const int prefix_m = prefix_rows(a) * group;
-    const int prefix_tiles = prefix_view(a, kWindow ? *parts.prefix_low : 0).tiles;
+    const int prefix_tiles = prefix_tiles_of(a, kWindow ? *parts.prefix_low : 0);
     int64_t prefix[2], pairs, total;
     {
         const int last = a.rows.B - 1;
@@ -1384,7 +1375,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
             prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
             end[k] = prefix[k] + parts.unit0[k][last] +
                      (z.len_ok && z.n > 0
-                          ? plan::head_units(k, z.n * group, own_view(a, z.n, z.len, group).tiles) * c.n_kv_heads
+                          ? plan::head_units(k, z.n * group, own_tiles(a, z.n, z.len, group)) * c.n_kv_heads
                           : 0);
         }
         pairs = end[0];
@@ -1396,7 +1387,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
     // this lane's item (0 the prefix's, 1 the request's own) and its place among the item's workers
     const int side = lane >> 4, at = lane & 15;
     const int m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
-    const int tiles = side ? own_view(a, q.n, q.len, group).tiles : prefix_tiles;
+    const int tiles = side ? own_tiles(a, q.n, q.len, group) : prefix_tiles;
     for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < c.n_kv_heads * chunks; i += gridDim.y * kJoinWarps) {
         const int h = i / chunks, m0 = (i - h * chunks) * per, m1 = min(m0 + per, own_m);
         int item = -1;             // the row tile that is looked at
