@@ -155,6 +155,8 @@ struct Partials {
     float2 *stats;      // (r, l): [R Hq] prefix, [R Hq] own, [kCtas][256] continued pairs, [2 kCtas][128] continued singles
     float *o;           // the same rows of D unnormalised outputs
     int *prefix_low;    // through a window: the first token of the prefix behind its first ones that any row sees
+    int4 *split;        // and, without a prefix, [kCtas] pairs, [2 kCtas] singles: the item that each worker leaves
+                        // unfinished, for the joining (request, -1: none; head; first row of the row tile; rows)
 };
 
 __device__ __forceinline__ int up16(int x) { return (int)((unsigned)x + 15u & ~15u); }
@@ -237,6 +239,7 @@ __device__ __forceinline__ void store8(float *to, const uint32_t *x, float f) {
 // The line as a CTA sees it.
 struct Line {
     int group, prefix_m, prefix_tiles, prefix_low;
+    int4 *split;
     int64_t prefix[2], pairs, total;   // units of the prefix's items by class, of all pairs, of all
 };
 
@@ -245,6 +248,7 @@ struct Line {
 // its registers and code would burden the loop over tiles.
 struct Walk {
     int64_t u, hi, start;             // cursor, end, first unit of the item at the cursor
+    int record;                       // the worker's place in Partials::split
     int cls, b, head, k, m, tiles;    // that item: request (-1: the prefix), head, row tile of the class, rows, tiles
     int wb;                           // 32 requests' sizes from request wb on:
     int w_n[32], w_len[32], w_first[32];
@@ -381,6 +385,8 @@ __device__ __noinline__ int walk_next(const AttentionArgs &a, const Line &z, Wal
             }
         }
         if (p.tiles > 0) {
+            if (kWindow && p.out == kFirst && z.prefix_tiles == 0 && lane == 0)
+                z.split[k.record] = make_int4(b, head, p.m0, p.rows);
             if (lane == 0) slot = p;
             __syncwarp();
             return p.tiles;
@@ -422,8 +428,9 @@ struct Stream {
     }
 };
 
-__device__ __noinline__ void stream_begin(const AttentionArgs &a, const Line &z, Stream &s, int cls, int64_t lo, int64_t to,
-                                          int b0, int64_t own0, int lane) {
+__device__ __noinline__ void stream_begin(const AttentionArgs &a, const Line &z, Stream &s, int id, int cls, int64_t lo,
+                                          int64_t to, int b0, int64_t own0, int lane) {
+    if (kWindow && lane == 0) s.walk.record = (int)blockIdx.x + (cls == plan::kPair ? 0 : kCtas + (int)blockIdx.x + id);
     walk_begin(a, z, s.walk, cls, lo, to, b0, own0, lane);
     Piece &p = s.slots[s.count % kPieces];
     const int tiles = walk_next(a, z, s.walk, p, lane);
@@ -618,6 +625,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         for (int i = 0; i < kThreads / 32; ++i) prefix_low = min(prefix_low, (int)scan[0][i]);
         __syncthreads();
         if (blockIdx.x == 0 && tid == 0) *parts.prefix_low = prefix_low;
+        if (tid < 3) parts.split[tid * kCtas + blockIdx.x].x = -1;     // (of some worker, all are between them)
     }
     const int prefix_tiles = prefix_tiles_of(a, prefix_low);
     int64_t prefix[2];
@@ -659,6 +667,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
         line.prefix_m = prefix_m;
         line.prefix_tiles = prefix_tiles;
         line.prefix_low = prefix_low;
+        line.split = parts.split;
         line.prefix[0] = prefix[0];
         line.prefix[1] = prefix[1];
         line.pairs = pairs;
@@ -904,14 +913,14 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
             bool ok = true, pairing = true;
 #pragma unroll 1
             for (int i = 2; i >= 0; i -= 2)
-                stream_begin(a, line, streams[i >> 1], i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
+                stream_begin(a, line, streams[i >> 1], i >> 1, i == 0 ? plan::kPair : plan::kSingle, from_s[i], to_s[i], found_request[i],
                              found_units[i], lane);
             uint32_t taken = 0;                  // pieces given to the groups, modulo 2^16 (a multiple of the ring's laps)
 #pragma unroll 1
             for (uint32_t k = 0; ok; ++k) {
                 if (pairing && streams[0].tiles == 0) {
                     pairing = false;
-                    stream_begin(a, line, streams[0], plan::kSingle, from_s[1], to_s[1], found_request[1], found_units[1], lane);
+                    stream_begin(a, line, streams[0], 0, plan::kSingle, from_s[1], to_s[1], found_request[1], found_units[1], lane);
                 }
                 const uint32_t e = k % kRounds;
                 if (!warp_wait(round_empty(e), ((k / kRounds) & 1) ^ 1, abort)) { ok = false; break; }
@@ -1357,14 +1366,18 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials parts, const int per) {
     griddep_wait();
-    const int lane = threadIdx.x & 31, b = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const dspark_kv_cache &c = a.cache;
     const int D = c.head_dim, group = a.n_q_heads / c.n_kv_heads, Hq = a.n_q_heads;
-    const Request q = load_request(a, b);
-    if (q.n == 0) return;
-    // the line: units of the prefix by class, of all pairs, of all (the last request's end)
+    int b = blockIdx.x;
+    Request q = load_request(a, b);
     const int prefix_m = prefix_rows(a) * group;
     const int prefix_tiles = prefix_tiles_of(a, kWindow ? *parts.prefix_low : 0);
+    // without a prefix only items that a worker left unfinished are joined, in steps of kUnit rows a block
+    constexpr int kUnit = 64, kUnits = plan::kTileRows / kUnit;
+    const bool listed = kWindow && prefix_tiles == 0;
+    if (q.n == 0 && !listed) return;
+    // the line: units of the prefix by class, of all pairs, of all (the last request's end)
     int64_t prefix[2], pairs, total;
     {
         const int last = a.rows.B - 1;
@@ -1381,15 +1394,47 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         pairs = end[0];
         total = end[0] + end[1];
     }
-    const int64_t own0 = parts.unit0[0][b] + prefix[0], own1 = parts.unit0[1][b] + prefix[1];
     const int64_t all = (int64_t)a.rows.n_rows * Hq;
-    const int own_m = q.n * group, chunks = (own_m + per - 1) / per;
+    auto bad_row = [&](int64_t place) {
+        T *out = static_cast<T *>(a.out) + place * D;
+        if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+        if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+    };
+    if (listed && blockIdx.y == 0 && !q.len_ok)
+        for (int i = warp; i < q.n * Hq; i += kJoinWarps) bad_row(q.first * Hq + i);
     // this lane's item (0 the prefix's, 1 the request's own) and its place among the item's workers
     const int side = lane >> 4, at = lane & 15;
-    const int m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
-    const int tiles = side ? own_tiles(a, q.n, q.len, group) : prefix_tiles;
-    for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < c.n_kv_heads * chunks; i += gridDim.y * kJoinWarps) {
-        const int h = i / chunks, m0 = (i - h * chunks) * per, m1 = min(m0 + per, own_m);
+    int64_t own0, own1;
+    int own_m, m_of, rows, tiles;
+    auto of_request = [&]() {
+        own0 = parts.unit0[0][b] + prefix[0], own1 = parts.unit0[1][b] + prefix[1];
+        own_m = q.n * group;
+        m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
+        tiles = side ? own_tiles(a, q.n, q.len, group) : prefix_tiles;
+    };
+    if (!listed) of_request();
+    const int chunks = listed ? 0 : (own_m + per - 1) / per;
+    const int from = listed ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.y * kJoinWarps + warp;
+    const int step = listed ? gridDim.x * gridDim.y : gridDim.y * kJoinWarps;
+    const int jobs = listed ? 3 * kCtas * kUnits : c.n_kv_heads * chunks;
+    for (int i = from; i < jobs; i += step) {
+        int h = 0, m0, m1, every = 1;
+        if (listed) {
+            const int4 record = parts.split[i / kUnits];
+            const int first = i % kUnits * kUnit;
+            if (record.x < 0 || first >= record.w) continue;
+            b = record.x;
+            q = load_request(a, b);
+            of_request();
+            h = record.y;
+            m0 = record.z + first + warp;
+            m1 = record.z + min(first + kUnit, record.w);
+            every = kJoinWarps;
+        } else {
+            h = i / chunks;
+            m0 = (i - h * chunks) * per;
+            m1 = min(m0 + per, own_m);
+        }
         int item = -1;             // the row tile that is looked at
         bool has = false, first = false, more = false, done = false;
         int64_t part0 = 0;
@@ -1419,13 +1464,12 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
             more = __any_sync(0xffffffffu, go_on);
             if (turn == 0) done = __any_sync(0xffffffffu, side && alone && prefix_tiles == 0);
         };
-        for (int m = m0; m < m1; ++m) {
+        for (int m = m0; m < m1; m += every) {
             const int blk = m / group;
             const int64_t place = (q.first + blk) * Hq + h * group + (m - blk * group);
             T *out = static_cast<T *>(a.out) + place * D;
             if (!q.len_ok) {
-                if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-                if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+                bad_row(place);
                 continue;
             }
             const int mt = m_of + m, now = mt / plan::kTileRows;
@@ -1486,7 +1530,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
 }
 
 struct Regions {
-    size_t unit1, stats, o, low, bytes;
+    size_t unit1, stats, o, split, low, bytes;
 };
 Regions regions(int B, int n_rows, int n_q_heads, int D) {
     const size_t parts = 2 * (size_t)n_rows * n_q_heads + 2 * (size_t)kCtas * plan::kTileRows;
@@ -1494,7 +1538,8 @@ Regions regions(int B, int n_rows, int n_q_heads, int D) {
     g.unit1 = align_up((size_t)B * sizeof(int64_t), 256);
     g.stats = 2 * g.unit1;
     g.o = align_up(g.stats + parts * sizeof(float2), 256);
-    g.low = align_up(g.o + parts * D * sizeof(float), 256);
+    g.split = align_up(g.o + parts * D * sizeof(float), 256);
+    g.low = g.split + (kWindow ? align_up(3 * kCtas * sizeof(int4), 256) : 0);
     g.bytes = g.low + (kWindow ? 256 : 0);
     return g;
 }
@@ -1519,7 +1564,9 @@ cudaError_t launch_t(const AttentionArgs &a, const Partials &p, cudaStream_t s) 
     const int64_t rows = (int64_t)a.rows.n_rows * a.n_q_heads;
     const int per = rows >= kJoinRows * 8 * kNumSMs ? kJoinRows : 1;
     const int64_t warps = (rows + (int64_t)a.rows.B * per - 1) / ((int64_t)a.rows.B * per);
-    const int y = (int)((warps + kJoinWarps - 1) / kJoinWarps);
+    int y = (int)((warps + kJoinWarps - 1) / kJoinWarps);
+    if (kWindow) y = y < 2048 / a.rows.B ? y : 2048 / a.rows.B;     // of long blocks most rows need no joining
+    if (y < 1) y = 1;
     return launch_dependent(attention_join_kernel<T>, dim3(a.rows.B, y < 1024 ? y : 1024), dim3(kJoinWarps * 32), 0, s, a, p,
                             per);
 }
@@ -1536,7 +1583,7 @@ cudaError_t launch_blocks(const AttentionArgs &a, cudaStream_t s) {
     const Regions g = regions(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.head_dim);
     const Partials p{{reinterpret_cast<int64_t *>(a.ws), reinterpret_cast<int64_t *>(a.ws + g.unit1)},
                      reinterpret_cast<float2 *>(a.ws + g.stats), reinterpret_cast<float *>(a.ws + g.o),
-                     reinterpret_cast<int *>(a.ws + g.low)};
+                     reinterpret_cast<int *>(a.ws + g.low), reinterpret_cast<int4 *>(a.ws + g.split)};
     return a.dt == DSPARK_BF16 ? launch_format<__nv_bfloat16>(a, p, s) : launch_format<__half>(a, p, s);
 }
 
