@@ -1363,7 +1363,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 constexpr int kJoinWarps = 8, kJoinRows = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32, kWindow ? 4 : 1)
 attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials parts, const int per) {
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1565,7 +1565,7 @@ cudaError_t launch_t(const AttentionArgs &a, const Partials &p, cudaStream_t s) 
     const int per = rows >= kJoinRows * 8 * kNumSMs ? kJoinRows : 1;
     const int64_t warps = (rows + (int64_t)a.rows.B * per - 1) / ((int64_t)a.rows.B * per);
     int y = (int)((warps + kJoinWarps - 1) / kJoinWarps);
-    if (kWindow) y = y < 2048 / a.rows.B ? y : 2048 / a.rows.B;     // of long blocks most rows need no joining
+    if (kWindow) y = y < 4 * kNumSMs / a.rows.B ? y : 4 * kNumSMs / a.rows.B;     // of long blocks most rows need no joining
     if (y < 1) y = 1;
     return launch_dependent(attention_join_kernel<T>, dim3(a.rows.B, y < 1024 ? y : 1024), dim3(kJoinWarps * 32), 0, s, a, p,
                             per);
