@@ -478,7 +478,7 @@ DSPARK_API dspark_status dspark_kv_read(
  * axis axis[i]; axis NULL means one axis.
  */
 typedef struct dspark_rotary {
-    const uint64_t *step;  /* [n_pairs], device */
+    const uint64_t *step;  /* [n_pairs], device, 16-byte aligned */
     const int32_t *axis;   /* [n_pairs] values in [0, n_axes), device, or NULL (then n_axes is 1) */
     int32_t n_pairs;       /* a multiple of 4, 2 n_pairs <= head_dim */
     int32_t n_axes;

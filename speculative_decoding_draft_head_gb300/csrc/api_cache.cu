@@ -49,7 +49,7 @@ dspark_status check_rows(const PagedRows &p, const dspark_kv_cache *c) {
 
 dspark_status check_rotary(const dspark_rotary *z, int head_dim) {
     if (!z) return fail(DSPARK_ERR_INVALID_ARG, "rotary is NULL");
-    if (!z->step || !aligned(z->step, 8) || !aligned(z->axis, 4))
+    if (!z->step || !aligned(z->step, 16) || !aligned(z->axis, 4))
         return fail(DSPARK_ERR_INVALID_ARG, "rotary's steps are NULL or its arrays not aligned");
     if (z->n_pairs < 4 || z->n_pairs % 4 != 0 || z->n_pairs > head_dim / 2)
         return fail(DSPARK_ERR_INVALID_ARG, "n_pairs must be a positive multiple of 4 up to half of head_dim (got %d, %d)",

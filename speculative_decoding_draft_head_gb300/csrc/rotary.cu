@@ -8,8 +8,8 @@
 // 2^64, is one integer product that wraps where the angle does.  Its error is
 // |p| 2^-65 turns, so 2^-34 turns at the last 31-bit position, where the fp32
 // product p w_i would be off by hundreds of radians.  What is left after the
-// nearest quarter turn, in [-1/8, 1/8] of a turn, goes to sincospi in fp32: sine and
-// cosine are off by a few 2^-25, the turned values by that times their pair's
+// nearest quarter turn, in [-1/8, 1/8] of a turn, goes through short series in fp32: sine
+// and cosine are off by less than 2^-23, the turned values by that times their pair's
 // size, in fp32; keys are rounded once, to their codes, other rows once, to
 // their type.
 //
@@ -25,15 +25,26 @@
 namespace dspark {
 namespace {
 
-// cosine and sine of a 64-bit fraction of a turn
+// Cosine and sine of a 64-bit fraction of a turn.  To the nearest quarter turn r is left, |r| <= 1/8, which is one
+// rounding off (2^-24 of it); then the Taylor series of sin(2 pi r) and cos(2 pi r) up to r^9 and r^10, whose rest is
+// below 2^-28.  The sine's first factor is in two parts, so that only r's rounding and the last sum's count: off by
+// less than 2^-23.6; the cosine's sum of terms, at most 0.3, is some four roundings off: less than 2^-23.2.
 __device__ __forceinline__ void turn(uint64_t phase, float &c, float &s) {
-    const uint32_t hi = (uint32_t)(phase >> 32);
-    const uint32_t quarter = (hi + 0x20000000u) >> 30;            // to the nearest
-    float c0, s0;
-    sincospif((float)(int)(hi - (quarter << 30)) * 0x1p-31f, &s0, &c0);
-    const float x = (quarter & 1) ? s0 : c0, y = (quarter & 1) ? c0 : s0;
-    c = (quarter == 1 || quarter == 2) ? -x : x;
-    s = quarter >= 2 ? -y : y;
+    constexpr double t = 6.283185307179586476925286766559, t2 = t * t;
+    constexpr float s1 = (float)t, s1_rest = (float)(t - (double)s1);
+    constexpr float s3 = (float)(-t * t2 / 6), s5 = (float)(t * t2 * t2 / 120), s7 = (float)(-t * t2 * t2 * t2 / 5040),
+                    s9 = (float)(t * t2 * t2 * t2 * t2 / 362880);
+    constexpr float c2 = (float)(-t2 / 2), c4 = (float)(t2 * t2 / 24), c6 = (float)(-t2 * t2 * t2 / 720),
+                    c8 = (float)(t2 * t2 * t2 * t2 / 40320), c10 = (float)(-t2 * t2 * t2 * t2 * t2 / 3628800);
+    const uint32_t hi = (uint32_t)(phase >> 32), quarter = hi + 0x20000000u & 0xc0000000u;
+    const float r = (float)(int)(hi - quarter) * 0x1p-32f, r2 = r * r;
+    const float sum = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, s9, s7), s5), s3), s1_rest);
+    const float s0 = fmaf(r, s1, r * sum);
+    const float c0 = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, c10, c8), c6), c4), c2), 1.f);
+    // a quarter turn on: (c, s) -> (-s, c)
+    const bool odd = quarter & 0x40000000u;
+    c = __uint_as_float(__float_as_uint(odd ? s0 : c0) ^ (quarter + 0x40000000u & 0x80000000u));
+    s = __uint_as_float(__float_as_uint(odd ? c0 : s0) ^ (quarter & 0x80000000u));
 }
 
 // A lane's eight elements of a head row: four first and four second partners
@@ -90,16 +101,21 @@ __device__ __forceinline__ int axis_of(const dspark_rotary &z, int pair) {
 // the angles of a lane's four pairs at a row's positions (or at `at`, where there are none)
 __device__ __forceinline__ void angles(const dspark_rotary &z, int pair, const int32_t *positions, int64_t n_rows, int64_t row,
                                        int64_t at, float (&c)[4], float (&s)[4]) {
+    const ulonglong2 lo = __ldg(reinterpret_cast<const ulonglong2 *>(z.step + pair));
+    const ulonglong2 hi = __ldg(reinterpret_cast<const ulonglong2 *>(z.step + pair) + 1);
+    const uint64_t steps[4] = {lo.x, lo.y, hi.x, hi.y};
+    if (positions && !z.axis) at = positions[row];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (positions) at = positions[axis_of(z, pair + i) * n_rows + row];
-        turn((uint64_t)at * z.step[pair + i], c[i], s[i]);
+        if (positions && z.axis) at = positions[axis_of(z, pair + i) * n_rows + row];
+        turn((uint64_t)at * steps[i], c[i], s[i]);
     }
 }
 
 // ---------------------------------------------------------------- rows alone --
-// A block takes `rows` consecutive rows, a thread an eighth-element group of one of
-// them for every `phases`-th head, four heads at a time.
+// A block takes `rows` consecutive rows, a thread eight elements of kRowsEach of them,
+// `rows` / kRowsEach apart, for every `phases`-th head: four heads at a time, or four rows
+// where there are few heads, so that enough loads are under way.
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;
 
@@ -111,46 +127,56 @@ struct TurnRows {
     bool inverse;
 };
 
-template <typename T, bool kAdjacent>
+template <typename T, bool kAdjacent, int kRowsEach>
 __global__ void __launch_bounds__(kRowThreads)
 rotary_rows_kernel(const __grid_constant__ TurnRows a, const T *x, T *out) {     // (may be the same rows)
+    constexpr int kHeadsEach = kRowUnroll / kRowsEach;
     const int at = (int)threadIdx.x / a.eighths, eighth = (int)threadIdx.x - at * a.eighths;
-    const int phase = at / a.rows, row = blockIdx.x * a.rows + at - phase * a.rows;
+    const int every = a.rows / kRowsEach, phase = at / every, row = blockIdx.x * a.rows + at - phase * every;
     if (phase >= a.phases || row >= a.n_rows) return;
     const Eighth e(eighth, a.z.n_pairs, kAdjacent);
-    const T *from = x + row * a.row_stride + phase * a.head_stride + e.off0;
+    const int64_t begin = row * a.row_stride + phase * a.head_stride + e.off0;
+    const T *from = x + begin;
     T *to = out + row * a.out_row_stride + phase * a.out_head_stride + e.off0;
     const int apart = e.off1 - e.off0;
-    const int64_t step = a.phases * a.head_stride, out_step = a.phases * a.out_head_stride;
+    // item j of a step: row j, or head j
+    const int64_t item = kRowsEach > 1 ? every * a.row_stride : a.phases * a.head_stride;
+    const int64_t out_item = kRowsEach > 1 ? every * a.out_row_stride : a.phases * a.out_head_stride;
+    const int64_t step = kHeadsEach * a.phases * a.head_stride, out_step = kHeadsEach * a.phases * a.out_head_stride;
+    auto there = [&](int h, int j) { return kRowsEach > 1 ? row + j * every < a.n_rows : h + j * a.phases < a.n_heads; };
     Four<T> in[kRowUnroll][2];
     auto load = [&](int h) {
 #pragma unroll
         for (int j = 0; j < kRowUnroll; ++j)
-            if (h + j * a.phases < a.n_heads) in[j][0].load(from + j * step), in[j][1].load(from + j * step + apart);
-        from += kRowUnroll * step;
+            if (there(h, j)) in[j][0].load(from + j * item), in[j][1].load(from + j * item + apart);
+        from += step;
     };
     load(phase);
-    float c[4], s[4];
+    float c[kRowsEach][4], s[kRowsEach][4];
     if (e.pair >= 0) {
-        angles(a.z, e.pair, a.positions, a.n_rows, row, 0, c, s);
-        if (a.inverse) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = -s[i];
+        for (int j = 0; j < kRowsEach; ++j) {
+            if (j > 0 && !there(0, j)) break;
+            angles(a.z, e.pair, a.positions, a.n_rows, row + j * every, 0, c[j], s[j]);
+            if (a.inverse) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[j][i] = -s[j][i];
+            }
         }
     }
-    for (int h = phase; h < a.n_heads; h += kRowUnroll * a.phases) {
+    for (int h = phase; h < a.n_heads; h += kHeadsEach * a.phases) {
         if (h > phase) load(h);
 #pragma unroll
         for (int j = 0; j < kRowUnroll; ++j) {
-            if (h + j * a.phases >= a.n_heads) break;
+            if (!there(h, j)) break;
             float y[8];
             in[j][0].get(y);
             in[j][1].get(y + 4);
-            if (e.pair >= 0) turn8<kAdjacent>(y, c, s);
-            Four<T>::store(to + j * out_step, y);
-            Four<T>::store(to + j * out_step + apart, y + 4);
+            if (e.pair >= 0) turn8<kAdjacent>(y, c[kRowsEach > 1 ? j : 0], s[kRowsEach > 1 ? j : 0]);
+            Four<T>::store(to + j * out_item, y);
+            Four<T>::store(to + j * out_item + apart, y + 4);
         }
-        to += kRowUnroll * out_step;
+        to += out_step;
     }
 }
 
@@ -308,29 +334,43 @@ void append_t(const AppendRotary &a, const void *q, const void *k, const void *v
     else append_pairs<T, DSPARK_KV_INT8, 16>(a, qt, kt, vt, ot, s);
 }
 
-template <typename T>
+template <typename T, int kRowsEach>
 void rows_t(const TurnRows &a, const void *x, void *out, cudaStream_t s) {
     const int blocks = (a.n_rows + a.rows - 1) / a.rows;
-    if (a.z.adjacent)
-        rotary_rows_kernel<T, true><<<blocks, kRowThreads, 0, s>>>(a, static_cast<const T *>(x), static_cast<T *>(out));
-    else
-        rotary_rows_kernel<T, false><<<blocks, kRowThreads, 0, s>>>(a, static_cast<const T *>(x), static_cast<T *>(out));
+    const T *from = static_cast<const T *>(x);
+    T *to = static_cast<T *>(out);
+    if (a.z.adjacent) rotary_rows_kernel<T, true, kRowsEach><<<blocks, kRowThreads, 0, s>>>(a, from, to);
+    else rotary_rows_kernel<T, false, kRowsEach><<<blocks, kRowThreads, 0, s>>>(a, from, to);
+}
+
+template <typename T>
+void rows_each(TurnRows a, const void *x, void *out, cudaStream_t s) {
+    // Heads of a row that a block takes side by side: a stretch of 1 KB, where they lie so (the turns of a row are made
+    // once for each; fp32 rows of 32 heads of 128 took 60 us without, 50 with four).
+    const int bytes = a.eighths * 8 * (int)sizeof(T);
+    int side = a.head_stride < a.row_stride ? (1024 + bytes - 1) / bytes : 1;
+    side = side < a.n_heads ? side : a.n_heads;
+    int most = kRowThreads / (a.eighths * side);
+    most = most > 1 ? most : 1;
+    // four rows a thread where there are fewer heads, and rows enough for every SM
+    const bool rows4 = a.n_heads <= 2 * side && (int64_t)a.n_rows >= (int64_t)most * kRowUnroll * 2 * kNumSMs;
+    const int even = (a.n_rows + 2 * kNumSMs - 1) / (2 * kNumSMs);
+    const int every = most < even ? most : even;
+    a.rows = rows4 ? kRowUnroll * every : every;
+    a.phases = kRowThreads / (every * a.eighths);
+    a.phases = a.phases < a.n_heads ? a.phases : a.n_heads;
+    if (rows4) rows_t<T, kRowUnroll>(a, x, out, s);
+    else rows_t<T, 1>(a, x, out, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary_rows(const RotaryRowsArgs &g, cudaStream_t s) {
-    // rows a block: as many as its threads hold, fewer where that would leave SMs without a block (then several
-    // threads share a row's heads)
-    const int eighths = g.head_dim / 8, most = kRowThreads / eighths, even = (g.n_rows + 2 * kNumSMs - 1) / (2 * kNumSMs);
-    const int rows = most < even ? most : even;
-    int phases = kRowThreads / (rows * eighths);
-    phases = phases < g.n_heads ? phases : g.n_heads;
     const TurnRows a{g.z, g.row_stride, g.head_stride, g.out_row_stride, g.out_head_stride, g.positions,
-                     g.n_rows, g.n_heads, eighths, rows, phases, g.inverse};
-    if (g.dt == DSPARK_BF16) rows_t<__nv_bfloat16>(a, g.x, g.out, s);
-    else if (g.dt == DSPARK_F16) rows_t<__half>(a, g.x, g.out, s);
-    else rows_t<float>(a, g.x, g.out, s);
+                     g.n_rows, g.n_heads, g.head_dim / 8, 1, 1, g.inverse};
+    if (g.dt == DSPARK_BF16) rows_each<__nv_bfloat16>(a, g.x, g.out, s);
+    else if (g.dt == DSPARK_F16) rows_each<__half>(a, g.x, g.out, s);
+    else rows_each<float>(a, g.x, g.out, s);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,7 @@ one unit in the last place of a value below 1.  A turned value is two fp32
 products and a sum: two roundings of 2^-24 of |a cos| + |b sin|.  In all (|a| + |b|)
 (2^-23 + 2^-23), and half a step of the output's type."""
 import math
+from fractions import Fraction
 
 import torch
 
@@ -18,16 +19,19 @@ def frequencies(n, base=10000.0):
 
 
 def angles(positions, freq, axis=None):
-    """[rows, pairs] angles in 64 bits of positions [axes, rows]: less whole turns by integers, so that the farthest
-    positions lose nothing."""
-    from fractions import Fraction
+    """[rows, pairs] angles in 64 bits of positions [axes, rows], less whole turns: the turns of a step are taken in
+    whole numbers of 2^-96 turns, three words of 32 bits, so that the farthest positions lose nothing."""
     pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
     out = torch.zeros((positions.shape[1], len(freq)), dtype=torch.float64)
+    word = 2 ** 32
     for i, w in enumerate(freq.tolist()):
-        turns = Fraction(w) / (2 * pi)
-        for r, p in enumerate(positions[0 if axis is None else axis[i]].tolist()):
-            t = p * turns
-            out[r, i] = float(t - round(t)) * 2 * math.pi
+        steps = round(Fraction(w) / (2 * pi) * 2 ** 96) % 2 ** 96
+        w0, w1, w2 = steps >> 64, steps >> 32 & word - 1, steps & word - 1
+        p = positions[0 if axis is None else axis[i]].long()
+        low = p * w1 + torch.div(p * w2, word, rounding_mode="floor")      # in 2^-64 turns
+        high = (p * w0 + torch.div(low, word, rounding_mode="floor")) % word
+        turns = (high.double() + (low % word).double() / word) / word
+        out[:, i] = torch.where(turns > 0.5, turns - 1, turns) * 2 * math.pi
     return out
 
 

@@ -36,6 +36,8 @@ CASES = [  # rows, heads, D, pairs, adjacent, axes
     (65, 4, 96, 20, False, 3),
     (40, 3, 256, 128, False, 1),
     (500, 9, 128, 16, True, 2),
+    (20011, 1, 64, 32, False, 1),
+    (40003, 2, 32, 12, True, 3),
 ]
 
 
