@@ -71,8 +71,9 @@ struct Divider {
 
 struct WindowArgs {
     AttentionArgs a;
-    Divider by_cluster, by_slots, by_heads, by_group, by_page;      // the last: chunks a page
-    int slots;          // row blocks of a request that have blocks of their own; more follow in a loop
+    Divider by_cluster, by_heads, by_group, by_page;     // the last: chunks a page
+    bool listed;        // items in the order of packed rows (see slot_of), or one for each request and head, of which
+                        // more row blocks follow in a loop
     int cluster;        // blocks an item's tokens are split over
 };
 
@@ -196,6 +197,25 @@ struct View {
     int64_t first;                              // packed row of the request's first
 };
 
+// Row blocks of requests of any lengths, each of `rows` rows: request b's first one has number
+// row0[b] group / rows + b, which leaves at least as many numbers as it has blocks up to the next request's.
+__device__ __forceinline__ int64_t slot_of(int64_t row0, int b, int group, int rows) {
+    return (int64_t)((uint64_t)row0 * (uint64_t)group / (uint64_t)rows) + b;
+}
+// the largest b whose first number is `slot` or less, by the whole warp (32 probes a round); -1: none
+__device__ __forceinline__ int find_slot(const int64_t *__restrict__ row0, int B, int64_t slot, int group, int rows, int lane) {
+    int lo = 0, n = B;
+    while (true) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const unsigned hits = __ballot_sync(0xffffffffu, i < n && slot_of(row0[lo + i], lo + i, group, rows) <= slot);
+        if (hits == 0) return -1;
+        const int k = 31 - __clz(hits);
+        lo += k * step;
+        n = min(step, n - k * step);
+        if (step == 1) return lo;
+    }
+}
+
 template <typename T, int kFormat, int DP, int N>
 __global__ void __launch_bounds__(kThreads, Shape<DP, N>::kBlocks)
 window_kernel(const __grid_constant__ WindowArgs w) {
@@ -224,15 +244,26 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     View &view = views[warp];
     int m0;
     {
-        int slot, head;
-        item = w.by_slots.div(item, slot);
-        const int b = w.by_heads.div(item, head);
+        int head, b;
+        const int slot = w.by_heads.div(item, head);
+        if (w.listed) {
+            b = find_slot(a.rows.row0, a.rows.B, slot, group, kRows, lane);
+            if (b < 0) b = 0;
+        } else {
+            b = slot;
+        }
         const Request q = load_request(a, b);
         if (lane == 0) view.b = b, view.head = head, view.first = q.first, view.n = q.n;
-        m0 = slot * kRows;
+        // (no row0 that is no good may lead past a request's rows)
+        const int64_t at = w.listed && q.rows_ok ? (slot - slot_of(q.first, b, group, kRows)) * kRows : 0;
+        m0 = at >= 0 && at < (int64_t)q.n * group ? (int)at : q.n * group;
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < a.rows.B; i += kThreads) {
+                const Request x = load_request(a, i);
+                if (!x.rows_ok || (x.n > 0 && !x.len_ok)) atomicOr(c.flags, kFlagBadLength);
+            }
         if (!q.rows_ok || (q.n > 0 && !q.len_ok)) {     // no rows, or rows of NaN
-            if (slot == 0 && head == 0 && split == 0 && threadIdx.x == 0) atomicOr(c.flags, kFlagBadLength);
-            if (slot == 0 && split == 0)
+            if (m0 == 0 && split == 0)
                 for (int i = threadIdx.x; i < q.n * group * (D / 8); i += kThreads) {
                     const int m = i / (D / 8), blk = m / group;
                     const int64_t place = (q.first + blk) * a.n_q_heads + head * group + (m - blk * group);
@@ -654,7 +685,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             }
             cluster.sync();     // before another block's memory goes, or is written again
         }
-        m0 = view.m0 + w.slots * kRows;
+        m0 = w.listed ? view.n * group : view.m0 + kRows;
         if (m0 >= view.n * group) break;
         __syncthreads();        // the ring, the ranges and the queries are the next rows'
         if (D != DP) {
@@ -663,6 +694,13 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             __syncthreads();
         }
     }
+}
+
+// tokens of a request that its rows see at most (of an average block)
+int64_t seen_tokens(const AttentionArgs &a) {
+    const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len;
+    const int64_t seen = (int64_t)a.window + a.sinks + a.rows.n_rows / a.rows.B;
+    return own < seen ? own : seen;
 }
 
 template <typename T, int kFormat, int DP, int N>
@@ -674,20 +712,18 @@ cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const AttentionArgs &a = w.a;
     const int group = a.n_q_heads / a.cache.n_kv_heads;
-    // row blocks of an average request, which one block each takes at once
-    const int64_t rows = ((int64_t)a.rows.n_rows + a.rows.B - 1) / a.rows.B * group;
-    w.slots = (int)(((a.rows.n_rows > a.rows.B ? rows * 3 / 2 : rows) + 8 * N - 1) / (8 * N));
+    // a row a request is what decoding has: no list is needed then (and none is looked through)
+    w.listed = a.rows.n_rows > a.rows.B;
     // an item's tokens go to a cluster of up to 8 blocks while there are fewer blocks than SMs hold and a warp has
     // four chunks or more
-    int64_t blocks = (int64_t)a.rows.B * a.cache.n_kv_heads * w.slots;
-    const int64_t own = (int64_t)a.rows.max_pages * a.cache.page_size + a.prefix_len, seen = (int64_t)a.window + a.sinks;
-    const int64_t chunks = (own < seen ? own : seen) / kChunk;
+    const int64_t items = w.listed ? (int64_t)a.rows.n_rows * group / (8 * N) + a.rows.B : a.rows.B;
+    int64_t blocks = items * a.cache.n_kv_heads;
+    const int64_t chunks = seen_tokens(a) / kChunk;
     w.cluster = 1;
     while (w.cluster < kMaxCluster && blocks * w.cluster * 2 <= (int64_t)kNumSMs * Shape<DP, N>::kBlocks && chunks >= w.cluster * 2 * kWarps * 4)
         w.cluster *= 2;
     blocks *= w.cluster;
     w.by_cluster = Divider(w.cluster);
-    w.by_slots = Divider(w.slots);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -722,19 +758,24 @@ cudaError_t launch_t(WindowArgs &w, cudaStream_t s) {
 
 }  // namespace
 
-// Blocks with many rows go to the 128-row tiles of the tensor cores.
-static bool many_rows(int B, int n_rows, int n_q_heads, int n_kv_heads) {
+// Blocks with many rows of a kv head go to the 128-row tiles of the tensor cores (window_blocks.cu) when there is
+// enough to do: those start later (55 us before the first result) and an item costs them more, then a tile less.
+// Measured, rows a kv head x requests, window 1,024, D = 128 (here / there, us): 64 x 64 111 / 152, 128 x 64 196 / 167,
+// 256 x 64 358 / 187, 512 x 64 692 / 307, 128 x 8 34 / 89, 256 x 8 62 / 76, 512 x 8 104 / 82, 1,024 x 1 34 / 70;
+// window 128: 256 x 64 154 / 111, window 8,000: 128 x 32 594 / 361.
+static bool may_be_many(int B, int n_rows, int n_q_heads, int n_kv_heads) {
     return ((int64_t)n_rows + B - 1) / B * (n_q_heads / n_kv_heads) >= 128;
 }
-
 size_t window_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim) {
-    return many_rows(B, n_rows, n_q_heads, n_kv_heads) ? window_blocks_ws_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) : 0;
+    return may_be_many(B, n_rows, n_q_heads, n_kv_heads) ? window_blocks_ws_bytes(B, n_rows, n_q_heads, n_kv_heads, head_dim) : 0;
 }
 
 cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s) {
-    if (many_rows(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.n_kv_heads)) return launch_window_blocks(a, s);
-    WindowArgs w{a, Divider(), Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
-                 Divider(a.cache.page_size / kChunk), 1, 1};
+    if (may_be_many(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.n_kv_heads) &&
+        (double)a.rows.n_rows * a.n_q_heads * (double)(seen_tokens(a) + 256) >= 40e6)
+        return launch_window_blocks(a, s);
+    WindowArgs w{a, Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
+                 Divider(a.cache.page_size / kChunk), false, 1};
     return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
 }
 

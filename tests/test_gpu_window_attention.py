@@ -271,3 +271,35 @@ def test_pages_beyond_32_bits_of_codes():
     got = binding.window_attention(q.cuda(), cache, torch.tensor([[last]], dtype=torch.int32).cuda(),
                                    torch.tensor([40]).int().cuda(), torch.tensor([0, 2]).cuda(), window=30, sinks=1)
     _check(got, plain_window.attention(q, pool, torch.tensor([0, 2]), [40], 30, 1))
+
+
+@pytest.mark.parametrize("B", [70, 1100])
+def test_a_long_block_among_many_short_ones(B):
+    """Requests without rows, of one row and one of 90: every row is some block's, whatever the average."""
+    rows = [(b % 3) for b in range(B)]
+    rows[B // 2] = 90
+    _run(rows, [(37 * b) % 200 for b in range(B)], 20, 4, 2, 64, 16, 33, 4)
+
+
+def test_as_many_rows_as_requests_but_not_one_each():
+    _run([0, 5, 0, 0, 0, 2, 0], [9, 200, 3, 50, 0, 129, 4], 30, 8, 2, 64, 16, 50, 5)
+
+
+def test_row_starts_that_are_no_good():
+    """Flagged; the requests between good ones keep their results."""
+    gen = torch.Generator().manual_seed(8)
+    lens = [30, 40, 50]
+    pool = plain_cache.Pool(gen, lens, 0, 2, 64, 16, E4M3)
+    q = torch.randn((9, 4, 64), generator=gen).to(BF16)
+    row0 = torch.tensor([0, 4, 2, 6])       # request 1 ends before it begins
+    cache = pool.cache(binding)
+    out = dict(out=torch.full((9, 4, 64), 7.0, dtype=BF16, device="cuda"))
+    binding.window_attention(q.cuda(), cache, pool.table.cuda(), torch.tensor(lens).int().cuda(), row0.cuda(), window=20, out=out)
+    torch.cuda.synchronize()
+    assert binding.read_device_flags(cache.flags) == binding.FLAG_BAD_LENGTH
+    assert bool((out["out"][6:] == 7).all())
+    for bad in (torch.tensor([-3, 2, 4, 6]), torch.tensor([0, 2, 4, 1 << 40])):
+        cache.flags.zero_()
+        binding.window_attention(q.cuda(), cache, pool.table.cuda(), torch.tensor(lens).int().cuda(), bad.cuda(), window=20, out=out)
+        torch.cuda.synchronize()
+        assert binding.read_device_flags(cache.flags) == binding.FLAG_BAD_LENGTH
