@@ -1362,22 +1362,20 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
 // bounds it is reading the parts.
 constexpr int kJoinWarps = 8, kJoinRows = 4;
 
+#ifdef DSPARK_WINDOW_BLOCKS
+#include "window_join.cuh"
+#else
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32, kWindow ? 4 : 1)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials parts, const int per) {
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, b = blockIdx.x;
     const dspark_kv_cache &c = a.cache;
     const int D = c.head_dim, group = a.n_q_heads / c.n_kv_heads, Hq = a.n_q_heads;
-    int b = blockIdx.x;
-    Request q = load_request(a, b);
-    const int prefix_m = prefix_rows(a) * group;
-    const int prefix_tiles = prefix_tiles_of(a, kWindow ? *parts.prefix_low : 0);
-    // without a prefix only items that a worker left unfinished are joined, in steps of kUnit rows a block
-    constexpr int kUnit = 64, kUnits = plan::kTileRows / kUnit;
-    const bool listed = kWindow && prefix_tiles == 0;
-    if (q.n == 0 && !listed) return;
+    const Request q = load_request(a, b);
+    if (q.n == 0) return;
     // the line: units of the prefix by class, of all pairs, of all (the last request's end)
+    const int prefix_m = prefix_rows(a) * group, prefix_tiles = plan::token_tiles(a.prefix_len);
     int64_t prefix[2], pairs, total;
     {
         const int last = a.rows.B - 1;
@@ -1387,54 +1385,20 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         for (int k = 0; k < 2; ++k) {
             prefix[k] = plan::head_units(k, prefix_m, prefix_tiles) * c.n_kv_heads;
             end[k] = prefix[k] + parts.unit0[k][last] +
-                     (z.len_ok && z.n > 0
-                          ? plan::head_units(k, z.n * group, own_tiles(a, z.n, z.len, group)) * c.n_kv_heads
-                          : 0);
+                     (z.len_ok && z.n > 0 ? plan::head_units(k, z.n * group, plan::token_tiles(z.len)) * c.n_kv_heads : 0);
         }
         pairs = end[0];
         total = end[0] + end[1];
     }
+    const int64_t own0 = parts.unit0[0][b] + prefix[0], own1 = parts.unit0[1][b] + prefix[1];
     const int64_t all = (int64_t)a.rows.n_rows * Hq;
-    auto bad_row = [&](int64_t place) {
-        T *out = static_cast<T *>(a.out) + place * D;
-        if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-        if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
-    };
-    if (listed && blockIdx.y == 0 && !q.len_ok)
-        for (int i = warp; i < q.n * Hq; i += kJoinWarps) bad_row(q.first * Hq + i);
+    const int own_m = q.n * group, chunks = (own_m + per - 1) / per;
     // this lane's item (0 the prefix's, 1 the request's own) and its place among the item's workers
     const int side = lane >> 4, at = lane & 15;
-    int64_t own0, own1;
-    int own_m, m_of, rows, tiles;
-    auto of_request = [&]() {
-        own0 = parts.unit0[0][b] + prefix[0], own1 = parts.unit0[1][b] + prefix[1];
-        own_m = q.n * group;
-        m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
-        tiles = side ? own_tiles(a, q.n, q.len, group) : prefix_tiles;
-    };
-    if (!listed) of_request();
-    const int chunks = listed ? 0 : (own_m + per - 1) / per;
-    const int from = listed ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.y * kJoinWarps + warp;
-    const int step = listed ? gridDim.x * gridDim.y : gridDim.y * kJoinWarps;
-    const int jobs = listed ? 3 * kCtas * kUnits : c.n_kv_heads * chunks;
-    for (int i = from; i < jobs; i += step) {
-        int h = 0, m0, m1, every = 1;
-        if (listed) {
-            const int4 record = parts.split[i / kUnits];
-            const int first = i % kUnits * kUnit;
-            if (record.x < 0 || first >= record.w) continue;
-            b = record.x;
-            q = load_request(a, b);
-            of_request();
-            h = record.y;
-            m0 = record.z + first + warp;
-            m1 = record.z + min(first + kUnit, record.w);
-            every = kJoinWarps;
-        } else {
-            h = i / chunks;
-            m0 = (i - h * chunks) * per;
-            m1 = min(m0 + per, own_m);
-        }
+    const int m_of = side ? 0 : (int)q.first * group, rows = side ? own_m : prefix_m;
+    const int tiles = side ? plan::token_tiles(q.len) : prefix_tiles;
+    for (int i = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); i < c.n_kv_heads * chunks; i += gridDim.y * kJoinWarps) {
+        const int h = i / chunks, m0 = (i - h * chunks) * per, m1 = min(m0 + per, own_m);
         int item = -1;             // the row tile that is looked at
         bool has = false, first = false, more = false, done = false;
         int64_t part0 = 0;
@@ -1464,12 +1428,13 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
             more = __any_sync(0xffffffffu, go_on);
             if (turn == 0) done = __any_sync(0xffffffffu, side && alone && prefix_tiles == 0);
         };
-        for (int m = m0; m < m1; m += every) {
+        for (int m = m0; m < m1; ++m) {
             const int blk = m / group;
             const int64_t place = (q.first + blk) * Hq + h * group + (m - blk * group);
             T *out = static_cast<T *>(a.out) + place * D;
             if (!q.len_ok) {
-                bad_row(place);
+                if (lane * 4 < D) *reinterpret_cast<uint2 *>(out + lane * 4) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+                if (lane == 0 && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
                 continue;
             }
             const int mt = m_of + m, now = mt / plan::kTileRows;
@@ -1528,6 +1493,7 @@ attention_join_kernel(const __grid_constant__ AttentionArgs a, const Partials pa
         }
     }
 }
+#endif
 
 struct Regions {
     size_t unit1, stats, o, split, low, bytes;
