@@ -1,16 +1,17 @@
 """Decoding rounds with a target model's attention in them.
 
-    python examples/target_pass.py [--rounds 8] [--batch 64] [--prompt 1000]
+    python examples/target_pass.py [--rounds 8] [--batch 64] [--prompt 1000] [--rotary] [--window 256 --sinks 4]
 
-A target of one attention layer (no positions, so a token's query, key and
-value are rows of three tables) answers a batch of requests that share a
-prompt.  The prompt enters the quantised cache once, on pages that every
+A target of one attention layer (a token's query, key and value are rows of
+three tables; with --rotary turned by the token's position) answers a batch of
+requests that share a prompt.  The prompt enters the quantised cache once, on pages that every
 request's attention reads.  Each round then
 
   1. drafts a block per request and schedules how much of it to verify,
   2. packs the anchor and the scheduled tokens of every request into rows,
   3. writes their keys and values behind the request's own cached tokens,
-  4. lets every row attend to the prompt, the own tokens and its block,
+  4. lets every row attend to the prompt, the own tokens and its block (with
+     --window to the last tokens of these and the first --sinks ones),
   5. verifies the drafted tokens with the logits of these rows.
 
 The tokens that the verification rejects leave nothing to undo: the next round
@@ -44,7 +45,8 @@ class Target:
         return attended.flatten(1) @ self.unembed.t() / 16
 
 
-def run(rounds=8, B=64, prompt=1000, G=5, V=4096, r=64, Hq=16, Hkv=4, D=128, page=64, dtype=torch.float8_e4m3fn, seed=0):
+def run(rounds=8, B=64, prompt=1000, G=5, V=4096, r=64, Hq=16, Hkv=4, D=128, page=64, dtype=torch.float8_e4m3fn, seed=0,
+        rotary=False, window=None, sinks=0):
     """Runs ``rounds`` rounds; returns dict(target, cache, prompt, pages, block_table, tokens, length): ``tokens``
     [B, rounds * (G + 1) + 1] what each request was given, -1 padded, the first ``length`` of them cached."""
     dev = torch.device("cuda")
@@ -66,8 +68,13 @@ def run(rounds=8, B=64, prompt=1000, G=5, V=4096, r=64, Hq=16, Hkv=4, D=128, pag
     cache = binding.KVCache.empty(order.numel(), Hkv, page, D, dtype=dtype, device=dev)
     given = torch.randint(V, (prompt,), generator=gen, device=dev)
     zero = torch.zeros(1, dtype=torch.int32, device=dev)
-    binding.kv_append(target.k[given], target.v[given], cache, pages[None], zero,
-                      torch.tensor([0, prompt], device=dev))
+    # (D / 2 pairs, the usual frequencies)
+    turn = binding.Rotary(10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))) if rotary else None
+    prompt_row0 = torch.tensor([0, prompt], device=dev)
+    if rotary:
+        binding.kv_append_rotary(target.k[given], target.v[given], cache, pages[None], zero, prompt_row0, turn)
+    else:
+        binding.kv_append(target.k[given], target.v[given], cache, pages[None], zero, prompt_row0)
 
     n = B * (G + 1)
     j = torch.arange(G + 1, device=dev)
@@ -85,9 +92,17 @@ def run(rounds=8, B=64, prompt=1000, G=5, V=4096, r=64, Hq=16, Hkv=4, D=128, pag
         to = torch.where(j <= verify_len[:, None], row0[:-1, None] + j, n)  # row n takes what is not verified
         rows = torch.zeros(n + 1, dtype=torch.int64, device=dev).scatter_(0, to.flatten(), block.flatten())[:n]
 
-        binding.kv_append(target.k[rows], target.v[rows], cache, block_table, length, row0)
-        att = binding.block_attention(target.q[rows], cache, block_table, length + verify_len + 1, row0,
-                                      prefix_pages=pages, prefix_len=prompt)
+        q = target.q[rows]
+        if rotary:
+            binding.kv_append_rotary(target.k[rows], target.v[rows], cache, block_table, length, row0, turn, q=q, out=q,
+                                     offset=prompt)
+        else:
+            binding.kv_append(target.k[rows], target.v[rows], cache, block_table, length, row0)
+        seen = (q, cache, block_table, length + verify_len + 1, row0)
+        if window:
+            att = binding.window_attention(*seen, window=window, sinks=sinks, prefix_pages=pages, prefix_len=prompt)
+        else:
+            att = binding.block_attention(*seen, prefix_pages=pages, prefix_len=prompt)
         out = binding.verify(target.logits(att["out"]), base, e_in, w_out, anchor, draft, verify_len, temperature,
                              seed=seed + t, target_row0=row0[:-1])
 
@@ -107,8 +122,11 @@ def main():
     ap.add_argument("--rounds", type=int, default=8)
     ap.add_argument("--batch", type=int, default=64)
     ap.add_argument("--prompt", type=int, default=1000)
+    ap.add_argument("--rotary", action="store_true")
+    ap.add_argument("--window", type=int)
+    ap.add_argument("--sinks", type=int, default=0)
     a = ap.parse_args()
-    r = run(a.rounds, a.batch, a.prompt)
+    r = run(a.rounds, a.batch, a.prompt, rotary=a.rotary, window=a.window, sinks=a.sinks)
     flags = binding.read_device_flags(r["cache"].flags)
     total = int(r["length"].sum())
     print("%d requests, %d rounds, %d tokens given (%.2f a request and round), cache flags %d"

@@ -74,6 +74,7 @@ struct WindowArgs {
     Divider by_cluster, by_heads, by_group, by_page;     // the last: chunks a page
     bool listed;        // items in the order of packed rows (see slot_of), or one for each request and head, of which
                         // more row blocks follow in a loop
+    float requests_a_slot;
     int cluster;        // blocks an item's tokens are split over
 };
 
@@ -202,9 +203,14 @@ struct View {
 __device__ __forceinline__ int64_t slot_of(int64_t row0, int b, int group, int rows) {
     return (int64_t)((uint64_t)row0 * (uint64_t)group / (uint64_t)rows) + b;
 }
-// the largest b whose first number is `slot` or less, by the whole warp (32 probes a round); -1: none
-__device__ __forceinline__ int find_slot(const int64_t *__restrict__ row0, int B, int64_t slot, int group, int rows, int lane) {
-    int lo = 0, n = B;
+// the largest b whose first number is `slot` or less, by the whole warp: 32 probes around `guess`, which nearly
+// always hold it, else 32 a round; -1: none
+__device__ __forceinline__ int find_slot(const int64_t *__restrict__ row0, int B, int64_t slot, int group, int rows, int guess,
+                                         int lane) {
+    int lo = max(min(guess - 16, B - 32), 0), n = B;
+    const unsigned near = __ballot_sync(0xffffffffu, lo + lane < B && slot_of(row0[lo + lane], lo + lane, group, rows) <= slot);
+    if (near != 0 && (near != 0xffffffffu || lo + 32 >= B)) return lo + 31 - __clz(near);
+    lo = 0;
     while (true) {
         const int step = (n + 31) / 32, i = lane * step;
         const unsigned hits = __ballot_sync(0xffffffffu, i < n && slot_of(row0[lo + i], lo + i, group, rows) <= slot);
@@ -247,7 +253,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
         int head, b;
         const int slot = w.by_heads.div(item, head);
         if (w.listed) {
-            b = find_slot(a.rows.row0, a.rows.B, slot, group, kRows, lane);
+            b = find_slot(a.rows.row0, a.rows.B, slot, group, kRows, (int)((float)slot * w.requests_a_slot), lane);
             if (b < 0) b = 0;
         } else {
             b = slot;
@@ -717,6 +723,7 @@ cudaError_t launch_n(WindowArgs &w, cudaStream_t s) {
     // an item's tokens go to a cluster of up to 8 blocks while there are fewer blocks than SMs hold and a warp has
     // four chunks or more
     const int64_t items = w.listed ? (int64_t)a.rows.n_rows * group / (8 * N) + a.rows.B : a.rows.B;
+    w.requests_a_slot = (float)a.rows.B / (float)items;
     int64_t blocks = items * a.cache.n_kv_heads;
     const int64_t chunks = seen_tokens(a) / kChunk;
     w.cluster = 1;
@@ -775,7 +782,7 @@ cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s) {
         (double)a.rows.n_rows * a.n_q_heads * (double)(seen_tokens(a) + 256) >= 40e6)
         return launch_window_blocks(a, s);
     WindowArgs w{a, Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
-                 Divider(a.cache.page_size / kChunk), false, 1};
+                 Divider(a.cache.page_size / kChunk), false, 0.f, 1};
     return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
 }
 
