@@ -592,7 +592,7 @@ DSPARK_API size_t dspark_window_workspace_bytes(int B, int n_rows, int n_q_heads
  *
  * Everything else, scales, results, roundings, flags and limits, as
  * dspark_block_attention; window >= 1, sinks >= 0, and prefix_len +
- * max_pages * page_size below 2^31.
+ * max_pages * page_size at most 2^31 - 256.
  */
 DSPARK_API dspark_status dspark_window_attention(
     const dspark_kv_cache *cache, const void *q, int64_t q_stride, dspark_dtype dtype, int n_q_heads,

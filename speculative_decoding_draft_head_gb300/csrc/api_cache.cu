@@ -212,8 +212,8 @@ dspark_status dspark_window_attention(const dspark_kv_cache *cache, const void *
         return fail(DSPARK_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0 (got %d, %d)", window, sinks);
     if (row_mask && window < 64)
         return fail(DSPARK_ERR_INVALID_ARG, "window must be at least 64 with row_mask (got %d)", window);
-    if ((int64_t)max_pages * cache->page_size + prefix_len > 0x7fffffff)
-        return fail(DSPARK_ERR_INVALID_ARG, "prefix_len + max_pages * page_size passes 2^31 - 1 tokens");
+    if ((int64_t)max_pages * cache->page_size + prefix_len > 0x7fffff00)
+        return fail(DSPARK_ERR_INVALID_ARG, "prefix_len + max_pages * page_size passes 2^31 - 256 tokens");
     if (nothing) return DSPARK_OK;
     a.window = window;
     a.sinks = sinks;

@@ -303,3 +303,33 @@ def test_row_starts_that_are_no_good():
         binding.window_attention(q.cuda(), cache, pool.table.cuda(), torch.tensor(lens).int().cuda(), bad.cuda(), window=20, out=out)
         torch.cuda.synchronize()
         assert binding.read_device_flags(cache.flags) == binding.FLAG_BAD_LENGTH
+
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("rows,ctx,prefix,Hq,Hkv,D,page,window,sinks", [
+    ([1], [9000], 0, 4, 1, 96, 48, 8000, 40),
+    ([1, 1], [5000, 3], 700, 8, 2, 80, 16, 5200, 4),
+    ([2], [4000], 0, 8, 1, 128, 64, 3900, 1),          # 16 rows of a kv head
+    ([3], [4000], 900, 8, 1, 128, 64, 4500, 1000),     # 24
+    ([5, 0], [4000, 7], 0, 20, 2, 64, 32, 3000, 4),    # 50: several row blocks
+])
+def test_few_rows_over_long_windows(rows, ctx, prefix, Hq, Hkv, D, page, window, sinks, fmt):
+    """An item's tokens are split over a cluster's blocks."""
+    _run(rows, ctx, prefix, Hq, Hkv, D, page, window, sinks, fmt=fmt)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Of blocks with many rows, whose launches meet in a workspace: each stream's is its own."""
+    shape = ([260, 300, 90, 280], [500, 300, 700, 0], 0, 16, 2, 128, 64, 900, 4)
+    got, q, pool, row0, lens = _run(*shape)
+    cache, args = pool.cache(binding), (pool.table.cuda(), torch.tensor(lens).int().cuda(), row0.cuda())
+    assert binding.window_workspace_bytes(4, q.shape[0], 16, 2, 128) > 0
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    qs = [q.cuda(), (q * 2).cuda()]
+    want = [binding.window_attention(x, cache, *args, window=900, sinks=4) for x in qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [binding.window_attention(x, cache, *args, window=900, sinks=4, stream=s) for x, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
