@@ -317,19 +317,3 @@ def test_few_rows_over_long_windows(rows, ctx, prefix, Hq, Hkv, D, page, window,
     """An item's tokens are split over a cluster's blocks."""
     _run(rows, ctx, prefix, Hq, Hkv, D, page, window, sinks, fmt=fmt)
 
-
-def test_two_calls_at_once_on_two_streams():
-    """Of blocks with many rows, whose launches meet in a workspace: each stream's is its own."""
-    shape = ([260, 300, 90, 280], [500, 300, 700, 0], 0, 16, 2, 128, 64, 900, 4)
-    got, q, pool, row0, lens = _run(*shape)
-    cache, args = pool.cache(binding), (pool.table.cuda(), torch.tensor(lens).int().cuda(), row0.cuda())
-    assert binding.window_workspace_bytes(4, q.shape[0], 16, 2, 128) > 0
-    streams = [torch.cuda.Stream() for _ in range(2)]
-    qs = [q.cuda(), (q * 2).cuda()]
-    want = [binding.window_attention(x, cache, *args, window=900, sinks=4) for x in qs]
-    torch.cuda.synchronize()
-    for _ in range(5):
-        outs = [binding.window_attention(x, cache, *args, window=900, sinks=4, stream=s) for x, s in zip(qs, streams)]
-        torch.cuda.synchronize()
-        for a, b in zip(outs, want):
-            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
