@@ -257,6 +257,7 @@ size_t attention_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int 
 cudaError_t launch_block_attention(const AttentionArgs &a, cudaStream_t s);
 size_t window_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s);
+cudaError_t launch_window_rows_f16(const AttentionArgs &a, cudaStream_t s);   // its fp16 rows
 // its blocks with many rows
 size_t window_blocks_ws_bytes(int B, int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_window_blocks(const AttentionArgs &a, cudaStream_t s);

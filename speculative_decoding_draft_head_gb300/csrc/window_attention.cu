@@ -763,8 +763,18 @@ cudaError_t launch_t(WindowArgs &w, cudaStream_t s) {
     return e4m3 ? launch_dp<T, DSPARK_KV_E4M3, 128>(w, s) : launch_dp<T, DSPARK_KV_INT8, 128>(w, s);
 }
 
+template <typename T>
+cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
+    WindowArgs w{a, Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
+                 Divider(a.cache.page_size / kChunk), false, 0.f, 1};
+    return launch_t<T>(w, s);
+}
+
 }  // namespace
 
+#ifdef DSPARK_WINDOW_F16
+cudaError_t launch_window_rows_f16(const AttentionArgs &a, cudaStream_t s) { return launch_rows<__half>(a, s); }
+#else
 // Blocks with many rows of a kv head go to the 128-row tiles of the tensor cores (window_blocks.cu) when there is
 // enough to do: those start later (55 us before the first result) and an item costs them more, then a tile less.
 // Measured, rows a kv head x requests, window 1,024, D = 128 (here / there, us): 64 x 64 111 / 152, 128 x 64 196 / 167,
@@ -781,9 +791,8 @@ cudaError_t launch_window_attention(const AttentionArgs &a, cudaStream_t s) {
     if (may_be_many(a.rows.B, a.rows.n_rows, a.n_q_heads, a.cache.n_kv_heads) &&
         (double)a.rows.n_rows * a.n_q_heads * (double)(seen_tokens(a) + 256) >= 40e6)
         return launch_window_blocks(a, s);
-    WindowArgs w{a, Divider(), Divider(a.cache.n_kv_heads), Divider(a.n_q_heads / a.cache.n_kv_heads),
-                 Divider(a.cache.page_size / kChunk), false, 0.f, 1};
-    return a.dt == DSPARK_BF16 ? launch_t<__nv_bfloat16>(w, s) : launch_t<__half>(w, s);
+    return a.dt == DSPARK_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_window_rows_f16(a, s);
 }
+#endif
 
 }  // namespace dspark
