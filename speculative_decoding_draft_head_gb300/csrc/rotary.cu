@@ -115,7 +115,11 @@ __device__ __forceinline__ void angles(const dspark_rotary &z, int pair, const i
 // ---------------------------------------------------------------- rows alone --
 // A block takes `rows` consecutive rows, a thread eight elements of kRowsEach of them,
 // `rows` / kRowsEach apart, for every `phases`-th head: four heads at a time, or four rows
-// where there are few heads, so that enough loads are under way.
+// where there are few heads, so that enough loads are under way.  Measured: 60,001 rows of
+// 16 heads of 80 bf16 elements, heads first, 51 us (6.0 TB/s, 89% of a copy's rate); 9,000
+// rows of 32 heads of 128 fp32 elements 50 us (5.9 TB/s); 200,000 rows of one head of
+// 128 bf16 elements 41 us (2.5 TB/s): there the sines and cosines, one for two elements,
+// are what bounds it.
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;
 
@@ -186,7 +190,14 @@ rotary_rows_kernel(const __grid_constant__ TurnRows a, const T *x, T *out) {    
 // and quantised; of the values, quantised.  Each warp has rows of its own, or
 // (`phases` > 1) several warps, of a block and of several, share the steps of the
 // same rows.  The one-off work of a quantised head row, its maximum's exchange and two
-// divisions, is done for four at once, by a lane each.
+// divisions, is done for four at once, by a lane each; a step's rows are loaded during
+// the one before.
+//
+// Measured (one GB300, cold caches): 55,000 tokens of 13 prompts, 32 query and 8 kv heads of
+// 128 bf16 elements, 201 us (6.3 TB/s, 93% of a copy's rate); with sines and cosines in
+// shared memory and made for four rows a block 258 us.  Blocks an SM (by registers): four
+// 209 us, five 201, six 209 (spills); of fp32 rows four 352, five 360.  One token of 32
+// requests: 6.2 us, of a Python call's 15.
 constexpr int kAppendThreads = 128;
 
 struct AppendRotary {
@@ -199,7 +210,7 @@ struct AppendRotary {
 };
 
 template <typename T, int kFormat, int kLanes, bool kAdjacent>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 4 : 5)
 kv_append_rotary_kernel(const __grid_constant__ AppendRotary a, const T *q, const T *__restrict__ k,
                         const T *__restrict__ v, T *q_out) {
     constexpr float kTop = kFormat == DSPARK_KV_E4M3 ? 448.f : 127.f;

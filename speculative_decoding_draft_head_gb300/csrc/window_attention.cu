@@ -34,6 +34,18 @@
 //     of rows 2 t and 2 t + 1.
 // In shared memory 16-byte pieces of a chunk are permuted so that neither read
 // meets itself in a bank.
+//
+// What bounds it.  With 8 rows an item, memory: 64 single tokens of 64 heads over 4,100 of
+// their up to 20,000 tokens in 82 us (5.8 TB/s, 85% of a copy's rate).  With more, the
+// issue of instructions, of which the half-rate integer pipe has half: some 320 a chunk for 16 rows (64
+// of them conversions) and 1,250 a warp and item for its start and its joining; 256
+// blocks of 1 to 6 rows of 32 heads over 1,040 tokens in 121 us (4.3 TB/s).  What
+// counted on the way: bounds looked at only where a chunk is an edge (209 -> 167 us for
+// those blocks), queries in shared memory and row blocks that do not exist left out
+// (142), what the loop does not need out of its registers (130), divisions by
+// multiplication and a joining without any (118; 121 with items in the order of packed
+// rows).  Two chunks a step, for two chains of products at once, took 193 us: the loop
+// leaves the instruction cache.  8, 12 or 16 warps an SM make no difference.
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -82,7 +94,7 @@ struct WindowArgs {
 template <int DP, int N>
 struct Shape {
     static constexpr int kAcc = DP / 64 * N;       // sixteens of a lane's sums
-    static constexpr int kBlocks = kAcc <= 2 ? 4 : kAcc <= 4 ? 4 : 3;
+    static constexpr int kBlocks = kAcc <= 4 ? 4 : 3;
     static constexpr int kStages = 3;
 };
 template <int DP>
@@ -236,7 +248,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     __shared__ float2 stats[kWarps + 1][kRows];   // (r, l) of the warps, and of the block
     __shared__ float weights[kWarps][kRows];      // of the warps' parts in the block's
     __shared__ float lacks[kRows];                // what the rows' queries lack
-    __shared__ int64_t row_place[kRows];             // of the rows' results, in heads
+    __shared__ int64_t row_place[kRows];          // of the rows' results, in heads
 
     const AttentionArgs &a = w.a;
     const dspark_kv_cache &c = a.cache;
@@ -270,12 +282,12 @@ window_kernel(const __grid_constant__ WindowArgs w) {
             }
         if (!q.rows_ok || (q.n > 0 && !q.len_ok)) {     // no rows, or rows of NaN
             if (m0 == 0 && split == 0)
-                for (int i = threadIdx.x; i < q.n * group * (D / 8); i += kThreads) {
-                    const int m = i / (D / 8), blk = m / group;
+                for (int64_t i = threadIdx.x; i < (int64_t)q.n * group * (D / 8); i += kThreads) {
+                    const int m = (int)(i / (D / 8)), blk = m / group;
                     const int64_t place = (q.first + blk) * a.n_q_heads + head * group + (m - blk * group);
-                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + place * D)[i - m * (D / 8)] =
+                    reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + place * D)[i - (int64_t)m * (D / 8)] =
                         make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    if (i == m * (D / 8) && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
+                    if (i == (int64_t)m * (D / 8) && a.lse) a.lse[place] = __int_as_float(0x7fffffff);
                 }
             return;
         }
