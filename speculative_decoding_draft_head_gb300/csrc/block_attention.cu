@@ -1135,6 +1135,15 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     sees = a.mask == DSPARK_MASK_CAUSAL ? ctx + min(blk, p.n - 1) + 1 : p.len;
                 }
             }
+            // of the warp's rows: tokens in [all_low, all_end) all of them see, tokens below none_low (but first ones) or
+            // from none_end on none
+            int all_low = 0, all_end = 0, none_low = 0, none_end = 0;
+            if constexpr (kWindow) {
+                all_low = __reduce_max_sync(0xffffffffu, live ? low : 0);
+                none_low = __reduce_min_sync(0xffffffffu, live ? low : 0x7fffffff);
+                all_end = __reduce_min_sync(0xffffffffu, live ? sees : 0x7fffffff);
+                none_end = a.row_mask ? p.len : __reduce_max_sync(0xffffffffu, live ? sees : 0);
+            }
             float r = -INFINITY, l = 0.f, lack = 1.f;
             bool rescale_q = false;
 #pragma unroll 1
@@ -1149,10 +1158,7 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                 if (warp_live) {
                     const uint32_t ss = n % kScaleSlots;
                     const float *ks = reinterpret_cast<const float *>(gen + L::kScale) + (w * kScaleSlots + ss) * 256, *vs = ks + 128;
-                    // some row does not see some token of this tile
-                    bool masked = token > ctx - plan::kTile;
-                    if constexpr (kWindow)
-                        masked = masked || __any_sync(0xffffffffu, live && low > token && sinks - plan::kTile < token);
+                    const bool masked = token > ctx - plan::kTile;   // some row does not see some token of this tile
                     float ref = r == -INFINITY ? 0.f : r;
                     __syncwarp();
                     // the row's scores 32 columns at a time: more would spill, and with this much shared
@@ -1161,7 +1167,19 @@ attention_kernel(const __grid_constant__ AttentionArgs a, const Partials parts) 
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pr[16], bits = ~0u;
                         bool some_hidden = false;
-                        if (masked) {
+                        // (through a window: whether all of the warp's rows see all of these columns, or none any)
+                        bool look = masked;
+                        if constexpr (kWindow) {
+                            const int t = token + 32 * q;
+                            look = !(t + 32 <= all_end && (t >= all_low || t + 32 <= sinks));
+                            if (t >= none_end || (t + 32 <= none_low && t >= sinks)) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) pr[i] = 0;
+                                tmem_st16(my_s + 16u * (uint32_t)q, pr);
+                                continue;
+                            }
+                        }
+                        if (look) {
                             const int from_t = token + 32 * q, full = min(max(sees - from_t, 0), 32);
                             bits = full == 32 ? ~0u : (1u << full) - 1;
                             if constexpr (kWindow) {
