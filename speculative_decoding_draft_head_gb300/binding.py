@@ -758,7 +758,11 @@ def window_attention(q, cache, block_table, kv_len, row0, *, window, sinks=0, pr
     dspark_window_attention.
 
     Returns dict(out, lse): out like q, lse [n_rows, n_q_heads] fp32."""
-    return _attention((int(window), int(sinks)), q, cache, block_table, kv_len, row0, prefix_pages, prefix_len, mask,
+    window, sinks = int(window), int(sinks)
+    if window > 0x7fffffff or sinks > 0x7fffffff or window < 0 or sinks < 0:
+        # (more than any cache holds is all of it; what is below 0 the library refuses)
+        window, sinks = (max(-1, min(x, 0x7fffffff)) for x in (window, sinks))
+    return _attention((window, sinks), q, cache, block_table, kv_len, row0, prefix_pages, prefix_len, mask,
                       row_mask, scale, out, workspace, stream)
 
 
@@ -777,9 +781,6 @@ def _attention(window, q, cache, block_table, kv_len, row0, prefix_pages, prefix
     qs = _row_stride(q, "q", Hq, cache)
     pages_p = None if prefix_pages is None else _vec(prefix_pages, "prefix_pages", torch.int32, n_pages, cache)
     words_p = None if row_mask is None else _vec(row_mask, "row_mask", torch.int64, n, cache)
-    if window is not None:
-        # (more than any cache holds is all of it)
-        window = tuple(max(-1, min(x, 0x7fffffff)) for x in window)
     if out is None:
         with _on(stream):
             out = dict(out=torch.empty((n, Hq, D), dtype=q.dtype, device=dev),
@@ -791,23 +792,29 @@ def _attention(window, q, cache, block_table, kv_len, row0, prefix_pages, prefix
         if out.get("lse") is not None:
             _need(out["lse"], "lse", dtype=torch.float32, shape=(n, Hq), device=dev)
             lse_p = out["lse"].data_ptr()
-    need = 1
-    if workspace is None:
-        need = (attention_workspace_bytes if window is None else window_workspace_bytes)(B, n, Hq, cache.n_kv_heads, D)
+    scale = D ** -0.5 if scale is None else float(scale)
+    if window is not None and workspace is None and not window_workspace_bytes(B, n, Hq, cache.n_kv_heads, D):
+        _check(lib.dspark_window_attention(
+            cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p, n_pages,
+            prefix_len, window[0], window[1], _MASKS[mask], words_p, scale, out["out"].data_ptr(), lse_p, None, 0, raw))
+        return out
     # (two launches that meet in the workspace: another thread's must not come in between)
-    with _default_ws.lock if workspace is None and (need or window is None) else _AS_IT_IS:
-        if workspace is not None:
+    with _default_ws.lock if workspace is None else _AS_IT_IS:
+        if workspace is None:
+            size = attention_workspace_bytes if window is None else window_workspace_bytes
+            ws_p, ws_n, workspace = _default_ws.attention(size(B, n, Hq, cache.n_kv_heads, D), dev, stream, raw)
+        else:
             _need(workspace, "workspace", device=dev)
             ws_p, ws_n = workspace.data_ptr(), workspace.numel()
-        elif need or window is None:
-            ws_p, ws_n, workspace = _default_ws.attention(need, dev, stream, raw)
+        if window is None:
+            status = lib.dspark_block_attention(
+                cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p,
+                n_pages, prefix_len, _MASKS[mask], words_p, scale, out["out"].data_ptr(), lse_p, ws_p, ws_n, raw)
         else:
-            ws_p, ws_n = None, 0
-        head = (cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p,
-                n_pages, prefix_len)
-        tail = (_MASKS[mask], words_p, D ** -0.5 if scale is None else float(scale), out["out"].data_ptr(), lse_p, ws_p, ws_n,
-                raw)
-        status = lib.dspark_block_attention(*head, *tail) if window is None else lib.dspark_window_attention(*head, *window, *tail)
+            status = lib.dspark_window_attention(
+                cache._ref, q.data_ptr(), qs, _ROW_DTYPES[q.dtype], Hq, row0_p, n, B, table_p, max_pages, len_p, pages_p,
+                n_pages, prefix_len, window[0], window[1], _MASKS[mask], words_p, scale, out["out"].data_ptr(), lse_p, ws_p,
+                ws_n, raw)
     _check(status)
     return out
 
