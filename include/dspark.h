@@ -591,7 +591,8 @@ DSPARK_API size_t dspark_window_workspace_bytes(int B, int n_rows, int n_q_heads
  * away as soon as the window has passed it.
  *
  * Everything else, scales, results, roundings, flags and limits, as
- * dspark_block_attention; window >= 1, sinks >= 0, and prefix_len +
+ * dspark_block_attention (with fp16 results of blocks that have few rows, the
+ * softmax terms count to 2^-22); window >= 1, sinks >= 0, and prefix_len +
  * max_pages * page_size at most 2^31 - 256.
  */
 DSPARK_API dspark_status dspark_window_attention(

@@ -8,7 +8,9 @@
 //   O = sum_j 2^(s_j - r) v_j,   l = sum_j 2^(s_j - r),   out = O / l,
 //   lse = ln 2 (r + log2 l).
 // q after a power of two per row and the codes are exact in fp16, scales and
-// all sums are fp32, and P = 2^(s_j - r) (2^12 vs_j) is rounded once to fp16 (2^-11).
+// all sums are fp32, and P = 2^(s_j - r) (2^12 vs_j) is rounded once to fp16 (2^-11);
+// for fp16 results, whose own rounding is no larger, its rest is rounded to a second
+// fp16 and multiplied too, so that P counts to 2^-22.
 // The reference is an integer that moves only when a P passes fp16's range.
 //
 // A row sees at most window + sinks tokens, so that an item (a request's kv head
@@ -240,6 +242,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
     using Sl = Slot<DP>;
     constexpr int kStages = Shape<DP, N>::kStages, kRows = 8 * N, kHalves = DP / 64;
     constexpr int kCols = DP / 8;                 // dimensions of a lane's rows
+    constexpr int kParts = std::is_same_v<T, __half> ? 2 : 1;   // fp16 parts of P
     constexpr int kPieces = DP / 16, kPer = 32 / kPieces;   // pieces of a token; tokens a copy takes at once
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ View views[kWarps];
@@ -545,7 +548,7 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 }
                 // softmax terms and what they weigh the values' codes with; whether one of these, or a sum, passes its
                 // bound
-                uint32_t pk[M][2];
+                uint32_t pk[M][kParts][2];
                 float sum[M][2];
 #pragma unroll 1
                 for (bool again = false;; again = true) {
@@ -556,10 +559,17 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                         float p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(x[n][e], lack[n][e & 1], -ref[n][e & 1]));
-                        pk[n][0] = half_pair(p[0] * vs[0], p[1] * vs[0]);
-                        pk[n][1] = half_pair(p[2] * vs[1], p[3] * vs[1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x0 = p[2 * e] * vs[e], x1 = p[2 * e + 1] * vs[e];
+                            pk[n][0][e] = half_pair(x0, x1);
+                            if constexpr (kParts == 2) {
+                                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&pk[n][0][e]));
+                                pk[n][1][e] = half_pair(x0 - h.x, x1 - h.y);
+                            }
+                        }
                         static_assert(kPast + 0x0400u == 0x8000u, "");
-                        past |= __vmaxu2(pk[n][0], pk[n][1]) + 0x04000400u;       // kPast and more: a half's top bit
+                        past |= __vmaxu2(pk[n][0][0], pk[n][0][1]) + 0x04000400u;       // kPast and more: a half's top bit
                         sum[n][0] = p[0] + p[2];
                         sum[n][1] = p[1] + p[3];
                         most = max3(most, sum[n][0], sum[n][1]);
@@ -587,8 +597,11 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                 for (int n = 0; n < M; ++n) {
                     l[n][0] += sum[n][0];
                     l[n][1] += sum[n][1];
-                    pk[n][0] = transpose8x8(pk[n][0]);
-                    pk[n][1] = transpose8x8(pk[n][1]);
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i) {
+                        pk[n][i][0] = transpose8x8(pk[n][i][0]);
+                        pk[n][i][1] = transpose8x8(pk[n][i][1]);
+                    }
                 }
                 // outputs
                 uint32_t vw[4][DP / 32];
@@ -610,7 +623,10 @@ window_kernel(const __grid_constant__ WindowArgs w) {
                     decode4<kFormat>(__byte_perm(vw[0][k >> 1], vw[1][k >> 1], pick), a0, a1);
                     decode4<kFormat>(__byte_perm(vw[2][k >> 1], vw[3][k >> 1], pick), a2, a3);
 #pragma unroll
-                    for (int n = 0; n < M; ++n) mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][0], pk[n][1]);
+                    for (int n = 0; n < M; ++n)
+#pragma unroll
+                        for (int i = 0; i < kParts; ++i)
+                            mma16816(o[n][k], as_u32(a0), as_u32(a1), as_u32(a2), as_u32(a3), pk[n][i][0], pk[n][i][1]);
                 }
                 s = s + 1 == kStages ? 0 : s + 1;
             }

@@ -317,3 +317,12 @@ def test_few_rows_over_long_windows(rows, ctx, prefix, Hq, Hkv, D, page, window,
     """An item's tokens are split over a cluster's blocks."""
     _run(rows, ctx, prefix, Hq, Hkv, D, page, window, sinks, fmt=fmt)
 
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("name", ["one token", "lengths around the window", "verify blocks", "window into the prefix",
+                                  "head of 96", "blocks of many row blocks"])
+def test_fp16_results_have_little_but_their_own_rounding(name, fmt):
+    """Of few rows the softmax terms count in two fp16 parts: 2^-22 in the place of 2^-11."""
+    got, q, pool, row0, lens = _run(*SHAPES[name], fmt=fmt, dtype=F16, check=False)
+    window, sinks = SHAPES[name][-2:]
+    _check(got, plain_window.attention(q, pool, row0, lens, window, sinks, terms=2.0 ** -22))
