@@ -494,7 +494,7 @@ typedef struct dspark_rotary {
  * sizes that are 1 need no stride.  out may be x with the same strides, else
  * the two must not overlap.  positions [n_axes][n_rows] int32, any sign.
  * fp32 inside, one rounding to dtype.
- * Limits: head_dim a multiple of 8 up to 256, n_heads at most 65536; either the heads
+ * Limits: head_dim a multiple of 8 up to 256, n_heads at most 65536, n_rows at most 2^30; either the heads
  * of a row or the rows of a head lie inside one stride of the other.
  */
 DSPARK_API dspark_status dspark_rotary_rows(
@@ -517,7 +517,7 @@ DSPARK_API dspark_status dspark_rotary_rows(
  * likewise, q itself with its stride or not overlapping q, k and v.  Rows that
  * belong to no request are neither read from nor written to, in the cache or q_out;
  * queries of a row whose place is no good are turned all the same.
- * Limits: those of dspark_kv_append; at most 65536 heads.
+ * Limits: those of dspark_kv_append; at most 65536 heads and 2^30 rows.
  */
 DSPARK_API dspark_status dspark_kv_append_rotary(
     const dspark_kv_cache *cache, const dspark_rotary *rotary, const void *q, int64_t q_stride, int n_q_heads,

@@ -234,6 +234,7 @@ dspark_status dspark_rotary_rows(const dspark_rotary *rotary, const void *x, int
     if (dtype != DSPARK_BF16 && dtype != DSPARK_F32 && dtype != DSPARK_F16)
         return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     if (n_rows < 0 || n_heads < 1) return fail(DSPARK_ERR_INVALID_ARG, "bad n_rows %d or n_heads %d", n_rows, n_heads);
+    if (n_rows > kMaxRotaryRows) return fail(DSPARK_ERR_UNSUPPORTED, "n_rows must be at most 2^30 (got %d)", n_rows);
     if (n_heads > kMaxRotaryHeads) return fail(DSPARK_ERR_UNSUPPORTED, "n_heads must be at most %d", kMaxRotaryHeads);
     if (inverse != 0 && inverse != 1) return fail(DSPARK_ERR_INVALID_ARG, "inverse must be 0 or 1");
     if (n_rows == 0) return DSPARK_OK;
@@ -280,6 +281,7 @@ dspark_status dspark_kv_append_rotary(const dspark_kv_cache *cache, const dspark
         return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     if (positions && offset != 0) return fail(DSPARK_ERR_INVALID_ARG, "offset must be 0 when positions are given");
     if (!aligned(positions, 4)) return fail(DSPARK_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    if (n_rows > kMaxRotaryRows) return fail(DSPARK_ERR_UNSUPPORTED, "n_rows must be at most 2^30 (got %d)", n_rows);
     if (cache->n_kv_heads > kMaxRotaryHeads || (q && n_q_heads > kMaxRotaryHeads))
         return fail(DSPARK_ERR_UNSUPPORTED, "at most %d heads", kMaxRotaryHeads);
     if (n_rows == 0) return DSPARK_OK;

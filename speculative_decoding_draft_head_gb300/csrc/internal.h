@@ -265,6 +265,7 @@ cudaError_t launch_window_blocks(const AttentionArgs &a, cudaStream_t s);
 // ------------------------------------------------------- rotary positions --
 constexpr int kMaxRotaryDim = 256;
 constexpr int kMaxRotaryHeads = 1 << 16;
+constexpr int kMaxRotaryRows = 1 << 30;      // the kernels round up what they count in 31 bits
 struct RotaryRowsArgs {
     dspark_rotary z;
     const void *x;

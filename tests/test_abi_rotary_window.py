@@ -153,6 +153,13 @@ def test_append_rejects(over, status, needle):
     assert _append(**over) == status and needle in _err(), _err()
 
 
+@pytest.mark.parametrize("call", [_rows, _append])
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 31) - 1])
+def test_more_rows_than_the_kernels_count(call, n):
+    """Rounded up to what a block takes, numbers of rows near 2^31 would wrap."""
+    assert call(n=n) == 2 and "n_rows must be at most 2^30" in _err(), _err()
+
+
 @pytest.mark.parametrize("over,status,needle", [
     (dict(dt=1), 2, "bf16 or fp16"),
     (dict(Hq=3), 1, "multiple of n_kv_heads"),
